@@ -81,6 +81,8 @@ extern "C" {
  * 512 threads). */
 #define TW_MAX_H_BF16 16384
 #define TW_MAX_H_F32 8192
+/* Largest inner size of tw_gemm_q8. */
+#define TW_MAX_K_Q8 65536
 
 typedef enum { TW_BF16 = 0, TW_F32 = 1 } tw_dtype;
 
@@ -92,6 +94,12 @@ typedef enum {
     TW_ERR_CUDA = -4,
     TW_ERR_UNSUPPORTED = -5
 } tw_status;
+
+/* 8-bit types of the quantised entry points (tw_*_q8). */
+typedef enum {
+    TW_INT8 = 0, /* signed integers, quantised to [-127, 127] */
+    TW_E4M3 = 1  /* 8-bit floats: 4 exponent, 3 mantissa bits, at most 448 */
+} tw_qtype;
 
 /* Kernel choice for tw_fused_reduce_add_rmsnorm_ex. */
 typedef enum {
@@ -221,6 +229,58 @@ int tw_split_launch(const void* const* partials, int n_parts,
                     int n_out, void* residual_out, int64_t T, int64_t H,
                     float eps, int64_t t_split, int max_sms, void* s0, void* s1,
                     int dtype);
+
+/* 8-bit serving of the layer around the fused step: quantised activations
+ * and weights for the linear layers on either side of the norm (an addition
+ * of this library; the pages do not quantise).  A token's row v is held as
+ * 8-bit values q with one fp32 scale s:
+ *   s = max_h |v[h]| / top,  q[h] = round(v[h] / s),  v[h] ~ q[h] * s
+ * with top = 127 (TW_INT8) or 448 (TW_E4M3), rounded to nearest even.  The
+ * kernels multiply by top / max instead of dividing by s, so a quotient within
+ * an ulp or two of a rounding boundary may round to its neighbour.  A row
+ * whose largest magnitude is below 2^-117 is a zero row: s = 0, q = 0.  A row
+ * that holds a NaN or an infinity: s = NaN, q = 0 (it stands for NaN
+ * throughout).  8-bit tensors are [T, H] with row stride H bytes, 16-byte
+ * aligned; scales are fp32 [T], 4-byte aligned; only rows and scales of tokens
+ * [t0, t1) are written.  The other conventions are those at the top. */
+
+/* The fused step with 8-bit outputs: out[k][t,h] and out_scale[k][t] hold the
+ * quantised y[t,:] = x / rms * weight for every destination k (the fp32 row is
+ * quantised, not a rounded copy; the largest magnitude is taken of
+ * x * weight, so that a row whose product overflows fp32 counts as one that
+ * holds an infinity), residual_out[t,:] = x in dtype as
+ * ever.  out_scale is a HOST array of n_out DEVICE pointers.  Kernel chosen as
+ * by TW_PATH_AUTO.  qtype is a tw_qtype; the alias rule covers the scales. */
+int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,
+                                   const void* residual, const void* weight,
+                                   void* const* out, float* const* out_scale,
+                                   int n_out, void* residual_out, int64_t T,
+                                   int64_t H, float eps, int64_t t0, int64_t t1,
+                                   int max_sms, void* stream, int dtype,
+                                   int qtype);
+
+/* Rows [t0, t1) of x [T, H] (dtype) quantised into out and out_scale: the
+ * input of a linear layer that does not come from the norm (the attention's
+ * output, an activation).  H limits and alignment as for the fused step. */
+int tw_quantize_rows_q8(const void* x, void* out, float* out_scale, int64_t T,
+                        int64_t H, int64_t t0, int64_t t1, int max_sms,
+                        void* stream, int dtype, int qtype);
+
+/* A linear layer on 8-bit operands, one scale per token and per channel:
+ *   out[t,n] = x_scale[t] * w_scale[n] * sum_k x[t,k] * w[n,k]
+ * for t in [t0, t1), rounded once to dtype (TW_BF16 or TW_F32).  x [T, K] and
+ * w [N, K] are 8-bit of one qtype (int8 values may use all of [-128, 127]),
+ * out is [T, N]; all row-major and dense.  Products are exact, their sum is
+ * held in fp32: exact for int8 while every partial sum stays within 2^24 (any
+ * K <= 1024), otherwise off by a few 2^-24 of the largest partial sum.
+ * Rules: K a multiple of 16, 16 <= K <= TW_MAX_K_Q8, 1 <= N < 2^31, T < 2^31;
+ * x, w and out 16-byte aligned, the scales 4-byte aligned; any T and N.
+ * Written to partials[r] of the fused step, out is a row-parallel layer's
+ * partial. */
+int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
+               const float* w_scale, void* out, int64_t T, int64_t N, int64_t K,
+               int64_t t0, int64_t t1, int max_sms, void* stream, int dtype,
+               int qtype);
 
 /* The fused step for tensors in page-locked HOST memory (cudaHostAlloc or
  * cudaHostRegister): partials, residual, weight, out and residual_out are host

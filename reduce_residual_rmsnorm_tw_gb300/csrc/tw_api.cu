@@ -68,8 +68,8 @@ struct DeviceState {
     // Clusters of 1, 2, 4, 8 CTAs that run at once, per kernel instantiation:
     // [0] with every CTA alone on its SM (budgeted launches), [1] with CTAs
     // free to share SMs; then [log2 cluster][dtype][vectors per thread 1, 2,
-    // 4][partials held 2, 4, 8, 16].
-    int max_clusters[2][4][2][3][4] = {};
+    // 4][partials held 2, 4, 8, 16][8-bit outputs].
+    int max_clusters[2][4][2][3][4][2] = {};
     unsigned int* status = nullptr;
     cudaEvent_t fork = nullptr;
     cudaEvent_t join = nullptr;
@@ -120,6 +120,9 @@ int device_state(DeviceState** out) {
         // its first launch, which may wait for running kernels).
         if ((e = static_cast<cudaError_t>(signal_prepare())) != cudaSuccess)
             return cuda_fail(e, "cudaFuncGetAttributes");
+        if ((e = static_cast<cudaError_t>(gemm_prepare(d.smem_optin))) != cudaSuccess ||
+            (e = static_cast<cudaError_t>(quantize_prepare(d.smem_optin))) != cudaSuccess)
+            return cuda_fail(e, "cudaFuncSetAttribute");
         // The cluster kernel is optional: if it cannot be configured, that
         // path reports TW_ERR_UNSUPPORTED and the others still run.
         e = static_cast<cudaError_t>(cluster_set_attributes(d.smem_optin));
@@ -132,16 +135,18 @@ int device_state(DeviceState** out) {
             for (int i = 0; d.cluster_ready && i < 4; ++i)
                 for (int dt = 0; dt < 2; ++dt)
                     for (int v = 0; v < 3; ++v)
-                        for (int q = 0; q < 4; ++q) {
-                            int n = 0;
-                            if (cluster_max_active(1 << i, shared ? 0 : kExclusiveSmemBytes, dt,
-                                                   1 << v, 2 << q, &n) != cudaSuccess ||
-                                n < 1) {
-                                (void)cudaGetLastError();
-                                n = static_cast<int>(kClusterPathMaxTokens);
+                        for (int q = 0; q < 4; ++q)
+                            for (int q8 = 0; q8 < 2; ++q8) {
+                                int n = 0;
+                                if (cluster_max_active(1 << i, shared ? 0 : kExclusiveSmemBytes,
+                                                       dt, 1 << v, 2 << q, q8 != 0, &n) !=
+                                        cudaSuccess ||
+                                    n < 1) {
+                                    (void)cudaGetLastError();
+                                    n = static_cast<int>(kClusterPathMaxTokens);
+                                }
+                                d.max_clusters[shared][i][dt][v][q][q8] = n;
                             }
-                            d.max_clusters[shared][i][dt][v][q] = n;
-                        }
         if ((e = cudaGetSymbolAddress(reinterpret_cast<void**>(&d.status), g_status_word)) !=
             cudaSuccess)
             return cuda_fail(e, "cudaGetSymbolAddress");
@@ -178,6 +183,9 @@ struct Args {
     const unsigned int* ready = nullptr;  // readiness flags (rows kernel only)
     int64_t block_tokens = 0;
     unsigned int epoch = 0;
+    int q8 = 0;  // 8-bit outputs of type qtype, with out_scale[k][t] per token
+    int qtype = 0;
+    float* const* out_scale = nullptr;
 };
 
 size_t elem_size(int dtype) { return dtype == TW_BF16 ? 2 : 4; }
@@ -242,24 +250,48 @@ int check_args(const Args& a) {
                             "start on a 16-byte boundary", r, (long long)a.H, a.n_parts);
     }
 
-    // Aliasing: outputs against inputs and against each other.
+    if (a.q8) {
+        if (a.qtype != TW_INT8 && a.qtype != TW_E4M3)
+            return fail(TW_ERR_INVALID_ARG, "qtype %d is not TW_INT8 or TW_E4M3", a.qtype);
+        if (!a.out_scale) return fail(TW_ERR_INVALID_ARG, "out_scale is NULL");
+        for (int k = 0; k < a.n_out; ++k) {
+            if (!a.out_scale[k]) return fail(TW_ERR_INVALID_ARG, "out_scale[%d] is NULL", k);
+            if ((reinterpret_cast<uintptr_t>(a.out_scale[k]) & 3u) != 0)
+                return fail(TW_ERR_ALIGNMENT, "out_scale[%d] is not 4-byte aligned", k);
+        }
+    }
+
+    // Aliasing: outputs (the destinations, residual_out, then the scales of
+    // 8-bit destinations) against inputs and against each other.
     const size_t tb = static_cast<size_t>(a.T) * static_cast<size_t>(a.H) * es;
     const size_t wb = static_cast<size_t>(a.H) * es;
-    const int n_outputs = a.n_out + 1;
+    const void* outs[2 * TW_MAX_OUTS + 1];
+    size_t out_bytes[2 * TW_MAX_OUTS + 1];
+    int n_outputs = 0;
+    for (int k = 0; k < a.n_out; ++k) {
+        outs[n_outputs] = a.out[k];
+        out_bytes[n_outputs++] = a.q8 ? tb / es : tb;
+    }
+    outs[n_outputs] = a.residual_out;
+    out_bytes[n_outputs++] = tb;
+    for (int k = 0; a.q8 && k < a.n_out; ++k) {
+        outs[n_outputs] = a.out_scale[k];
+        out_bytes[n_outputs++] = static_cast<size_t>(a.T) * sizeof(float);
+    }
     for (int i = 0; i < n_outputs; ++i) {
-        const void* o = i < a.n_out ? a.out[i] : a.residual_out;
+        const void* o = outs[i];
+        const size_t ob = out_bytes[i];
         const bool is_res_out = i == a.n_out;
         for (int r = 0; r < a.n_parts; ++r)
-            if (overlaps(o, tb, a.partials[r], tb))
+            if (overlaps(o, ob, a.partials[r], tb))
                 return fail(TW_ERR_ALIAS, "an output overlaps partials[%d]", r);
-        if (overlaps(o, tb, a.weight, wb)) return fail(TW_ERR_ALIAS, "an output overlaps weight");
-        if (overlaps(o, tb, a.residual, tb) && !(is_res_out && o == a.residual))
+        if (overlaps(o, ob, a.weight, wb)) return fail(TW_ERR_ALIAS, "an output overlaps weight");
+        if (overlaps(o, ob, a.residual, tb) && !(is_res_out && o == a.residual))
             return fail(TW_ERR_ALIAS, "an output overlaps residual (only residual_out == "
                         "residual, exactly, is allowed)");
-        for (int j = i + 1; j < n_outputs; ++j) {
-            const void* o2 = j < a.n_out ? a.out[j] : a.residual_out;
-            if (overlaps(o, tb, o2, tb)) return fail(TW_ERR_ALIAS, "two outputs overlap");
-        }
+        for (int j = i + 1; j < n_outputs; ++j)
+            if (overlaps(o, ob, outs[j], out_bytes[j]))
+                return fail(TW_ERR_ALIAS, "two outputs overlap");
     }
     return TW_OK;
 }
@@ -272,6 +304,9 @@ Params make_params(const Args& a, const DeviceState& d, int64_t t0, int64_t t1,
     p.residual = a.residual;
     p.weight = a.weight;
     p.residual_out = a.residual_out;
+    p.q8 = a.q8;
+    p.qtype = a.qtype;
+    for (int k = 0; a.q8 && k < a.n_out; ++k) p.out_scale[k] = a.out_scale[k];
     p.smid_log = smid_log;
     p.status = d.status;
     p.t0 = t0;
@@ -357,8 +392,8 @@ int launch_range(const Args& a, DeviceState& d, int64_t t0, int64_t t1, int path
         while ((2 << v) <= cluster_vectors_per_thread(p.row_bytes, cluster)) ++v;
         while ((4 << q) <= cluster_np(p.n_parts)) ++q;
         const int dt = a.dtype == TW_BF16 ? 0 : 1;
-        alone = d.max_clusters[0][log2c][dt][v][q];
-        shared = pdl ? d.max_clusters[1][log2c][dt][v][q] : 0;
+        alone = d.max_clusters[0][log2c][dt][v][q][a.q8];
+        shared = pdl ? d.max_clusters[1][log2c][dt][v][q][a.q8] : 0;
     }
     if (path == TW_PATH_AUTO) {
         const bool fits = pdl ? tokens <= (alone > shared ? alone : shared)
@@ -560,6 +595,16 @@ int fused_from_host(const Args& a, void* workspace, size_t workspace_bytes,
 
 int set_last_error(int code, const char* message) { return fail(code, "%s", message); }
 
+int device_info(DeviceInfo* out) {
+    DeviceState* d = nullptr;
+    const int rc = device_state(&d);
+    if (rc != TW_OK) return rc;
+    out->sm_count = d->sm_count;
+    out->smem_optin = d->smem_optin;
+    out->status = d->status;
+    return TW_OK;
+}
+
 int check_host_args(const void* const* partials, int n_parts, const void* residual,
                     const void* weight, void* const* out, int n_out, void* residual_out,
                     int64_t T, int64_t H, float eps, int64_t t0, int64_t t1, int max_sms,
@@ -614,6 +659,19 @@ int tw_fused_reduce_add_rmsnorm_flags(const void* const* partials, int n_parts,
     a.block_tokens = block_tokens;
     a.epoch = epoch;
     return tw::fused(a, TW_PATH_ROWS, nullptr, stream);
+}
+
+int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,
+                                   const void* residual, const void* weight, void* const* out,
+                                   float* const* out_scale, int n_out, void* residual_out,
+                                   int64_t T, int64_t H, float eps, int64_t t0, int64_t t1,
+                                   int max_sms, void* stream, int dtype, int qtype) {
+    Args a{partials, n_parts, residual, weight, out, n_out, residual_out,
+           T,        H,       eps,      t0,     t1,  max_sms, dtype};
+    a.q8 = 1;
+    a.qtype = qtype;
+    a.out_scale = out_scale;
+    return tw::fused(a, TW_PATH_AUTO, nullptr, stream);
 }
 
 int tw_fused_reduce_add_rmsnorm(const void* const* partials, int n_parts, const void* residual,

@@ -67,7 +67,12 @@ __device__ __forceinline__ void st_peer_f32(float* local, uint32_t rank, float v
 // that a launch with few partials keeps few registers and more CTAs fit on
 // an SM (N = 8 bf16 rows of 16 KB: 62 registers, 8 CTAs per SM, against 95
 // and 5 when every launch reserved room for 16).
-template <typename T, int VPT, int NP>
+//
+// Q8: out[k] is 8 bits wide with one scale per token.  Each CTA pushes the
+// maximum of |x * weight| over its columns beside its sum of squares, so the
+// exchange stays one cluster barrier (the rms factor cancels out of
+// q = rne(y * top / max|y|)).
+template <typename T, int VPT, int NP, bool Q8>
 __global__ void __launch_bounds__(kClusterThreads)
     cluster_kernel(const __grid_constant__ Params p) {
     using V = Vec<T>;
@@ -77,6 +82,9 @@ __global__ void __launch_bounds__(kClusterThreads)
     // cta_part[b][r]: CTA r's sum of squares of the token using buffer b,
     // written into every CTA of the cluster by CTA r itself.
     __shared__ float cta_part[2][kClusterMaxSize];
+    // The same two steps for the maxima of |x * weight| (8-bit outputs).
+    __shared__ float warp_max[Q8 ? kWarps : 1];
+    __shared__ float cta_max[Q8 ? 2 : 1][kClusterMaxSize];
 
     const int tid = threadIdx.x;
     const int warp = tid >> 5;
@@ -166,6 +174,13 @@ __global__ void __launch_bounds__(kClusterThreads)
         }
         ss = warp_sum(ss);
         if (lane == 0) warp_part[warp] = ss;
+        if constexpr (Q8) {
+            float m = 0.f;
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) m = max_abs_product<T>(m, x[k], wv[k]);
+            m = warp_max_abs(m);
+            if (lane == 0) warp_max[warp] = m;
+        }
         __syncthreads();
         if (!peers_started) {
             cluster_wait();
@@ -181,12 +196,25 @@ __global__ void __launch_bounds__(kClusterThreads)
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) s += warp_part[w];
             st_peer_f32(&cta_part[buf][crank], static_cast<uint32_t>(tid), s);
+            if constexpr (Q8) {
+                float m = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) m = max_abs(m, warp_max[w]);
+                st_peer_f32(&cta_max[buf][crank], static_cast<uint32_t>(tid), m);
+            }
         }
         cluster_sync();
         float total = 0.f;
         for (uint32_t r = 0; r < csize; ++r) total += cta_part[buf][r];
-        buf ^= 1;
         const float inv = rsqrtf(total * p.inv_H + p.eps);
+        [[maybe_unused]] RowQuant rq;
+        if constexpr (Q8) {
+            float m = 0.f;
+            for (uint32_t r = 0; r < csize; ++r) m = max_abs(m, cta_max[buf][r]);
+            rq = row_quant(m, inv, quant_top(p.qtype));
+            if (crank == 0 && tid < p.n_out) p.out_scale[tid][t] = rq.scale;
+        }
+        buf ^= 1;
 
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -196,11 +224,17 @@ __global__ void __launch_bounds__(kClusterThreads)
                 st_global_cs(static_cast<char*>(p.residual_out) + off, V::from_float(x[k]));
                 float w[E], y[E];
                 V::to_float(wv[k], w);
+                if constexpr (Q8) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) y[e] = (x[k][e] * inv) * w[e];
-                const uint4 packed = V::from_float(y);
-                for (int o = 0; o < p.n_out; ++o)
-                    st_global_cs(static_cast<char*>(p.out[o]) + off, packed);
+                    for (int e = 0; e < E; e += 2) mul2(y + e, x[k] + e, w + e);
+                    store_q8<E>(p.out, p.n_out, t * p.H + v * E, y, rq, p.qtype);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < E; ++e) y[e] = (x[k][e] * inv) * w[e];
+                    const uint4 packed = V::from_float(y);
+                    for (int o = 0; o < p.n_out; ++o)
+                        st_global_cs(static_cast<char*>(p.out[o]) + off, packed);
+                }
             }
         }
     }
@@ -210,30 +244,32 @@ __global__ void __launch_bounds__(kClusterThreads)
     if (!peers_started) cluster_wait();
 }
 
-template <typename T, int NP>
+template <typename T, int NP, bool Q8>
 void* cluster_entry_np(int vpt) {
     switch (vpt) {
-        case 1: return reinterpret_cast<void*>(&cluster_kernel<T, 1, NP>);
-        case 2: return reinterpret_cast<void*>(&cluster_kernel<T, 2, NP>);
-        case 4: return reinterpret_cast<void*>(&cluster_kernel<T, 4, NP>);
+        case 1: return reinterpret_cast<void*>(&cluster_kernel<T, 1, NP, Q8>);
+        case 2: return reinterpret_cast<void*>(&cluster_kernel<T, 2, NP, Q8>);
+        case 4: return reinterpret_cast<void*>(&cluster_kernel<T, 4, NP, Q8>);
         default: return nullptr;
     }
 }
 
-template <typename T>
+template <typename T, bool Q8>
 void* cluster_entry_for(int vpt, int np) {
     switch (np) {
-        case 2: return cluster_entry_np<T, 2>(vpt);
-        case 4: return cluster_entry_np<T, 4>(vpt);
-        case 8: return cluster_entry_np<T, 8>(vpt);
-        case 16: return cluster_entry_np<T, 16>(vpt);
+        case 2: return cluster_entry_np<T, 2, Q8>(vpt);
+        case 4: return cluster_entry_np<T, 4, Q8>(vpt);
+        case 8: return cluster_entry_np<T, 8, Q8>(vpt);
+        case 16: return cluster_entry_np<T, 16, Q8>(vpt);
         default: return nullptr;
     }
 }
 
-void* cluster_kernel_for(int dtype, int vpt, int np) {
-    return dtype == TW_BF16 ? cluster_entry_for<__nv_bfloat16>(vpt, np)
-                            : cluster_entry_for<float>(vpt, np);
+void* cluster_kernel_for(int dtype, int vpt, int np, bool q8) {
+    if (dtype == TW_BF16)
+        return q8 ? cluster_entry_for<__nv_bfloat16, true>(vpt, np)
+                  : cluster_entry_for<__nv_bfloat16, false>(vpt, np);
+    return q8 ? cluster_entry_for<float, true>(vpt, np) : cluster_entry_for<float, false>(vpt, np);
 }
 
 }  // namespace
@@ -261,18 +297,20 @@ int cluster_set_attributes(int smem_optin) {
     if (smem_optin < kExclusiveSmemBytes + 1024) return static_cast<int>(cudaErrorInvalidValue);
     for (int dt = 0; dt < 2; ++dt)
         for (int v = 1; v <= kClusterMaxVpt; v *= 2)
-            for (int np = 2; np <= 16; np *= 2) {
-                cudaError_t e = cudaFuncSetAttribute(cluster_kernel_for(dt, v, np),
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     kExclusiveSmemBytes);
-                if (e != cudaSuccess) return static_cast<int>(e);
-            }
+            for (int np = 2; np <= 16; np *= 2)
+                for (bool q8 : {false, true}) {
+                    cudaError_t e = cudaFuncSetAttribute(
+                        cluster_kernel_for(dt, v, np, q8),
+                        cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
+                    if (e != cudaSuccess) return static_cast<int>(e);
+                }
     return 0;
 }
 
-int cluster_max_active(int cluster, size_t smem_bytes, int dtype, int vpt, int np, int* n) {
-    // The instantiations differ in registers (by vectors per thread and
-    // partials held), so each is asked about separately.
+int cluster_max_active(int cluster, size_t smem_bytes, int dtype, int vpt, int np, bool q8,
+                       int* n) {
+    // The instantiations differ in registers (by vectors per thread,
+    // partials held and output width), so each is asked about separately.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
     cfg.blockDim = dim3(kClusterThreads);
@@ -285,13 +323,13 @@ int cluster_max_active(int cluster, size_t smem_bytes, int dtype, int vpt, int n
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return static_cast<int>(
-        cudaOccupancyMaxActiveClusters(n, cluster_kernel_for(dtype, vpt, np), &cfg));
+        cudaOccupancyMaxActiveClusters(n, cluster_kernel_for(dtype, vpt, np, q8), &cfg));
 }
 
 int launch_cluster(const Params& p, int dtype, int cluster, int n_clusters, size_t smem_bytes,
                    bool pdl, void* stream) {
     const int vpt = cluster_vectors_per_thread(p.row_bytes, cluster);
-    void* fn = cluster_kernel_for(dtype, vpt, cluster_np(p.n_parts));
+    void* fn = cluster_kernel_for(dtype, vpt, cluster_np(p.n_parts), p.q8 != 0);
     if (!fn) return static_cast<int>(cudaErrorInvalidValue);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster * n_clusters));

@@ -249,6 +249,126 @@ __device__ __forceinline__ void sum_squares(float (&ss2)[2], const float (&x)[E]
             : "f"(x[e]), "f"(x[e + 1]));
 }
 
+// ------------------------------------------------------ 8-bit outputs ---
+// A row v quantised to 8 bits with one scale: scale = max|v| / top and
+// q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  The kernels multiply
+// by mul = top / max|v|, so that no element pays a division; a quotient that
+// lands within an ulp of a rounding boundary may then round to the neighbour.
+// Rows whose largest magnitude is below kQuantTiny (so small that top / max
+// would overflow or the scale lose bits as a subnormal) count as zero rows:
+// scale 0, values 0.  A row that holds a NaN or an infinity has no scale:
+// scale NaN, values 0.
+constexpr float kQuantTiny = 6.0185e-36f;  // 2^-117
+
+__device__ __forceinline__ float quant_top(int qtype) { return qtype == TW_INT8 ? 127.f : 448.f; }
+
+// max(m, |v|), NaN if either is.
+__device__ __forceinline__ float max_abs(float m, float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+    return r;
+}
+
+// Largest of the warp's non-negative floats (NaN if any is): the bits of
+// non-negative floats order as unsigned integers, NaN above infinity.
+__device__ __forceinline__ float warp_max_abs(float m) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
+
+struct RowQuant {
+    float mul;    // top / max|v|; 0 where every value is 0 by rule
+    float scale;  // gain * max|v| / top
+    bool zero;    // every value of the row is 0
+};
+
+// The scale of a row whose elements are gain * v, m = max|v| (NaN or infinite
+// where the row holds one).  The gain (a norm's 1 / rms) cancels out of q.
+__device__ __forceinline__ RowQuant row_quant(float m, float gain, float top) {
+    RowQuant r;
+    const bool finite = m <= 3.402823466e38f;  // false for NaN too
+    r.zero = !finite || m < kQuantTiny;
+    r.mul = r.zero ? 0.f : __fdiv_rn(top, m);
+    r.scale = !finite ? __uint_as_float(0x7fffffffu)
+                      : (m < kQuantTiny ? 0.f * gain : __fdiv_rn(m * gain, top));
+    return r;
+}
+
+// Four values times mul, rounded to nearest even, as four int8 (|v * mul| is
+// at most 127 and a few ulps).  Adding 1.5 * 2^23 leaves the rounded integer
+// in the low bits of the sum's mantissa, its low byte being the int8.
+__device__ __forceinline__ uint32_t pack_int8(const float* v, float mul) {
+    uint32_t b[4];
+    asm("{\n\t.reg .b64 a, s, c;\n\t"
+        "mov.b64 s, {%8, %8};\n\t"
+        "mov.b64 c, {%9, %9};\n\t"
+        "mov.b64 a, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, a, s, c;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t"
+        "mov.b64 a, {%6, %7};\n\t"
+        "fma.rn.f32x2 a, a, s, c;\n\t"
+        "mov.b64 {%2, %3}, a;\n\t}"
+        : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3])
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(mul), "f"(12582912.f));
+    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// Four values times mul as four e4m3 (nearest even, saturating at 448).
+__device__ __forceinline__ uint32_t pack_e4m3(const float* v, float mul) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+        "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+        "mov.b32 %0, {lo, hi};\n\t}"
+        : "=r"(r)
+        : "f"(v[0] * mul), "f"(v[1] * mul), "f"(v[2] * mul), "f"(v[3] * mul));
+    return r;
+}
+
+// The E elements (8 or 4) of one 16-byte vector's worth of a row, quantised
+// and stored at p (E bytes, E-byte aligned) in each of n destinations.
+template <int E>
+__device__ __forceinline__ void store_q8(void* const* out, int n, int64_t off, const float* v,
+                                         const RowQuant& q, int qtype) {
+    uint32_t b[E / 4];
+#pragma unroll
+    for (int i = 0; i < E / 4; ++i) {
+        b[i] = qtype == TW_INT8 ? pack_int8(v + 4 * i, q.mul) : pack_e4m3(v + 4 * i, q.mul);
+        if (q.zero) b[i] = 0;
+    }
+    for (int k = 0; k < n; ++k) {
+        char* p = static_cast<char*>(out[k]) + off;
+        if constexpr (E == 8)
+            __stcs(reinterpret_cast<uint2*>(p), make_uint2(b[0], b[1]));
+        else
+            __stcs(reinterpret_cast<unsigned int*>(p), b[0]);
+    }
+}
+
+// y[0..1] = a[0..1] * b[0..1], two lanes per instruction.
+__device__ __forceinline__ void mul2(float* y, const float* a, const float* b) {
+    asm("{\n\t.reg .b64 a, b;\n\t"
+        "mov.b64 a, {%2, %3};\n\t"
+        "mov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "=f"(y[0]), "=f"(y[1])
+        : "f"(a[0]), "f"(a[1]), "f"(b[0]), "f"(b[1]));
+}
+
+// max(m, |x * w|) over one vector's elements (NaN if any product is).
+template <typename T>
+__device__ __forceinline__ float max_abs_product(float m, const float* x, const uint4& wv) {
+    constexpr int E = Vec<T>::kElems;
+    float w[E], v[E];
+    Vec<T>::to_float(wv, w);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+        mul2(v + e, x + e, w + e);
+        m = max_abs(max_abs(m, v[e]), v[e + 1]);
+    }
+    return m;
+}
+
 // Streaming 16-byte global store (written once, not re-read by this kernel).
 __device__ __forceinline__ void st_global_cs(void* p, const uint4& v) {
     __stcs(reinterpret_cast<uint4*>(p), v);
@@ -278,7 +398,8 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // Host side: launch fn(p) with the given shape, optionally with programmatic
 // stream serialization (see grid_dependency_wait).  Returns a cudaError_t.
-inline int launch_with_pdl(void* fn, const Params& p, int grid, int block, size_t smem_bytes,
+template <typename P>
+inline int launch_with_pdl(void* fn, const P& p, int grid, int block, size_t smem_bytes,
                            bool pdl, void* stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
@@ -290,7 +411,7 @@ inline int launch_with_pdl(void* fn, const Params& p, int grid, int block, size_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 1 : 0;
-    void* args[] = {const_cast<Params*>(&p)};
+    void* args[] = {const_cast<P*>(&p)};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, fn, args));
 }
 

@@ -50,6 +50,7 @@ struct Params {
     const void* residual;
     const void* weight;
     void* residual_out;
+    float* out_scale[TW_MAX_OUTS];  // 8-bit outputs: one scale per token
     uint32_t* smid_log;     // optional, rows kernel only
     unsigned int* status;   // device status word (bounded-wait give-ups)
     // Rows kernel: this launch's work counter pair (next unit to claim, CTAs
@@ -74,10 +75,48 @@ struct Params {
     int stages;             // rows kernel: ring depth (a multiple of producers)
     int producers;          // rows kernel: producer warps issuing copies (1..kRowsMaxProducers)
     int colsplit;           // 1: column-split mode
+    int q8;                 // 1: out[k] holds 8-bit values of type qtype
+    int qtype;              // tw_qtype
     int prefetch;           // 1: warm L2 before the dependency wait (overlapped launches)
     float eps;
     float inv_H;
 };
+
+// What the entry points outside tw_api.cu need of the current device's state
+// (set up on first use; tw_status, with the error recorded).
+struct DeviceInfo {
+    int sm_count;
+    int smem_optin;
+    unsigned int* status;  // device status word
+};
+int device_info(DeviceInfo* out);
+
+// Row quantisation (tw_quant.cu).
+struct QuantParams {
+    const void* x;
+    void* out;
+    float* out_scale;
+    int64_t t0, t1;     // token range
+    int64_t H;
+    int64_t row_bytes;  // H * element size (multiple of 16)
+    int qtype;          // tw_qtype
+};
+// Launch on at most max_sms SMs (cudaError_t as int).
+int launch_quantize(const QuantParams& p, int dtype, int max_sms, int sm_count, void* stream);
+int quantize_prepare(int smem_optin);
+
+// 8-bit matrix product (tw_gemm.cu).
+struct GemmArgs {
+    const void* x;        // [M, K] 8-bit, rows of the token range
+    const float* x_scale; // [M]
+    const void* w;        // [N, K] 8-bit
+    const float* w_scale; // [N]
+    void* out;            // [M, N]
+    int64_t M, N, K;
+    int dtype, qtype;
+};
+int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
+int gemm_prepare(int smem_optin);
 
 // Record `message` as the calling thread's last error and return `code`.
 int set_last_error(int code, const char* message);
@@ -106,6 +145,9 @@ size_t rows_plan(Params& p, int smem_optin);
 // Whether the launch planned in p (fixed schedule, unit size and ring set)
 // runs as two pipelines per CTA (`budgeted`: held below the SM count).
 bool rows_two_pipes_fit(const Params& p, bool budgeted);
+// Instantiations with 8-bit outputs (nullptr: none).
+void* rows_q8_entry(int dtype, int nv, int unit, int mode);
+void* rows2_q8_entry(int dtype, int nv, int unit);
 // Raise the dynamic shared memory limit of every kernel instantiation on the
 // current device (cudaError_t as int).
 int rows_set_smem_limit(int smem_optin);
@@ -117,10 +159,11 @@ int signal_prepare();
 // Vectors per thread the cluster kernel needs (0: the row is too long).
 int cluster_vectors_per_thread(int64_t row_bytes, int cluster);
 // Clusters of `cluster` CTAs of the cluster kernel instantiation for dtype,
-// vpt vectors per thread and np partials held in registers (2, 4, 8 or 16),
-// each CTA with smem_bytes of dynamic shared memory, that the current device
+// vpt vectors per thread, np partials held in registers (2, 4, 8 or 16) and
+// 8-bit outputs or not, each CTA with smem_bytes of dynamic shared memory, that the current device
 // can run at once (cudaError_t as int).
-int cluster_max_active(int cluster, size_t smem_bytes, int dtype, int vpt, int np, int* n);
+int cluster_max_active(int cluster, size_t smem_bytes, int dtype, int vpt, int np, bool q8,
+                       int* n);
 // Partials the cluster kernel holds in registers for n_parts partials.
 int cluster_np(int n_parts);
 int launch_cluster(const Params& p, int dtype, int cluster, int n_clusters, size_t smem_bytes,

@@ -1,0 +1,133 @@
+// tw_quant.cu -- rows quantised to 8 bits with one scale per token.
+//
+// s_t = max_h |x[t,h]| / top, q[t,h] = rne(x[t,h] * top / max): a row must be
+// seen whole before its first value is written, and is read only once: its
+// 16-byte vectors stay in registers between the two.  A row belongs to W
+// warps (W * 32 threads holding VPT vectors each), so short rows share a CTA
+// and long ones spread over it; one shuffle-free warp maximum, and for W > 1
+// one exchange through shared memory.  Bound by HBM: row_bytes in, H + 4 out.
+#include "tw_device.cuh"
+
+namespace tw {
+namespace {
+
+constexpr int kQuantThreads = 256;
+
+template <typename T, int VPT, int W>
+__global__ void __launch_bounds__(kQuantThreads)
+    quantize_kernel(const __grid_constant__ QuantParams p) {
+    constexpr int E = Vec<T>::kElems;
+    constexpr int kRows = kQuantThreads / 32 / W;  // rows per CTA at a time
+    __shared__ float warp_max[2][kQuantThreads / 32];
+    const int warp = threadIdx.x / 32;
+    const int slot = warp / W;                      // row of the CTA
+    const int rtid = threadIdx.x - slot * W * 32;   // thread of the row
+    const int nvec = static_cast<int>(p.row_bytes / 16);
+    const float top = quant_top(p.qtype);
+    grid_dependency_wait();
+    grid_launch_dependents();
+    int buf = 0;
+    // The CTA's rows step together, so that every thread meets the barrier.
+    for (int64_t t_cta = p.t0 + static_cast<int64_t>(blockIdx.x) * kRows; t_cta < p.t1;
+         t_cta += static_cast<int64_t>(gridDim.x) * kRows) {
+        const int64_t t = t_cta + slot;
+        const bool live = t < p.t1;
+        const char* row = static_cast<const char*>(p.x) + t * p.row_bytes;
+        uint4 raw[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = rtid + k * W * 32;
+            raw[k] = live && v < nvec ? ld_global_nc(row + static_cast<int64_t>(v) * 16)
+                                      : make_uint4(0, 0, 0, 0);
+        }
+        float m = 0.f;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            float f[E];
+            Vec<T>::to_float(raw[k], f);
+#pragma unroll
+            for (int e = 0; e < E; ++e) m = max_abs(m, f[e]);
+        }
+        m = warp_max_abs(m);
+        if constexpr (W > 1) {
+            if ((threadIdx.x & 31) == 0) warp_max[buf][warp] = m;
+            __syncthreads();
+            m = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) m = max_abs(m, warp_max[buf][slot * W + w]);
+            buf ^= 1;
+        }
+        const RowQuant rq = row_quant(m, 1.f, top);
+        if (live && rtid == 0) p.out_scale[t] = rq.scale;
+        void* out[1] = {p.out};
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = rtid + k * W * 32;
+            if (live && v < nvec) {
+                float f[E];
+                Vec<T>::to_float(raw[k], f);
+                store_q8<E>(out, 1, t * p.H + static_cast<int64_t>(v) * E, f, rq, p.qtype);
+            }
+        }
+    }
+}
+
+template <typename T>
+void* quantize_entry(int vpt, int w) {
+    switch (w * 16 + vpt) {
+        case 1 * 16 + 1: return reinterpret_cast<void*>(&quantize_kernel<T, 1, 1>);
+        case 1 * 16 + 2: return reinterpret_cast<void*>(&quantize_kernel<T, 2, 1>);
+        case 2 * 16 + 2: return reinterpret_cast<void*>(&quantize_kernel<T, 2, 2>);
+        case 4 * 16 + 2: return reinterpret_cast<void*>(&quantize_kernel<T, 2, 4>);
+        case 8 * 16 + 2: return reinterpret_cast<void*>(&quantize_kernel<T, 2, 8>);
+        case 8 * 16 + 4: return reinterpret_cast<void*>(&quantize_kernel<T, 4, 8>);
+        case 8 * 16 + 8: return reinterpret_cast<void*>(&quantize_kernel<T, 8, 8>);
+        default: return nullptr;
+    }
+}
+
+void* quantize_kernel_for(int dtype, int vpt, int w) {
+    return dtype == TW_BF16 ? quantize_entry<__nv_bfloat16>(vpt, w) : quantize_entry<float>(vpt, w);
+}
+
+// Warps per row and vectors per thread for rows of nvec vectors: two vectors
+// per thread (32 bytes in flight) until a row takes the whole CTA, more from
+// there on.
+void quantize_shape(int64_t nvec, int* vpt, int* w) {
+    *w = 1;
+    *vpt = nvec <= 32 ? 1 : 2;
+    while (*w < 8 && nvec > static_cast<int64_t>(*w) * 32 * *vpt) *w *= 2;
+    while (nvec > static_cast<int64_t>(*w) * 32 * *vpt) *vpt *= 2;
+}
+
+}  // namespace
+
+int quantize_prepare(int smem_optin) {
+    for (int dt = 0; dt < 2; ++dt)
+        for (int w = 1; w <= 8; w *= 2)
+            for (int vpt = 1; vpt <= 8; vpt *= 2) {
+                void* fn = quantize_kernel_for(dt, vpt, w);
+                if (!fn) continue;
+                cudaError_t e = cudaFuncSetAttribute(
+                    fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
+                if (e != cudaSuccess) return static_cast<int>(e);
+            }
+    return smem_optin < kExclusiveSmemBytes + 1024 ? static_cast<int>(cudaErrorInvalidValue) : 0;
+}
+
+int launch_quantize(const QuantParams& p, int dtype, int max_sms, int sm_count, void* stream) {
+    int vpt = 0, w = 0;
+    quantize_shape(p.row_bytes / 16, &vpt, &w);
+    void* fn = quantize_kernel_for(dtype, vpt, w);
+    if (!fn) return static_cast<int>(cudaErrorInvalidValue);
+    const int64_t rows = kQuantThreads / 32 / w;
+    const int64_t ctas = (p.t1 - p.t0 + rows - 1) / rows;
+    // Under a budget each CTA is alone on its SM; without one, eight share it.
+    const bool whole = max_sms >= sm_count;
+    const int64_t most = whole ? int64_t{8} * sm_count : max_sms;
+    const int grid = static_cast<int>(ctas < most ? ctas : most);
+    return launch_with_pdl(fn, p, grid, kQuantThreads, whole ? 0 : kExclusiveSmemBytes, whole,
+                           stream);
+}
+
+}  // namespace tw

@@ -20,6 +20,8 @@ MAX_PARTS, MAX_OUTS = 16, 8
 STATUS_NAMES = {0: "TW_OK", -1: "TW_ERR_INVALID_ARG", -2: "TW_ERR_ALIGNMENT",
                 -3: "TW_ERR_ALIAS", -4: "TW_ERR_CUDA", -5: "TW_ERR_UNSUPPORTED"}
 _DTYPES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32}
+TW_INT8, TW_E4M3 = 0, 1
+_QTYPES = {torch.int8: TW_INT8, torch.float8_e4m3fn: TW_E4M3}
 _ALL_SMS = 1 << 30  # clamped to the device's SM count by the library
 
 
@@ -62,6 +64,16 @@ def load():
     lib.tw_fused_reduce_add_rmsnorm_flags.restype = ctypes.c_int
     lib.tw_set_ready.argtypes = [vp, i64, i64, ctypes.c_uint32, vp]
     lib.tw_set_ready.restype = ctypes.c_int
+    lib.tw_fused_reduce_add_rmsnorm_q8.argtypes = [
+        pp, ctypes.c_int, vp, vp, pp, pp, ctypes.c_int, vp, i64, i64, ctypes.c_float, i64, i64,
+        ctypes.c_int, vp, ctypes.c_int, ctypes.c_int]
+    lib.tw_fused_reduce_add_rmsnorm_q8.restype = ctypes.c_int
+    lib.tw_quantize_rows_q8.argtypes = [vp, vp, vp, i64, i64, i64, i64, ctypes.c_int, vp,
+                                        ctypes.c_int, ctypes.c_int]
+    lib.tw_quantize_rows_q8.restype = ctypes.c_int
+    lib.tw_gemm_q8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_int, vp,
+                               ctypes.c_int, ctypes.c_int]
+    lib.tw_gemm_q8.restype = ctypes.c_int
     lib.tw_split_launch.argtypes = [pp, ctypes.c_int, vp, vp, pp, ctypes.c_int,
                                     vp, i64, i64, ctypes.c_float, i64,
                                     ctypes.c_int, vp, vp, ctypes.c_int]
@@ -233,6 +245,106 @@ tw_fused_reduce_add_rmsnorm_bf16 = _typed("tw_fused_reduce_add_rmsnorm_bf16",
                                           torch.bfloat16)
 tw_fused_reduce_add_rmsnorm_f32 = _typed("tw_fused_reduce_add_rmsnorm_f32",
                                          torch.float32)
+
+
+def _on_current_device(*tensors):
+    dev = torch.cuda.current_device() if tensors[0].is_cuda else None
+    for t in tensors:
+        if not t.is_cuda or t.get_device() != dev:
+            raise ValueError("every tensor must be on the current CUDA device")
+
+
+def _quantised(q, name="out"):
+    """The tw_qtype of an 8-bit tensor."""
+    qt = _QTYPES.get(q.dtype)
+    if qt is None:
+        raise ValueError(f"{name}: dtype {q.dtype} not supported (int8 or float8_e4m3fn)")
+    return qt
+
+
+def _dense(name, t, shape, dtype):
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+
+
+def tw_fused_reduce_add_rmsnorm_q8(partials, residual, weight, out, out_scale,
+                                   residual_out, eps, t0=0, t1=None,
+                                   max_sms=None, stream=None):
+    """The fused step with 8-bit outputs: every tensor of ``out`` ([T, H], all
+    int8 or all float8_e4m3fn) and its ``out_scale`` ([T] float32) hold the
+    normalised rows as values times one scale per token."""
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, H]")
+    shape, dtype = residual.shape, residual.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype} not supported (bfloat16 or float32)")
+    T, H = shape
+    n, n_out = len(partials), len(out)
+    if not n or not n_out or len(out_scale) != n_out:
+        raise ValueError("need at least one partial, one destination and a scale tensor for "
+                         "each destination")
+    for p in partials:
+        _dense("partials", p, shape, dtype)
+    _dense("residual", residual, shape, dtype)
+    _dense("residual_out", residual_out, shape, dtype)
+    _dense("weight", weight, (H,), dtype)
+    qt = _quantised(out[0])
+    for q, s in zip(out, out_scale):
+        _dense("out", q, shape, out[0].dtype)
+        _dense("out_scale", s, (T,), torch.float32)
+    _on_current_device(residual, weight, residual_out, *partials, *out, *out_scale)
+    if T == 0:
+        return
+    ptrs = ctypes.c_void_p * n_out
+    _check(load().tw_fused_reduce_add_rmsnorm_q8(
+        (ctypes.c_void_p * n)(*[p.data_ptr() for p in partials]), n, residual.data_ptr(),
+        weight.data_ptr(), ptrs(*[q.data_ptr() for q in out]),
+        ptrs(*[s.data_ptr() for s in out_scale]), n_out, residual_out.data_ptr(), T, H, eps, t0,
+        T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
+        _stream_handle(stream), _DTYPES[dtype], qt))
+
+
+def tw_quantize_rows_q8(x, out, out_scale, t0=0, t1=None, max_sms=None, stream=None):
+    """Rows [t0, t1) of ``x`` ([T, H] bfloat16 or float32) quantised into
+    ``out`` ([T, H] int8 or float8_e4m3fn) and ``out_scale`` ([T] float32)."""
+    if x.dim() != 2 or x.dtype not in _DTYPES:
+        raise ValueError("x must be a [T, H] bfloat16 or float32 tensor")
+    T, H = x.shape
+    _dense("x", x, x.shape, x.dtype)
+    qt = _quantised(out)
+    _dense("out", out, x.shape, out.dtype)
+    _dense("out_scale", out_scale, (T,), torch.float32)
+    _on_current_device(x, out, out_scale)
+    if T == 0:
+        return
+    _check(load().tw_quantize_rows_q8(
+        x.data_ptr(), out.data_ptr(), out_scale.data_ptr(), T, H, t0, T if t1 is None else t1,
+        _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[x.dtype], qt))
+
+
+def tw_gemm_q8(x, x_scale, w, w_scale, out, t0=0, t1=None, max_sms=None, stream=None):
+    """out[t, n] = x_scale[t] * w_scale[n] * sum_k x[t, k] * w[n, k] on rows
+    [t0, t1): ``x`` [T, K] and ``w`` [N, K] both int8 or both float8_e4m3fn,
+    the scales float32, ``out`` [T, N] bfloat16 or float32."""
+    if x.dim() != 2 or w.dim() != 2 or x.shape[1] != w.shape[1]:
+        raise ValueError("x must be [T, K] and w [N, K]")
+    T, K = x.shape
+    N = w.shape[0]
+    qt = _quantised(x, "x")
+    if out.dtype not in _DTYPES:
+        raise ValueError(f"dtype {out.dtype} not supported (bfloat16 or float32)")
+    _dense("x", x, (T, K), x.dtype)
+    _dense("w", w, (N, K), x.dtype)
+    _dense("x_scale", x_scale, (T,), torch.float32)
+    _dense("w_scale", w_scale, (N,), torch.float32)
+    _dense("out", out, (T, N), out.dtype)
+    _on_current_device(x, x_scale, w, w_scale, out)
+    if T == 0 or N == 0:
+        return
+    _check(load().tw_gemm_q8(
+        x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), T, N,
+        K, t0, T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
+        _stream_handle(stream), _DTYPES[out.dtype], qt))
 
 
 def tw_split_launch(partials, residual, weight, out, residual_out, eps,
