@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libtw.so")
 SOURCES = ["tw_api.cu", "tw_rows.cu", "tw_warp.cu", "tw_cluster.cu", "tw_host.cu",
            "tw_noalloc.cu", "tw_signal.cu", "tw_rows_q8.cu", "tw_q8.cu", "tw_quant.cu",
            "tw_gemm.cu"]
-HEADERS = ["tw_device.cuh", "tw_rows.cuh", "tw_internal.h", "tw_host.h"]
+HEADERS = ["tw_device.cuh", "tw_tcgen05.cuh", "tw_rows.cuh", "tw_internal.h", "tw_host.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

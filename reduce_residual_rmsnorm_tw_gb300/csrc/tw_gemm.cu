@@ -1,81 +1,553 @@
 // tw_gemm.cu -- matrix product of 8-bit operands with scales per token and
 // channel: out[t,n] = xs[t] ws[n] sum_k x[t,k] w[n,k].
 //
-// Plain tiles: a CTA computes 64 tokens x 64 channels, each thread 4 x 4 of
-// them, from 32-deep slices of both operands widened to fp32 in shared memory.
-#include <cuda_fp8.h>
+// The channels are the tensor cores' M side (128 rows of W per CTA), the
+// tokens their N side (a tile of BN, sized to the call), so that a few tokens
+// cost a narrow MMA and the weights stream through once.  A unit of CG CTAs
+// (1, or a pair sharing each token tile: CG = 2) walks the tiles persistently;
+// its accumulators are double-buffered in TMEM, so that a tile's epilogue
+// runs beside the next tile's products.
+//
+//   e4m3  both operands go from TMA's 128-byte-swizzled boxes straight into
+//         tcgen05.mma.kind::f8f6f4.
+//   int8  sm_103a has no integer tcgen05.  Integers to 2^11 are exact in f16
+//         and the products accumulate in fp32, so the operands are widened to
+//         f16 on the way: W into TMEM (the MMA's A operand may live there, and
+//         shared memory, which bounds this kernel, sees W once in 8 bits
+//         instead of three times), x into a second ring in shared memory.
+//         f16 rather than bf16, whose 8 bits of mantissa hold -128..127 as
+//         well, because one byte permute and one packed subtract make an
+//         f16: 0x6400 | (v + 128) is 1024 + 128 + v.
+//
+// With few tokens there are fewer tiles than SMs: a cluster of S CTAs then
+// splits K, and each adds up its share of the token columns from all S
+// accumulators, pushed into its shared memory by the others (in rank order:
+// the same bits every time).
+#include <cuda.h>
 
-#include "tw_device.cuh"
+#include <mutex>
+
+#include "tw_tcgen05.cuh"
 
 namespace tw {
 namespace {
 
-constexpr int kTile = 64, kDeep = 32;
+constexpr int kBlockK = 128;     // bytes (= 8-bit elements) of K per ring stage
+constexpr int kUnitK = 64;       // int8: K elements per widened slot
+constexpr int kRows = 128;       // channels per CTA
+constexpr int kSlots = 4;        // int8: widened slots (TMEM and shared memory)
+constexpr int kSlotColumns = kUnitK / 2;
+constexpr int kMaxStages = 8;
+constexpr int kTmemColumns = 512;
+constexpr int kMaxSplit = 8;
 
-__device__ __forceinline__ float widen(uint8_t b, int qtype) {
-    if (qtype == TW_INT8) return static_cast<float>(static_cast<int8_t>(b));
-    __nv_fp8_e4m3 v;
-    v.__x = b;
-    return static_cast<float>(v);
+// Warp roles: 0 TMA, 1 MMA, 4-7 epilogue, 8-11 and 12-15 widen (int8).
+constexpr int kEpilogueWarp = 4, kWidenWarp = 8;
+
+// Largest token tile: one unit's two accumulators (and, for int8, the widened
+// W) share 512 TMEM columns; a single CTA takes short tiles only.
+__host__ __device__ constexpr int max_tokens(int cg, bool int8) { return cg == 1 ? 64 : (int8 ? 192 : 256); }
+// Bytes of the ring, per CTA.
+__host__ __device__ constexpr int x_bytes(int cg, bool int8) { return max_tokens(cg, int8) / cg * kBlockK; }
+__host__ __device__ constexpr int stage_bytes(int cg, bool int8) { return kRows * kBlockK + x_bytes(cg, int8); }
+__host__ __device__ constexpr int slot_bytes(int cg, bool int8) {
+    return int8 ? max_tokens(cg, int8) / cg * kUnitK * 2 : 0;
+}
+__host__ __device__ constexpr int stages(int cg, bool int8) { return cg == 1 && !int8 ? 7 : 6; }
+// Split K: the accumulators of every CTA of the cluster for this CTA's columns.
+__host__ __device__ constexpr int join_bytes(int cg, bool int8) {
+    return cg == 1 ? max_tokens(cg, int8) * kRows * 4 : 0;
 }
 
-__global__ void __launch_bounds__(256) gemm_kernel(const __grid_constant__ GemmArgs g) {
-    __shared__ float xs[kDeep][kTile + 1], ws[kDeep][kTile + 1];
+struct Header {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t wide_full[kSlots], wide_empty[kSlots];
+    uint64_t acc_full[2], acc_empty[2];
+    uint64_t joined, drained;
+    uint32_t tmem;
+    int abort;
+    float x_scale[4][256];  // each epilogue warp's copy of its tile's
+};
+constexpr int kHeaderBytes = 5120;
+static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
+
+__host__ __device__ constexpr int smem_bytes(int cg, bool int8) {
+    return 1024 + kHeaderBytes + stages(cg, int8) * stage_bytes(cg, int8) +
+           kSlots * slot_bytes(cg, int8) + join_bytes(cg, int8);
+}
+static_assert(smem_bytes(1, true) <= 232448 && smem_bytes(1, false) <= 232448 &&
+                  smem_bytes(2, true) <= 232448 && smem_bytes(2, false) <= 232448,
+              "over the shared memory of an SM");
+
+struct GemmParams {
+    const float* x_scale;
+    const float* w_scale;
+    void* out;
+    unsigned int* status;
+    int64_t N;
+    int M;
+    int k_blocks;      // ring stages of the whole K
+    int channel_tiles; // of kRows * CG
+    int tiles;         // channel tiles * token tiles
+    int bn;            // tokens per tile
+    int split;         // CTAs that share K (CG 1)
+    int f32;           // output type
+};
+
+struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++at == n) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+__device__ __forceinline__ void gave_up(const GemmParams& p, volatile int* abort) {
+    *abort = 1;
+    atomicOr(p.status, 1u);
+}
+
+// A whole warp's wait: all lanes go on or all give up, so that the warp stays
+// whole for the .aligned instructions that follow.
+__device__ __forceinline__ bool warp_wait(const GemmParams& p, uint64_t* bar, uint32_t parity,
+                                          volatile int* abort) {
+    const bool ok = mbar_wait_cluster(smem_addr(bar), parity, abort);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    gave_up(p, abort);
+    return false;
+}
+
+// Four int8 as two pairs of f16.
+__device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
+    const uint32_t u = v ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1024 + 128
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 ha = __hsub2(*reinterpret_cast<const __half2*>(&a), bias);
+    const __half2 hb = __hsub2(*reinterpret_cast<const __half2*>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t*>(&ha);
+    hi = *reinterpret_cast<const uint32_t*>(&hb);
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+                 "r"(d)
+                 : "memory");
+}
+
+__device__ __forceinline__ void store_out(const GemmParams& p, int64_t at, float v) {
+    if (p.f32)
+        static_cast<float*>(p.out)[at] = v;
+    else
+        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+}
+
+template <int CG, bool INT8>
+__global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
+    gemm_kernel(const __grid_constant__ CUtensorMap x_map,
+                const __grid_constant__ CUtensorMap w_map,
+                const __grid_constant__ GemmParams p) {
+    constexpr uint32_t S = stages(CG, INT8);
+    constexpr int kStage = stage_bytes(CG, INT8), kSlot = slot_bytes(CG, INT8);
+    constexpr uint32_t kAcc = max_tokens(CG, INT8);         // TMEM columns between accumulators
+    constexpr uint32_t kWide = 2 * kAcc;                    // first widened slot's column
+    extern __shared__ unsigned char raw_smem[];
+    unsigned char* smem = reinterpret_cast<unsigned char*>(
+        (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
+    Header& h = *reinterpret_cast<Header*>(smem);
+    const uint32_t ring = smem_addr(smem) + kHeaderBytes;
+    const uint32_t slots = ring + S * kStage;
+    [[maybe_unused]] float* join = reinterpret_cast<float*>(smem + kHeaderBytes + S * kStage +
+                                                            kSlots * kSlot);
+    volatile int* abort = &h.abort;
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // With CG 2 the cluster is the pair; the even CTA issues its MMAs.  With
+    // CG 1 the cluster's CTAs split K.
+    const uint32_t rank = cluster_cta_rank();
+    const uint32_t unit = cluster_id_x(), units = cluster_count_x();
+    const bool leader = CG == 1 || rank == 0;
+    const int split = CG == 1 ? p.split : 1;
+    const int kb0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / split) : 0;
+    const int kb1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / split)
+                            : p.k_blocks;
+    const int bn_cta = p.bn / CG;  // token rows this CTA loads
+
+    if (threadIdx.x == 0) {
+        for (uint32_t s = 0; s < S; ++s) {
+            mbar_init(smem_addr(&h.full[s]), 1);
+            mbar_init(smem_addr(&h.empty[s]), INT8 ? 8 : 1);
+        }
+        for (int c = 0; c < kSlots; ++c) {
+            mbar_init(smem_addr(&h.wide_full[c]), 4 * CG);
+            mbar_init(smem_addr(&h.wide_empty[c]), 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(smem_addr(&h.acc_full[b]), 1);
+            mbar_init(smem_addr(&h.acc_empty[b]), 4 * CG);
+        }
+        mbar_init(smem_addr(&h.joined), 4 * split);
+        mbar_init(smem_addr(&h.drained), 1);
+        h.abort = 0;
+        mbar_init_fence();
+        tensormap_prefetch(&x_map);
+        tensormap_prefetch(&w_map);
+    }
+    if (warp == 1) tmem_alloc<CG>(smem_addr(&h.tmem), kTmemColumns);
+    tcgen05_fence_before();
+    __syncthreads();
+    // The peers' barriers must be initialised before anything arrives there.
+    if (CG == 2 || split > 1) cluster_barrier();
+    tcgen05_fence_after();
+    const uint32_t tmem = h.tmem;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-    const int64_t nt = (g.N + kTile - 1) / kTile, mt = (g.M + kTile - 1) / kTile;
-    for (int64_t tile = blockIdx.x; tile < nt * mt; tile += gridDim.x) {
-        const int64_t n0 = tile % nt * kTile, m0 = tile / nt * kTile;
-        float acc[4][4] = {};
-        for (int64_t k0 = 0; k0 < g.K; k0 += kDeep) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < kTile * kDeep; i += 256) {
-                const int r = i / kDeep, k = i % kDeep;
-                const bool in = k0 + k < g.K;
-                xs[k][r] = in && m0 + r < g.M
-                               ? widen(static_cast<const uint8_t*>(g.x)[(m0 + r) * g.K + k0 + k], g.qtype)
-                               : 0.f;
-                ws[k][r] = in && n0 + r < g.N
-                               ? widen(static_cast<const uint8_t*>(g.w)[(n0 + r) * g.K + k0 + k], g.qtype)
-                               : 0.f;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------- TMA -----
+        Ring r;
+        uint32_t issued = 0;
+        bool ok = true;
+        const uint32_t bytes = static_cast<uint32_t>((kRows + bn_cta) * kBlockK);
+        for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles); tile += units) {
+            const int channel = static_cast<int>(tile % p.channel_tiles) * (kRows * CG) +
+                                (CG == 2 ? static_cast<int>(rank) * kRows : 0);
+            const int token = static_cast<int>(tile / p.channel_tiles) * p.bn +
+                              (CG == 2 ? static_cast<int>(rank) * bn_cta : 0);
+            for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(S)) {
+                if (!mbar_wait_cluster(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
+                    gave_up(p, abort);
+                    ok = false;
+                    break;
+                }
+                // e4m3 pairs: both CTAs' copies count on the leader's barrier,
+                // which alone issues the products; int8: on this CTA's, whose
+                // warps widen them.
+                const uint32_t local = smem_addr(&h.full[r.at]);
+                const uint32_t bar = CG == 2 && !INT8 ? map_to_rank(local, 0) : local;
+                if (INT8 || leader) mbar_arrive_expect_tx(local, INT8 ? bytes : bytes * CG);
+                const uint32_t dst = ring + r.at * kStage;
+                tma_load_2d<INT8 ? 1 : CG>(dst, &w_map, kb * kBlockK, channel, bar);
+                tma_load_2d<INT8 ? 1 : CG>(dst + kRows * kBlockK, &x_map, kb * kBlockK, token,
+                                           bar);
             }
-            __syncthreads();
-#pragma unroll 8
-            for (int k = 0; k < kDeep; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        acc[i][j] = fmaf(xs[k][ty + 16 * i], ws[k][tx + 16 * j], acc[i][j]);
         }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-                if (m >= g.M || n >= g.N) continue;
-                const float v = acc[i][j] * g.x_scale[m] * g.w_scale[n];
-                if (g.dtype == TW_BF16)
-                    static_cast<__nv_bfloat16*>(g.out)[m * g.N + n] = __float2bfloat16_rn(v);
-                else
-                    static_cast<float*>(g.out)[m * g.N + n] = v;
+        if (*abort && (INT8 || leader)) {
+            // The copies in flight must land before the CTA may leave.
+            for (uint32_t k = 0; k < S && k < issued; ++k) {
+                if (r.at == 0) {
+                    r.at = S - 1;
+                    r.phase ^= 1u;
+                } else {
+                    --r.at;
+                }
+                if (!mbar_wait(smem_addr(&h.full[r.at]), r.phase, nullptr))
+                    atomicOr(p.status, 2u);
             }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------------- MMA -----
+        Ring r, acc;
+        bool ok = true;
+        const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
+        for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles);
+             tile += units, acc.next(2)) {
+            if (!mbar_wait_cluster(smem_addr(&h.acc_empty[acc.at]), acc.phase ^ 1u, abort)) {
+                gave_up(p, abort);
+                break;
+            }
+            tcgen05_fence_after();
+            const uint32_t d = tmem + acc.at * kAcc;
+            if constexpr (INT8) {
+                for (int k = 2 * kb0; k < 2 * kb1; ++k, r.next(kSlots)) {
+                    if (!mbar_wait_cluster(smem_addr(&h.wide_full[r.at]), r.phase, abort)) {
+                        gave_up(p, abort);
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_fence_after();
+                    const uint64_t b = smem_operand(slots + r.at * kSlot);
+                    const uint32_t a = tmem + kWide + r.at * kSlotColumns;
+#pragma unroll
+                    for (int i = 0; i < kUnitK / 16; ++i)
+                        mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape, k > 2 * kb0 || i > 0);
+                    mma_commit<CG>(smem_addr(&h.wide_empty[r.at]));
+                }
+            } else {
+                for (int k = kb0; k < kb1; ++k, r.next(S)) {
+                    if (!mbar_wait_cluster(smem_addr(&h.full[r.at]), r.phase, abort)) {
+                        gave_up(p, abort);
+                        ok = false;
+                        break;
+                    }
+                    tcgen05_fence_after();
+                    const uint64_t a = smem_operand(ring + r.at * kStage);
+                    const uint64_t b = smem_operand(ring + r.at * kStage + kRows * kBlockK);
+#pragma unroll
+                    for (int i = 0; i < kBlockK / 32; ++i)
+                        mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > kb0 || i > 0);
+                    mma_commit<CG>(smem_addr(&h.empty[r.at]));
+                }
+            }
+            if (ok) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]));
+        }
+        if (*abort) {
+            // Products in flight still read shared memory and write TMEM.
+            mma_commit<CG>(smem_addr(&h.drained));
+            if (!mbar_wait_cluster(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
+        }
+    } else if (warp >= kEpilogueWarp && warp < kEpilogueWarp + 4) {
+        // -------------------------------------------------- epilogue -----
+        // Thread = channel (TMEM lane), registers = tokens.
+        const int quarter = warp - kEpilogueWarp;
+        const int etid = quarter * 32 + lane;
+        float* x_scale = h.x_scale[quarter];
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        Ring acc;
+        for (uint32_t tile = unit; tile < static_cast<uint32_t>(p.tiles);
+             tile += units, acc.next(2)) {
+            const int64_t n = static_cast<int64_t>(tile % p.channel_tiles) * (kRows * CG) +
+                              (CG == 2 ? rank * kRows : 0) + etid;
+            const int t0 = static_cast<int>(tile / p.channel_tiles) * p.bn;
+            const float ws = n < p.N ? p.w_scale[n] : 0.f;
+            __syncwarp();
+            for (int i = lane; i < p.bn; i += 32)
+                x_scale[i] = t0 + i < p.M ? p.x_scale[t0 + i] : 0.f;
+            __syncwarp();
+            if (!warp_wait(p, &h.acc_full[acc.at], acc.phase, abort)) break;
+            tcgen05_fence_after();
+            const uint32_t d = tmem + acc.at * kAcc + lanes;
+            const int n_tok = p.M - t0 < p.bn ? p.M - t0 : p.bn;
+            if (CG == 1 && split > 1) {
+                // Push every CTA's columns to it, then add up this CTA's.
+                const int own = p.bn / split;
+                for (int c = 0; c < p.bn; c += 16) {
+                    uint32_t v[16];
+                    tmem_load16(v, d + c);
+                    tmem_wait_loads();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const int to = (c + j) / own;
+                        const float* slot =
+                            join + (static_cast<int>(rank) * own + (c + j - to * own)) * kRows +
+                            etid;
+                        st_cluster_f32(map_to_rank(smem_addr(slot), static_cast<uint32_t>(to)),
+                                       __uint_as_float(v[j]));
+                    }
+                    __syncwarp();
+                }
+                __syncwarp();
+                if (lane < split)
+                    mbar_arrive_cluster(map_to_rank(smem_addr(&h.joined),
+                                                    static_cast<uint32_t>(lane)));
+                if (!warp_wait(p, &h.joined, 0, abort)) break;
+                for (int j = 0; j < own; ++j) {
+                    const int c = static_cast<int>(rank) * own + j;
+                    float sum = 0.f;
+                    for (int s = 0; s < split; ++s) sum += join[(s * own + j) * kRows + etid];
+                    if (c < n_tok && n < p.N)
+                        store_out(p, (t0 + c) * p.N + n, sum * x_scale[c] * ws);
+                }
+                break;  // one tile per cluster
+            }
+            for (int c = 0; c < p.bn; c += 16) {
+                uint32_t v[16];
+                tmem_load16(v, d + c);
+                tmem_wait_loads();
+                if (c + 16 >= p.bn) {
+                    // The accumulator is read: hand it back before the stores.
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(map_to_rank(
+                        smem_addr(&h.acc_empty[acc.at]), CG == 2 ? 0u : rank));
+                }
+                if (n < p.N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (c + j < n_tok)
+                            store_out(p, (static_cast<int64_t>(t0) + c + j) * p.N + n,
+                                      __uint_as_float(v[j]) * x_scale[c + j] * ws);
+                }
+                __syncwarp();
+            }
+        }
+    } else if (INT8 && warp >= kWidenWarp) {
+        // ------------------------------------------------- widening ------
+        // Group 0 widens the first 64 K elements of every stage, group 1 the
+        // second 64: row `row` of W into TMEM lane `row`, and the token rows.
+        const int group = (warp - kWidenWarp) / 4;
+        const int row = threadIdx.x % 128;
+        const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
+        Ring r, c;
+        c.at = static_cast<uint32_t>(group);
+        bool ok = true;
+        for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles); tile += units) {
+            for (int kb = kb0; kb < kb1; ++kb, r.next(S)) {
+                ok = warp_wait(p, &h.full[r.at], r.phase, abort);
+                if (!ok) break;
+                const uint32_t stage = ring + r.at * kStage;
+                // 16-byte chunk i of row R lies at chunk i ^ (R & 7).
+                uint32_t w[32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 v = lds16(stage + row * kBlockK +
+                                          (((group * 4 + i) ^ (row & 7)) << 4));
+                    widen4(v.x, w[8 * i], w[8 * i + 1]);
+                    widen4(v.y, w[8 * i + 2], w[8 * i + 3]);
+                    widen4(v.z, w[8 * i + 4], w[8 * i + 5]);
+                    widen4(v.w, w[8 * i + 6], w[8 * i + 7]);
+                }
+                ok = warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort);
+                if (!ok) break;
+                tcgen05_fence_after();
+                tmem_store32(tmem + lanes + kWide + c.at * kSlotColumns, w);
+                // Eight neighbouring threads take one chunk of eight rows
+                // (eight different bank groups, read and written).
+                const uint32_t slot = slots + c.at * kSlot;
+                for (int i = row; i < bn_cta * 4; i += 128) {
+                    const int xr = (i & 7) + (i >> 5 << 3), ch = (i >> 3) & 3;
+                    const uint4 v = lds16(stage + kRows * kBlockK + xr * kBlockK +
+                                          (((group * 4 + ch) ^ (xr & 7)) << 4));
+                    uint32_t o[8];
+                    widen4(v.x, o[0], o[1]);
+                    widen4(v.y, o[2], o[3]);
+                    widen4(v.z, o[4], o[5]);
+                    widen4(v.w, o[6], o[7]);
+                    const uint32_t to = slot + xr * 128;
+                    sts16(to + (((2 * ch) ^ (xr & 7)) << 4), o[0], o[1], o[2], o[3]);
+                    sts16(to + (((2 * ch + 1) ^ (xr & 7)) << 4), o[4], o[5], o[6], o[7]);
+                }
+                tmem_wait_stores();
+                fence_async_shared();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&h.empty[r.at]));
+                    mbar_arrive_cluster(
+                        map_to_rank(smem_addr(&h.wide_full[c.at]), CG == 2 ? 0u : rank));
+                }
+                c.next(kSlots);
+                c.next(kSlots);
+            }
+        }
     }
+    __syncwarp();
+    tcgen05_fence_before();
+    __syncthreads();
+    // No CTA leaves while another may still write into it or read its rows.
+    if (CG == 2 || split > 1) cluster_barrier();
+    tcgen05_fence_after();
+    if (warp == 1) tmem_free<CG>(tmem, kTmemColumns);
+}
+
+// ------------------------------------------------------------ host side ---
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                 const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;
+
+// A [rows, K] 8-bit tensor read in boxes of 128 bytes x box_rows; what lies
+// outside reads as zeros (0 in both types).
+bool encode(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box_rows) {
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
+    const cuuint32_t box[2] = {kBlockK, static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t step[2] = {1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), size, stride,
+                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void* gemm_kernel_for(int cg, bool int8) {
+    if (cg == 1)
+        return int8 ? reinterpret_cast<void*>(&gemm_kernel<1, true>)
+                    : reinterpret_cast<void*>(&gemm_kernel<1, false>);
+    return int8 ? reinterpret_cast<void*>(&gemm_kernel<2, true>)
+                : reinterpret_cast<void*>(&gemm_kernel<2, false>);
 }
 
 }  // namespace
 
-int gemm_prepare(int) {
-    return static_cast<int>(cudaFuncSetAttribute(
-        gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes));
+int gemm_prepare(int smem_optin) {
+    for (int cg = 1; cg <= 2; ++cg)
+        for (bool int8 : {false, true}) {
+            if (smem_bytes(cg, int8) > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
+            cudaError_t e = cudaFuncSetAttribute(gemm_kernel_for(cg, int8),
+                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 smem_bytes(cg, int8));
+            if (e != cudaSuccess) return static_cast<int>(e);
+        }
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                     cudaEnableDefault, &found);
+    if (e != cudaSuccess) return static_cast<int>(e);
+    if (found != cudaDriverEntryPointSuccess || !fn)
+        return static_cast<int>(cudaErrorSymbolNotFound);
+    g_encode = reinterpret_cast<EncodeTiled>(fn);
+    return 0;
 }
 
 int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream) {
-    const int64_t tiles = ((g.N + kTile - 1) / kTile) * ((g.M + kTile - 1) / kTile);
-    const bool whole = max_sms >= d.sm_count;
-    const int64_t most = whole ? int64_t{4} * d.sm_count : max_sms;
-    const int grid = static_cast<int>(tiles < most ? tiles : most);
-    return launch_with_pdl(reinterpret_cast<void*>(&gemm_kernel), g, grid, 256,
-                           whole ? 0 : kExclusiveSmemBytes, whole, stream);
+    const bool int8 = g.qtype == TW_INT8;
+    const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
+    const int cg = g.M <= max_tokens(1, int8) || sms < 2 ? 1 : 2;
+    const int align = 16 * cg;
+    const int64_t token_tiles = (g.M + max_tokens(cg, int8) - 1) / max_tokens(cg, int8);
+    const int64_t per_tile = (g.M + token_tiles - 1) / token_tiles;
+    GemmParams p{};
+    p.x_scale = g.x_scale;
+    p.w_scale = g.w_scale;
+    p.out = g.out;
+    p.status = d.status;
+    p.N = g.N;
+    p.M = static_cast<int>(g.M);
+    p.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
+    p.bn = static_cast<int>((per_tile + align - 1) / align * align);
+    const int64_t channel_tiles = (g.N + kRows * cg - 1) / (kRows * cg);
+    const int64_t tiles = channel_tiles * ((g.M + p.bn - 1) / p.bn);
+    if (tiles > (int64_t{1} << 31) - 1 - sms) return static_cast<int>(cudaErrorInvalidValue);
+    p.channel_tiles = static_cast<int>(channel_tiles);
+    p.tiles = static_cast<int>(tiles);
+    p.f32 = g.dtype == TW_F32;
+    p.split = 1;
+    if (cg == 1)
+        while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.split * 2 <= p.k_blocks)
+            p.split *= 2;
+    CUtensorMap x_map, w_map;
+    if (!encode(&x_map, g.x, g.M, g.K, p.bn / cg) || !encode(&w_map, g.w, g.N, g.K, kRows))
+        return static_cast<int>(cudaErrorInvalidValue);
+
+    const int cluster = cg == 1 ? p.split : 2;
+    const int64_t most = sms / cluster;
+    const int64_t units = tiles < most ? tiles : most;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
+    cfg.blockDim = dim3(int8 ? 512 : 256);
+    cfg.dynamicSmemBytes = smem_bytes(cg, int8);
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = max_sms >= d.sm_count ? 2 : 1;
+    void* args[] = {&x_map, &w_map, &p};
+    return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8), args));
 }
 
 }  // namespace tw
