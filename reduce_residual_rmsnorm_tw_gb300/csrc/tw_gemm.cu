@@ -111,9 +111,10 @@ __device__ __forceinline__ void gave_up(const GemmParams& p, volatile int* abort
 
 // A whole warp's wait: all lanes go on or all give up, so that the warp stays
 // whole for the .aligned instructions that follow.
+template <bool CLUSTER = false>
 __device__ __forceinline__ bool warp_wait(const GemmParams& p, uint64_t* bar, uint32_t parity,
                                           volatile int* abort) {
-    const bool ok = mbar_wait_cluster(smem_addr(bar), parity, abort);
+    const bool ok = mbar_wait_slice<CLUSTER>(smem_addr(bar), parity, abort);
     if (__all_sync(0xffffffffu, ok)) return true;
     gave_up(p, abort);
     return false;
@@ -130,6 +131,13 @@ __device__ __forceinline__ void widen4(uint32_t v, uint32_t& lo, uint32_t& hi) {
     hi = *reinterpret_cast<const uint32_t*>(&hb);
 }
 
+__device__ __forceinline__ void widen16(const uint4& v, uint32_t* f) {
+    widen4(v.x, f[0], f[1]);
+    widen4(v.y, f[2], f[3]);
+    widen4(v.z, f[4], f[5]);
+    widen4(v.w, f[6], f[7]);
+}
+
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -137,10 +145,9 @@ __device__ __forceinline__ uint4 lds16(uint32_t addr) {
                  : "r"(addr));
     return v;
 }
-__device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
-                                      uint32_t d) {
-    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
-                 "r"(d)
+__device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* v) {
+    asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
                  : "memory");
 }
 
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
             const int token = static_cast<int>(tile / p.channel_tiles) * p.bn +
                               (CG == 2 ? static_cast<int>(rank) * bn_cta : 0);
             for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(S)) {
-                if (!mbar_wait_cluster(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
+                if (!mbar_wait_slice(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
                     gave_up(p, abort);
                     ok = false;
                     break;
@@ -254,56 +261,59 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
                     atomicOr(p.status, 2u);
             }
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------------- MMA -----
+        // The whole warp walks the slices and one elected lane issues: with
+        // the operands in warp-uniform code a slice's four MMAs issue in a
+        // fraction of the time a lone lane takes.
         Ring r, acc;
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles);
              tile += units, acc.next(2)) {
-            if (!mbar_wait_cluster(smem_addr(&h.acc_empty[acc.at]), acc.phase ^ 1u, abort)) {
-                gave_up(p, abort);
-                break;
-            }
+            ok = warp_wait(p, &h.acc_empty[acc.at], acc.phase ^ 1u, abort);
+            if (!ok) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * kAcc;
             if constexpr (INT8) {
                 for (int k = 2 * kb0; k < 2 * kb1; ++k, r.next(kSlots)) {
-                    if (!mbar_wait_cluster(smem_addr(&h.wide_full[r.at]), r.phase, abort)) {
-                        gave_up(p, abort);
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
+                    if (!ok) break;
                     tcgen05_fence_after();
-                    const uint64_t b = smem_operand(slots + r.at * kSlot);
-                    const uint32_t a = tmem + kWide + r.at * kSlotColumns;
+                    if (elect_one()) {
+                        const uint64_t b = smem_operand(slots + r.at * kSlot);
+                        const uint32_t a = tmem + kWide + r.at * kSlotColumns;
 #pragma unroll
-                    for (int i = 0; i < kUnitK / 16; ++i)
-                        mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape, k > 2 * kb0 || i > 0);
-                    mma_commit<CG>(smem_addr(&h.wide_empty[r.at]));
+                        for (int i = 0; i < kUnitK / 16; ++i)
+                            mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape,
+                                             k > 2 * kb0 || i > 0);
+                        mma_commit<CG>(smem_addr(&h.wide_empty[r.at]));
+                    }
+                    __syncwarp();
                 }
             } else {
                 for (int k = kb0; k < kb1; ++k, r.next(S)) {
-                    if (!mbar_wait_cluster(smem_addr(&h.full[r.at]), r.phase, abort)) {
-                        gave_up(p, abort);
-                        ok = false;
-                        break;
-                    }
+                    ok = warp_wait(p, &h.full[r.at], r.phase, abort);
+                    if (!ok) break;
                     tcgen05_fence_after();
-                    const uint64_t a = smem_operand(ring + r.at * kStage);
-                    const uint64_t b = smem_operand(ring + r.at * kStage + kRows * kBlockK);
+                    if (elect_one()) {
+                        const uint64_t a = smem_operand(ring + r.at * kStage);
+                        const uint64_t b = smem_operand(ring + r.at * kStage + kRows * kBlockK);
 #pragma unroll
-                    for (int i = 0; i < kBlockK / 32; ++i)
-                        mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > kb0 || i > 0);
-                    mma_commit<CG>(smem_addr(&h.empty[r.at]));
+                        for (int i = 0; i < kBlockK / 32; ++i)
+                            mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > kb0 || i > 0);
+                        mma_commit<CG>(smem_addr(&h.empty[r.at]));
+                    }
+                    __syncwarp();
                 }
             }
-            if (ok) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]));
+            if (ok && elect_one()) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]));
+            __syncwarp();
         }
-        if (*abort) {
+        if (!ok) {
             // Products in flight still read shared memory and write TMEM.
-            mma_commit<CG>(smem_addr(&h.drained));
-            if (!mbar_wait_cluster(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
+            if (elect_one()) mma_commit<CG>(smem_addr(&h.drained));
+            if (!mbar_wait_slice(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
         }
     } else if (warp >= kEpilogueWarp && warp < kEpilogueWarp + 4) {
         // -------------------------------------------------- epilogue -----
@@ -349,7 +359,7 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
                 if (lane < split)
                     mbar_arrive_cluster(map_to_rank(smem_addr(&h.joined),
                                                     static_cast<uint32_t>(lane)));
-                if (!warp_wait(p, &h.joined, 0, abort)) break;
+                if (!warp_wait<true>(p, &h.joined, 0, abort)) break;
                 for (int j = 0; j < own; ++j) {
                     const int c = static_cast<int>(rank) * own + j;
                     float sum = 0.f;
@@ -367,8 +377,9 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
                     // The accumulator is read: hand it back before the stores.
                     tcgen05_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(map_to_rank(
-                        smem_addr(&h.acc_empty[acc.at]), CG == 2 ? 0u : rank));
+                    if (lane == 0)
+                        mbar_arrive_pair(
+                            map_to_rank(smem_addr(&h.acc_empty[acc.at]), CG == 2 ? 0u : rank));
                 }
                 if (n < p.N) {
 #pragma unroll
@@ -386,6 +397,10 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
         // second 64: row `row` of W into TMEM lane `row`, and the token rows.
         const int group = (warp - kWidenWarp) / 4;
         const int row = threadIdx.x % 128;
+        // 16-byte chunks of the token rows per thread: 32 rows x 4 chunks at
+        // a time, this warp's first row x_row0.
+        constexpr int kTokenChunks = max_tokens(CG, true) / CG / 32;
+        const int x_row0 = row / 32 * 8, x_row = x_row0 + (row & 7), x_chunk = row / 8 % 4;
         const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
         Ring r, c;
         c.at = static_cast<uint32_t>(group);
@@ -395,46 +410,44 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
                 ok = warp_wait(p, &h.full[r.at], r.phase, abort);
                 if (!ok) break;
                 const uint32_t stage = ring + r.at * kStage;
-                // 16-byte chunk i of row R lies at chunk i ^ (R & 7).
-                uint32_t w[32];
+                // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
+                // neighbouring threads take one chunk of eight rows (eight
+                // different bank groups, read and written).
+                uint4 raw[4 + kTokenChunks];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 v = lds16(stage + row * kBlockK +
-                                          (((group * 4 + i) ^ (row & 7)) << 4));
-                    widen4(v.x, w[8 * i], w[8 * i + 1]);
-                    widen4(v.y, w[8 * i + 2], w[8 * i + 3]);
-                    widen4(v.z, w[8 * i + 4], w[8 * i + 5]);
-                    widen4(v.w, w[8 * i + 6], w[8 * i + 7]);
-                }
+                for (int i = 0; i < 4; ++i)
+                    raw[i] = lds16(stage + row * kBlockK + (((group * 4 + i) ^ (row & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < kTokenChunks; ++i)
+                    if (i * 32 + x_row0 < bn_cta)
+                        raw[4 + i] = lds16(stage + kRows * kBlockK + (i * 32 + x_row) * kBlockK +
+                                           (((group * 4 + x_chunk) ^ (x_row & 7)) << 4));
+                uint32_t w[32], x[kTokenChunks][8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) widen16(raw[i], w + 8 * i);
+#pragma unroll
+                for (int i = 0; i < kTokenChunks; ++i) widen16(raw[4 + i], x[i]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&h.empty[r.at]));
                 ok = warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort);
                 if (!ok) break;
                 tcgen05_fence_after();
                 tmem_store32(tmem + lanes + kWide + c.at * kSlotColumns, w);
-                // Eight neighbouring threads take one chunk of eight rows
-                // (eight different bank groups, read and written).
-                const uint32_t slot = slots + c.at * kSlot;
-                for (int i = row; i < bn_cta * 4; i += 128) {
-                    const int xr = (i & 7) + (i >> 5 << 3), ch = (i >> 3) & 3;
-                    const uint4 v = lds16(stage + kRows * kBlockK + xr * kBlockK +
-                                          (((group * 4 + ch) ^ (xr & 7)) << 4));
-                    uint32_t o[8];
-                    widen4(v.x, o[0], o[1]);
-                    widen4(v.y, o[2], o[3]);
-                    widen4(v.z, o[4], o[5]);
-                    widen4(v.w, o[6], o[7]);
-                    const uint32_t to = slot + xr * 128;
-                    sts16(to + (((2 * ch) ^ (xr & 7)) << 4), o[0], o[1], o[2], o[3]);
-                    sts16(to + (((2 * ch + 1) ^ (xr & 7)) << 4), o[4], o[5], o[6], o[7]);
-                }
-                tmem_wait_stores();
+                const uint32_t slot = slots + c.at * kSlot + x_row * 128;
+#pragma unroll
+                for (int i = 0; i < kTokenChunks; ++i)
+                    if (i * 32 + x_row0 < bn_cta) {
+                        const uint32_t to = slot + i * 32 * 128;
+                        sts16(to + (((2 * x_chunk) ^ (x_row & 7)) << 4), x[i]);
+                        sts16(to + (((2 * x_chunk + 1) ^ (x_row & 7)) << 4), x[i] + 4);
+                    }
                 fence_async_shared();
+                tmem_wait_stores();
                 tcgen05_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&h.empty[r.at]));
-                    mbar_arrive_cluster(
+                if (lane == 0)
+                    mbar_arrive_pair(
                         map_to_rank(smem_addr(&h.wide_full[c.at]), CG == 2 ? 0u : rank));
-                }
                 c.next(kSlots);
                 c.next(kSlots);
             }

@@ -41,6 +41,17 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
                  : "memory");
 }
+// Arrive on a barrier of a CTA of the pair for work that stays in this CTA:
+// its own shared-memory writes (already ordered for the async proxy by
+// fence_async_shared) and TMEM accesses (complete, behind
+// tcgen05.fence::before_thread_sync), which this SM's half of the pair's next
+// MMA uses.  No generic access of the other CTA depends on it, so the arrive
+// keeps CTA scope: at cluster scope the release first waits for every earlier
+// access of the thread to be visible there, about 1000 clocks for each slice
+// of a product (the int8 kernel ran at half the speed).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -52,15 +63,23 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         : "memory");
     return done != 0;
 }
-// As mbar_wait, seeing what the cluster's other CTAs released.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
-                                                  const volatile int* abort) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t start = global_timer_ns();
-    while (true) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if (abort && *abort) return false;
-        if (global_timer_ns() - start > kWaitLimitNs) return false;
+// As mbar_wait, for the waits of a product's slices: the abort flag and the
+// clock are looked at once in 64 tries.  CLUSTER: see what the cluster's other
+// CTAs released (their writes into this CTA's shared memory); without it the
+// acquire stays within the CTA, which is all that work signalled with
+// mbar_arrive_pair, a TMA or a commit needs, and costs no invalidation.
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool mbar_wait_slice(uint32_t bar, uint32_t parity,
+                                                const volatile int* abort) {
+    uint64_t start = 0;
+    for (uint32_t tries = 1;; ++tries) {
+        if (CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (tries % 64 == 0) {
+            if (abort && *abort) return false;
+            const uint64_t now = global_timer_ns();
+            if (start == 0) start = now;
+            if (now - start > kWaitLimitNs) return false;
+        }
     }
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t remote, float v) {
@@ -70,6 +89,17 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t remote, float v) {
 // (the tensor cores').
 __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// One lane of a whole warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
 }
 
 // ----------------------------------------------------------------- TMA ---
