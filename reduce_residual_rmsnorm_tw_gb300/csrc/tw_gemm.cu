@@ -41,7 +41,9 @@ constexpr int kMaxStages = 8;
 constexpr int kTmemColumns = 512;
 constexpr int kMaxSplit = 8;
 
-// Warp roles: 0 TMA, 1 MMA, 4-7 epilogue, 8-11 and 12-15 widen (int8).
+// Warp roles: 0 TMA, 1 MMA, 4-7 epilogue, from 8 on kGroups of four widen
+// (int8).
+constexpr int kGroups = 4;
 constexpr int kEpilogueWarp = 4, kWidenWarp = 8;
 
 // Largest token tile: one unit's two accumulators (and, for int8, the widened
@@ -66,7 +68,7 @@ struct Header {
     uint64_t joined, drained;
     uint32_t tmem;
     int abort;
-    float x_scale[4][256];  // each epilogue warp's copy of its tile's
+    alignas(16) float x_scale[4][256];  // each epilogue warp's copy of its tile's
 };
 constexpr int kHeaderBytes = 5120;
 static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
@@ -158,8 +160,52 @@ __device__ __forceinline__ void store_out(const GemmParams& p, int64_t at, float
         static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
 }
 
+// Sixteen tokens of one channel per thread, scaled and stored: v[j] belongs to
+// token t + j (j < n_tok) and channel n (a warp's lanes hold neighbouring
+// channels; n >= N: none).  bf16 neighbours trade every other token, so that
+// each lane stores two channels of one token (an odd N leaves rows unaligned:
+// single values then).
+__device__ __forceinline__ void store16(const GemmParams& p, const uint32_t (&v)[16],
+                                        const float* x_scale, float ws, int64_t t, int n_tok,
+                                        int64_t n, int lane) {
+    float y[16];
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const float4 xs = *reinterpret_cast<const float4*>(x_scale + j);
+        y[j] = __uint_as_float(v[j]) * xs.x * ws;
+        y[j + 1] = __uint_as_float(v[j + 1]) * xs.y * ws;
+        y[j + 2] = __uint_as_float(v[j + 2]) * xs.z * ws;
+        y[j + 3] = __uint_as_float(v[j + 3]) * xs.w * ws;
+    }
+    if (p.f32) {
+        float* out = static_cast<float*>(p.out) + t * p.N + n;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < n_tok && n < p.N) out[j * p.N] = y[j];
+    } else if (p.N % 2 == 0) {
+        const bool odd = lane & 1;
+        // The lane's token of a pair is t + j + odd, its channels n & ~1 and
+        // the next.
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (t + odd) * p.N + (n - odd);
+#pragma unroll
+        for (int j = 0; j < 16; j += 2) {
+            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[j + 1], 1);
+            const __nv_bfloat162 two =
+                odd ? __floats2bfloat162_rn(got, y[j + 1]) : __floats2bfloat162_rn(y[j], got);
+            if (j + odd < n_tok && n < p.N)
+                *reinterpret_cast<__nv_bfloat162*>(out + j * p.N) = two;
+        }
+    } else {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.N + n;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (j < n_tok && n < p.N) out[j * p.N] = __float2bfloat16_rn(y[j]);
+    }
+    __syncwarp();
+}
+
 template <int CG, bool INT8>
-__global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
+__global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap x_map,
                 const __grid_constant__ CUtensorMap w_map,
                 const __grid_constant__ GemmParams p) {
@@ -381,20 +427,13 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
                         mbar_arrive_pair(
                             map_to_rank(smem_addr(&h.acc_empty[acc.at]), CG == 2 ? 0u : rank));
                 }
-                if (n < p.N) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (c + j < n_tok)
-                            store_out(p, (static_cast<int64_t>(t0) + c + j) * p.N + n,
-                                      __uint_as_float(v[j]) * x_scale[c + j] * ws);
-                }
-                __syncwarp();
+                store16(p, v, x_scale + c, ws, static_cast<int64_t>(t0) + c, n_tok - c, n, lane);
             }
         }
     } else if (INT8 && warp >= kWidenWarp) {
         // ------------------------------------------------- widening ------
-        // Group 0 widens the first 64 K elements of every stage, group 1 the
-        // second 64: row `row` of W into TMEM lane `row`, and the token rows.
+        // Groups of four warps take the 64-element halves of the stages in
+        // turn: row `row` of W into TMEM lane `row`, and the token rows.
         const int group = (warp - kWidenWarp) / 4;
         const int row = threadIdx.x % 128;
         // 16-byte chunks of the token rows per thread: 32 rows x 4 chunks at
@@ -403,54 +442,56 @@ __global__ void __launch_bounds__(INT8 ? 512 : 256, 1)
         const int x_row0 = row / 32 * 8, x_row = x_row0 + (row & 7), x_chunk = row / 8 % 4;
         const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
         Ring r, c;
-        c.at = static_cast<uint32_t>(group);
-        bool ok = true;
-        for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles); tile += units) {
-            for (int kb = kb0; kb < kb1; ++kb, r.next(S)) {
-                ok = warp_wait(p, &h.full[r.at], r.phase, abort);
-                if (!ok) break;
-                const uint32_t stage = ring + r.at * kStage;
-                // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
-                // neighbouring threads take one chunk of eight rows (eight
-                // different bank groups, read and written).
-                uint4 raw[4 + kTokenChunks];
+        const int tile_units = 2 * (kb1 - kb0);
+        const int my_tiles = static_cast<int>(unit) < p.tiles
+                                 ? (p.tiles - 1 - static_cast<int>(unit)) / static_cast<int>(units) + 1
+                                 : 0;
+        const int64_t n_units = static_cast<int64_t>(my_tiles) * tile_units;
+        for (int i = 0; i < group; ++i) c.next(kSlots);
+        for (int i = 0; i < group / 2; ++i) r.next(S);
+        for (int64_t u = group; u < n_units; u += kGroups) {
+            const int half = static_cast<int>(u) & 1;
+            if (!warp_wait(p, &h.full[r.at], r.phase, abort)) break;
+            const uint32_t stage = ring + r.at * kStage;
+            // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
+            // neighbouring threads take one chunk of eight rows (eight
+            // different bank groups, read and written).
+            uint4 raw[4 + kTokenChunks];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    raw[i] = lds16(stage + row * kBlockK + (((group * 4 + i) ^ (row & 7)) << 4));
+            for (int i = 0; i < 4; ++i)
+                raw[i] = lds16(stage + row * kBlockK + (((half * 4 + i) ^ (row & 7)) << 4));
 #pragma unroll
-                for (int i = 0; i < kTokenChunks; ++i)
-                    if (i * 32 + x_row0 < bn_cta)
-                        raw[4 + i] = lds16(stage + kRows * kBlockK + (i * 32 + x_row) * kBlockK +
-                                           (((group * 4 + x_chunk) ^ (x_row & 7)) << 4));
-                uint32_t w[32], x[kTokenChunks][8];
+            for (int i = 0; i < kTokenChunks; ++i)
+                if (i * 32 + x_row0 < bn_cta)
+                    raw[4 + i] = lds16(stage + kRows * kBlockK + (i * 32 + x_row) * kBlockK +
+                                       (((half * 4 + x_chunk) ^ (x_row & 7)) << 4));
+            uint32_t w[32];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) widen16(raw[i], w + 8 * i);
+            for (int i = 0; i < 4; ++i) widen16(raw[i], w + 8 * i);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&h.empty[r.at]));
+            if (!warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort)) break;
+            tcgen05_fence_after();
+            tmem_store32(tmem + lanes + kWide + c.at * kSlotColumns, w);
+            const uint32_t slot = slots + c.at * kSlot + x_row * 128;
 #pragma unroll
-                for (int i = 0; i < kTokenChunks; ++i) widen16(raw[4 + i], x[i]);
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&h.empty[r.at]));
-                ok = warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort);
-                if (!ok) break;
-                tcgen05_fence_after();
-                tmem_store32(tmem + lanes + kWide + c.at * kSlotColumns, w);
-                const uint32_t slot = slots + c.at * kSlot + x_row * 128;
-#pragma unroll
-                for (int i = 0; i < kTokenChunks; ++i)
-                    if (i * 32 + x_row0 < bn_cta) {
-                        const uint32_t to = slot + i * 32 * 128;
-                        sts16(to + (((2 * x_chunk) ^ (x_row & 7)) << 4), x[i]);
-                        sts16(to + (((2 * x_chunk + 1) ^ (x_row & 7)) << 4), x[i] + 4);
-                    }
-                fence_async_shared();
-                tmem_wait_stores();
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive_pair(
-                        map_to_rank(smem_addr(&h.wide_full[c.at]), CG == 2 ? 0u : rank));
-                c.next(kSlots);
-                c.next(kSlots);
-            }
+            for (int i = 0; i < kTokenChunks; ++i)
+                if (i * 32 + x_row0 < bn_cta) {
+                    uint32_t x[8];
+                    widen16(raw[4 + i], x);
+                    const uint32_t to = slot + i * 32 * 128;
+                    sts16(to + (((2 * x_chunk) ^ (x_row & 7)) << 4), x);
+                    sts16(to + (((2 * x_chunk + 1) ^ (x_row & 7)) << 4), x + 4);
+                }
+            fence_async_shared();
+            tmem_wait_stores();
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_pair(map_to_rank(smem_addr(&h.wide_full[c.at]), CG == 2 ? 0u : rank));
+            const int step = (half + kGroups) / 2;  // stages on to unit u + kGroups
+            for (int i = 0; i < step; ++i) r.next(S);
+            for (int i = 0; i < kGroups; ++i) c.next(kSlots);
         }
     }
     __syncwarp();
@@ -547,7 +588,7 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     const int64_t units = tiles < most ? tiles : most;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
-    cfg.blockDim = dim3(int8 ? 512 : 256);
+    cfg.blockDim = dim3(int8 ? 256 + 128 * kGroups : 256);
     cfg.dynamicSmemBytes = smem_bytes(cg, int8);
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
