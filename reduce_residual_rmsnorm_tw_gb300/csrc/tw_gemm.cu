@@ -55,10 +55,15 @@ __host__ __device__ constexpr int stage_bytes(int cg, bool int8) { return kRows 
 __host__ __device__ constexpr int slot_bytes(int cg, bool int8) {
     return int8 ? max_tokens(cg, int8) / cg * kUnitK * 2 : 0;
 }
-__host__ __device__ constexpr int stages(int cg, bool int8) { return cg == 1 && !int8 ? 7 : 6; }
-// Split K: the accumulators of every CTA of the cluster for this CTA's columns.
-__host__ __device__ constexpr int join_bytes(int cg, bool int8) {
-    return cg == 1 ? max_tokens(cg, int8) * kRows * 4 : 0;
+__host__ __device__ constexpr int stages(int cg, bool int8) {
+    return cg == 1 ? (int8 ? 6 : 7) : (int8 ? 5 : 6);
+}
+// Staging of the output: two chunks of 32 tokens (bf16) or 16 (fp32) x 128
+// channels for TMA to store; or, with split K, the accumulators of every CTA
+// of the cluster for this CTA's columns.
+constexpr int kChunkBytes = 8192;
+__host__ __device__ constexpr int out_bytes(int cg, bool int8) {
+    return cg == 1 ? max_tokens(cg, int8) * kRows * 4 : 2 * kChunkBytes;
 }
 
 struct Header {
@@ -75,7 +80,7 @@ static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
 
 __host__ __device__ constexpr int smem_bytes(int cg, bool int8) {
     return 1024 + kHeaderBytes + stages(cg, int8) * stage_bytes(cg, int8) +
-           kSlots * slot_bytes(cg, int8) + join_bytes(cg, int8);
+           kSlots * slot_bytes(cg, int8) + out_bytes(cg, int8);
 }
 static_assert(smem_bytes(1, true) <= 232448 && smem_bytes(1, false) <= 232448 &&
                   smem_bytes(2, true) <= 232448 && smem_bytes(2, false) <= 232448,
@@ -93,6 +98,7 @@ struct GemmParams {
     int tiles;         // channel tiles * token tiles
     int bn;            // tokens per tile
     int split;         // CTAs that share K (CG 1)
+    int tma_out;       // rows of out are whole 16-byte units: stored by TMA
     int f32;           // output type
 };
 
@@ -160,54 +166,36 @@ __device__ __forceinline__ void store_out(const GemmParams& p, int64_t at, float
         static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
 }
 
-// Sixteen tokens of one channel per thread, scaled and stored: v[j] belongs to
-// token t + j (j < n_tok) and channel n (a warp's lanes hold neighbouring
-// channels; n >= N: none).  bf16 neighbours trade every other token, so that
-// each lane stores two channels of one token (an odd N leaves rows unaligned:
-// single values then).
-__device__ __forceinline__ void store16(const GemmParams& p, const uint32_t (&v)[16],
-                                        const float* x_scale, float ws, int64_t t, int n_tok,
-                                        int64_t n, int lane) {
-    float y[16];
+// y[j] = v[j] * x_scale[j] * ws for sixteen tokens (in this order: the product
+// of two small scales alone could lose its bits as a subnormal).
+__device__ __forceinline__ void scale16(float (&y)[16], const uint32_t (&v)[16],
+                                        const float (&xs)[16], float ws) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]) * xs[j] * ws;
+}
+__device__ __forceinline__ void load16(float (&y)[16], const float* x) {
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
-        const float4 xs = *reinterpret_cast<const float4*>(x_scale + j);
-        y[j] = __uint_as_float(v[j]) * xs.x * ws;
-        y[j + 1] = __uint_as_float(v[j + 1]) * xs.y * ws;
-        y[j + 2] = __uint_as_float(v[j + 2]) * xs.z * ws;
-        y[j + 3] = __uint_as_float(v[j + 3]) * xs.w * ws;
+        const float4 q = *reinterpret_cast<const float4*>(x + j);
+        y[j] = q.x;
+        y[j + 1] = q.y;
+        y[j + 2] = q.z;
+        y[j + 3] = q.w;
     }
-    if (p.f32) {
-        float* out = static_cast<float*>(p.out) + t * p.N + n;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < n_tok && n < p.N) out[j * p.N] = y[j];
-    } else if (p.N % 2 == 0) {
-        const bool odd = lane & 1;
-        // The lane's token of a pair is t + j + odd, its channels n & ~1 and
-        // the next.
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + (t + odd) * p.N + (n - odd);
-#pragma unroll
-        for (int j = 0; j < 16; j += 2) {
-            const float got = __shfl_xor_sync(0xffffffffu, odd ? y[j] : y[j + 1], 1);
-            const __nv_bfloat162 two =
-                odd ? __floats2bfloat162_rn(got, y[j + 1]) : __floats2bfloat162_rn(y[j], got);
-            if (j + odd < n_tok && n < p.N)
-                *reinterpret_cast<__nv_bfloat162*>(out + j * p.N) = two;
-        }
-    } else {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + t * p.N + n;
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (j < n_tok && n < p.N) out[j * p.N] = __float2bfloat16_rn(y[j]);
-    }
+}
+
+// This warp has read its part of an accumulator: hand it back to the leader.
+__device__ __forceinline__ void release_acc(uint64_t& bar, int cg, uint32_t rank, int lane) {
+    tcgen05_fence_before();
     __syncwarp();
+    if (lane == 0) mbar_arrive_pair(map_to_rank(smem_addr(&bar), cg == 2 ? 0u : rank));
 }
 
 template <int CG, bool INT8>
 __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap x_map,
                 const __grid_constant__ CUtensorMap w_map,
+                const __grid_constant__ CUtensorMap out_map,
                 const __grid_constant__ GemmParams p) {
     constexpr uint32_t S = stages(CG, INT8);
     constexpr int kStage = stage_bytes(CG, INT8), kSlot = slot_bytes(CG, INT8);
@@ -219,8 +207,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     Header& h = *reinterpret_cast<Header*>(smem);
     const uint32_t ring = smem_addr(smem) + kHeaderBytes;
     const uint32_t slots = ring + S * kStage;
-    [[maybe_unused]] float* join = reinterpret_cast<float*>(smem + kHeaderBytes + S * kStage +
-                                                            kSlots * kSlot);
+    unsigned char* staging = smem + kHeaderBytes + S * kStage + kSlots * kSlot;
     volatile int* abort = &h.abort;
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -248,10 +235,12 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             mbar_init(smem_addr(&h.acc_full[b]), 1);
             mbar_init(smem_addr(&h.acc_empty[b]), 4 * CG);
         }
-        mbar_init(smem_addr(&h.joined), 4 * split);
+        mbar_init(smem_addr(&h.joined), 1);
         mbar_init(smem_addr(&h.drained), 1);
         h.abort = 0;
         mbar_init_fence();
+        if (split > 1)
+            mbar_arrive_expect_tx(smem_addr(&h.joined), static_cast<uint32_t>(p.bn) * kRows * 4);
         tensormap_prefetch(&x_map);
         tensormap_prefetch(&w_map);
     }
@@ -367,6 +356,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         const int quarter = warp - kEpilogueWarp;
         const int etid = quarter * 32 + lane;
         float* x_scale = h.x_scale[quarter];
+        int chunk = 0;
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         Ring acc;
         for (uint32_t tile = unit; tile < static_cast<uint32_t>(p.tiles);
@@ -374,62 +364,124 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             const int64_t n = static_cast<int64_t>(tile % p.channel_tiles) * (kRows * CG) +
                               (CG == 2 ? rank * kRows : 0) + etid;
             const int t0 = static_cast<int>(tile / p.channel_tiles) * p.bn;
+            // Every load of the tile's scales in flight at once.
             const float ws = n < p.N ? p.w_scale[n] : 0.f;
+            float xs[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int j = i * 32 + lane;
+                xs[i] = j < p.bn && t0 + j < p.M ? p.x_scale[t0 + j] : 0.f;
+            }
             __syncwarp();
-            for (int i = lane; i < p.bn; i += 32)
-                x_scale[i] = t0 + i < p.M ? p.x_scale[t0 + i] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x_scale[i * 32 + lane] = xs[i];
             __syncwarp();
-            if (!warp_wait(p, &h.acc_full[acc.at], acc.phase, abort)) break;
+            // The four warps go on or give up together (they meet at barriers
+            // below).
+            const bool ok = warp_wait(p, &h.acc_full[acc.at], acc.phase, abort);
+            if (named_barrier_or(1, 128, !ok)) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * kAcc + lanes;
             const int n_tok = p.M - t0 < p.bn ? p.M - t0 : p.bn;
             if (CG == 1 && split > 1) {
-                // Push every CTA's columns to it, then add up this CTA's.
-                const int own = p.bn / split;
+                // Push every CTA's columns to it, then add up this CTA's: four
+                // columns of a channel travel as 16 bytes, [source][column /
+                // 4][channel].
+                const int own = p.bn / split;  // a multiple of 4
+                const uint32_t local = smem_addr(staging) +
+                                       (static_cast<uint32_t>(rank) * (own / 4) * kRows + etid) * 16;
+                const uint32_t bar = smem_addr(&h.joined);
+                int to = 0, at = 0;
                 for (int c = 0; c < p.bn; c += 16) {
                     uint32_t v[16];
                     tmem_load16(v, d + c);
                     tmem_wait_loads();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        const int to = (c + j) / own;
-                        const float* slot =
-                            join + (static_cast<int>(rank) * own + (c + j - to * own)) * kRows +
-                            etid;
-                        st_cluster_f32(map_to_rank(smem_addr(slot), static_cast<uint32_t>(to)),
-                                       __uint_as_float(v[j]));
+                    for (int j = 0; j < 16; j += 4) {
+                        st_async4(map_to_rank(local + at * (kRows * 4), to), v + j,
+                                  map_to_rank(bar, to));
+                        at += 4;
+                        if (at == own) {
+                            at = 0;
+                            ++to;
+                        }
                     }
-                    __syncwarp();
                 }
-                __syncwarp();
-                if (lane < split)
-                    mbar_arrive_cluster(map_to_rank(smem_addr(&h.joined),
-                                                    static_cast<uint32_t>(lane)));
                 if (!warp_wait<true>(p, &h.joined, 0, abort)) break;
-                for (int j = 0; j < own; ++j) {
+                const float4* part = reinterpret_cast<const float4*>(staging) + etid;
+                for (int j = 0; j < own; j += 4) {
+                    float4 sum = part[j / 4 * kRows];
+                    for (int s = 1; s < split; ++s) {
+                        const float4 q = part[(s * own + j) / 4 * kRows];
+                        sum.x += q.x;
+                        sum.y += q.y;
+                        sum.z += q.z;
+                        sum.w += q.w;
+                    }
                     const int c = static_cast<int>(rank) * own + j;
-                    float sum = 0.f;
-                    for (int s = 0; s < split; ++s) sum += join[(s * own + j) * kRows + etid];
-                    if (c < n_tok && n < p.N)
-                        store_out(p, (t0 + c) * p.N + n, sum * x_scale[c] * ws);
+                    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (c + i < n_tok && n < p.N)
+                            store_out(p, (static_cast<int64_t>(t0) + c + i) * p.N + n,
+                                      v[i] * x_scale[c + i] * ws);
                 }
                 break;  // one tile per cluster
+            }
+            if (p.tma_out) {
+                // Through shared memory, [token][channel], and out by TMA: the
+                // rows of a chunk leave as whole 256- or 512-byte lines beside
+                // the next chunk's loads.
+                const int per_chunk = p.f32 ? 16 : 32;
+                for (int c = 0; c < p.bn; c += per_chunk, chunk ^= 1) {
+                    unsigned char* to = staging + chunk * kChunkBytes;
+                    if (etid == 0) bulk_wait_read<1>();
+                    named_barrier(1, 128);
+                    for (int k = 0; k < per_chunk; k += 16) {
+                        uint32_t v[16];
+                        tmem_load16(v, d + c + k);
+                        float xs16[16], y[16];
+                        load16(xs16, x_scale + c + k);
+                        tmem_wait_loads();
+                        scale16(y, v, xs16, ws);
+                        if (p.f32) {
+                            float* row = reinterpret_cast<float*>(to) + etid;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) row[j * kRows] = y[j];
+                        } else {
+                            __nv_bfloat16* row =
+                                reinterpret_cast<__nv_bfloat16*>(to) + k * kRows + etid;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) row[j * kRows] = __float2bfloat16_rn(y[j]);
+                        }
+                    }
+                    if (c + per_chunk >= p.bn) release_acc(h.acc_empty[acc.at], CG, rank, lane);
+                    fence_async_shared();
+                    named_barrier(1, 128);
+                    if (etid == 0) {
+                        if (c < n_tok && n < p.N)
+                            tma_store_2d(&out_map, static_cast<int>(n), t0 + c, smem_addr(to));
+                        bulk_commit();
+                    }
+                }
+                continue;
             }
             for (int c = 0; c < p.bn; c += 16) {
                 uint32_t v[16];
                 tmem_load16(v, d + c);
+                float xs16[16], y[16];
+                load16(xs16, x_scale + c);
                 tmem_wait_loads();
-                if (c + 16 >= p.bn) {
-                    // The accumulator is read: hand it back before the stores.
-                    tcgen05_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive_pair(
-                            map_to_rank(smem_addr(&h.acc_empty[acc.at]), CG == 2 ? 0u : rank));
-                }
-                store16(p, v, x_scale + c, ws, static_cast<int64_t>(t0) + c, n_tok - c, n, lane);
+                scale16(y, v, xs16, ws);
+                if (c + 16 >= p.bn) release_acc(h.acc_empty[acc.at], CG, rank, lane);
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < n_tok && n < p.N)
+                        store_out(p, (static_cast<int64_t>(t0) + c + j) * p.N + n, y[j]);
+                __syncwarp();
             }
         }
+        if (etid == 0) bulk_wait_read<0>();
     } else if (INT8 && warp >= kWidenWarp) {
         // ------------------------------------------------- widening ------
         // Groups of four warps take the 64-element halves of the stages in
@@ -497,6 +549,12 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     __syncwarp();
     tcgen05_fence_before();
     __syncthreads();
+    // After a wait that ran out, the other CTAs' pushes may still be on their
+    // way here.
+    if (split > 1 && *abort && threadIdx.x == 0 &&
+        !mbar_wait_slice<true>(smem_addr(&h.joined), 0, nullptr))
+        atomicOr(p.status, 2u);
+    __syncwarp();
     // No CTA leaves while another may still write into it or read its rows.
     if (CG == 2 || split > 1) cluster_barrier();
     tcgen05_fence_after();
@@ -510,17 +568,24 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;
 
-// A [rows, K] 8-bit tensor read in boxes of 128 bytes x box_rows; what lies
-// outside reads as zeros (0 in both types).
-bool encode(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box_rows) {
-    const cuuint64_t size[2] = {static_cast<cuuint64_t>(K), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(K)};
-    const cuuint32_t box[2] = {kBlockK, static_cast<cuuint32_t>(box_rows)};
+// A dense [rows, columns] tensor moved in boxes of box_columns x box_rows; what
+// lies outside reads as zeros (0 in every type).
+bool encode(CUtensorMap* m, CUtensorMapDataType type, int64_t elem, const void* base, int64_t rows,
+            int64_t columns, int box_columns, int box_rows, CUtensorMapSwizzle swizzle) {
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t stride[1] = {static_cast<cuuint64_t>(columns * elem)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_columns),
+                               static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t step[2] = {1, 1};
-    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), size, stride,
-                    box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+    return g_encode(m, type, 2, const_cast<void*>(base), size, stride, box, step,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// An 8-bit operand [rows, K], in boxes one swizzle row (128 bytes) wide.
+bool encode_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, int box_rows) {
+    return encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, base, rows, K, kBlockK, box_rows,
+                  CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 void* gemm_kernel_for(int cg, bool int8) {
@@ -557,7 +622,6 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     const bool int8 = g.qtype == TW_INT8;
     const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
     const int cg = g.M <= max_tokens(1, int8) || sms < 2 ? 1 : 2;
-    const int align = 16 * cg;
     const int64_t token_tiles = (g.M + max_tokens(cg, int8) - 1) / max_tokens(cg, int8);
     const int64_t per_tile = (g.M + token_tiles - 1) / token_tiles;
     GemmParams p{};
@@ -568,19 +632,30 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.N = g.N;
     p.M = static_cast<int>(g.M);
     p.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
-    p.bn = static_cast<int>((per_tile + align - 1) / align * align);
+    p.f32 = g.dtype == TW_F32;
     const int64_t channel_tiles = (g.N + kRows * cg - 1) / (kRows * cg);
-    const int64_t tiles = channel_tiles * ((g.M + p.bn - 1) / p.bn);
+    const int64_t tiles = channel_tiles * token_tiles;
     if (tiles > (int64_t{1} << 31) - 1 - sms) return static_cast<int>(cudaErrorInvalidValue);
     p.channel_tiles = static_cast<int>(channel_tiles);
     p.tiles = static_cast<int>(tiles);
-    p.f32 = g.dtype == TW_F32;
     p.split = 1;
     if (cg == 1)
         while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.split * 2 <= p.k_blocks)
             p.split *= 2;
-    CUtensorMap x_map, w_map;
-    if (!encode(&x_map, g.x, g.M, g.K, p.bn / cg) || !encode(&w_map, g.w, g.N, g.K, kRows))
+    // Whole chunks of the output's staging, or of each CTA's share of the
+    // columns (never above max_tokens, a multiple of both).
+    const int align = p.split > 1 ? (p.split > 4 ? 4 * p.split : 16) : 32;
+    p.bn = static_cast<int>((per_tile + align - 1) / align * align);
+    const int64_t es = p.f32 ? 4 : 2;
+    p.tma_out = p.split == 1 && g.N * es % 16 == 0;
+    CUtensorMap x_map, w_map, out_map{};
+    if (!encode_operand(&x_map, g.x, g.M, g.K, p.bn / cg) ||
+        !encode_operand(&w_map, g.w, g.N, g.K, kRows) ||
+        (p.tma_out && !encode(&out_map,
+                              p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              es, g.out, g.M, g.N, kRows, p.f32 ? 16 : 32,
+                              CU_TENSOR_MAP_SWIZZLE_NONE)))
         return static_cast<int>(cudaErrorInvalidValue);
 
     const int cluster = cg == 1 ? p.split : 2;
@@ -600,7 +675,7 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = max_sms >= d.sm_count ? 2 : 1;
-    void* args[] = {&x_map, &w_map, &p};
+    void* args[] = {&x_map, &w_map, &out_map, &p};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8), args));
 }
 

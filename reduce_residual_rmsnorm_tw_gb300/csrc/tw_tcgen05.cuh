@@ -37,10 +37,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
     return remote;
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
-                 : "memory");
-}
 // Arrive on a barrier of a CTA of the pair for work that stays in this CTA:
 // its own shared-memory writes (already ordered for the async proxy by
 // fence_async_shared) and TMEM accesses (complete, behind
@@ -82,8 +78,14 @@ __device__ __forceinline__ bool mbar_wait_slice(uint32_t bar, uint32_t parity,
         }
     }
 }
-__device__ __forceinline__ void st_cluster_f32(uint32_t remote, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote), "f"(v) : "memory");
+// Four floats into another CTA's shared memory; they count 16 bytes on its
+// barrier `bar` (both shared::cluster addresses) when they have landed.
+__device__ __forceinline__ void st_async4(uint32_t remote, const uint32_t* v, uint32_t bar) {
+    asm volatile(
+        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 "
+        "[%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+        : "memory");
 }
 // Order this thread's shared-memory writes before later async-proxy reads
 // (the tensor cores').
@@ -123,6 +125,23 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
             ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
             "l"(map), "r"(x), "r"(y), "r"(bar)
             : "memory");
+}
+
+// One box from this CTA's shared memory to a 2-D tensor (parts outside it are
+// not written), in this thread's current bulk group.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, int x, int y, uint32_t src) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     map),
+                 "r"(x), "r"(y), "r"(src)
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the newest N of this thread's bulk groups have read their source.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
 }
 
 // ---------------------------------------------------------------- TMEM ---
