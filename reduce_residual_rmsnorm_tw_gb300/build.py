@@ -15,7 +15,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtw.so")
 SOURCES = ["tw_api.cu", "tw_rows.cu", "tw_warp.cu", "tw_cluster.cu", "tw_host.cu",
            "tw_noalloc.cu", "tw_signal.cu", "tw_rows_q8.cu", "tw_q8.cu", "tw_quant.cu",
-           "tw_gemm.cu"]
+           "tw_gemm.cu", "tw_gemv.cu"]
 HEADERS = ["tw_device.cuh", "tw_tcgen05.cuh", "tw_rows.cuh", "tw_internal.h", "tw_host.h"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")

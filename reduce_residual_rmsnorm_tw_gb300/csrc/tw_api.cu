@@ -121,6 +121,7 @@ int device_state(DeviceState** out) {
         if ((e = static_cast<cudaError_t>(signal_prepare())) != cudaSuccess)
             return cuda_fail(e, "cudaFuncGetAttributes");
         if ((e = static_cast<cudaError_t>(gemm_prepare(d.smem_optin))) != cudaSuccess ||
+            (e = static_cast<cudaError_t>(gemv_prepare(d.smem_optin))) != cudaSuccess ||
             (e = static_cast<cudaError_t>(quantize_prepare(d.smem_optin))) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute");
         // The cluster kernel is optional: if it cannot be configured, that

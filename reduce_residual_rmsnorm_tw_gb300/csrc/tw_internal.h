@@ -115,6 +115,10 @@ struct GemmArgs {
     int64_t M, N, K;
     int dtype, qtype;
 };
+// Calls of at most this many tokens stream the weights (tw_gemv.cu).
+constexpr int kGemvTokens = 8;
+int launch_gemv(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
+int gemv_prepare(int smem_optin);
 int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
 int gemm_prepare(int smem_optin);
 

@@ -133,5 +133,7 @@ extern "C" int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
                          K,
                          dtype,
                          qtype};
-    return tw::launch_status(tw::launch_gemm(g, max_sms, d, stream), "gemm_q8 launch");
+    const int err = g.M <= tw::kGemvTokens ? tw::launch_gemv(g, max_sms, d, stream)
+                                           : tw::launch_gemm(g, max_sms, d, stream);
+    return tw::launch_status(err, "gemm_q8 launch");
 }
