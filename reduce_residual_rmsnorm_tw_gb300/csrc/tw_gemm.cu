@@ -210,7 +210,10 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     unsigned char* staging = smem + kHeaderBytes + S * kStage + kSlots * kSlot;
     volatile int* abort = &h.abort;
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // A warp index the compiler knows to be the same in all lanes: the MMA
+    // warp's operands then live in uniform registers.
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+    const int lane = threadIdx.x % 32;
     // With CG 2 the cluster is the pair; the even CTA issues its MMAs.  With
     // CG 1 the cluster's CTAs split K.
     const uint32_t rank = cluster_cta_rank();
@@ -304,42 +307,56 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         Ring r, acc;
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
+        [[maybe_unused]] const uint64_t slot_operand = smem_operand(slots);
+        [[maybe_unused]] const uint64_t ring_operand = smem_operand(ring);
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles);
              tile += units, acc.next(2)) {
             ok = warp_wait(p, &h.acc_empty[acc.at], acc.phase ^ 1u, abort);
             if (!ok) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * kAcc;
+            // Whether the next slice is there is asked while this one's products
+            // issue: an answer takes about 100 clocks, a slice's products 300.
+            bool there = false;
             if constexpr (INT8) {
-                for (int k = 2 * kb0; k < 2 * kb1; ++k, r.next(kSlots)) {
-                    ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
+                const int n = 2 * (kb1 - kb0);
+                for (int k = 0; k < n; ++k) {
+                    if (!there) ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
+                    const uint32_t at = r.at;
+                    r.next(kSlots);
+                    there = k + 1 < n && mbar_test(smem_addr(&h.wide_full[r.at]), r.phase);
                     if (elect_one()) {
-                        const uint64_t b = smem_operand(slots + r.at * kSlot);
-                        const uint32_t a = tmem + kWide + r.at * kSlotColumns;
+                        const uint64_t b = slot_operand + at * (kSlot >> 4);
+                        const uint32_t a = tmem + kWide + at * kSlotColumns;
 #pragma unroll
                         for (int i = 0; i < kUnitK / 16; ++i)
-                            mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape,
-                                             k > 2 * kb0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.wide_empty[r.at]));
+                            mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape, k > 0 || i > 0);
+                        mma_commit<CG>(smem_addr(&h.wide_empty[at]));
                     }
                     __syncwarp();
+                    there = __all_sync(0xffffffffu, there);
                 }
             } else {
-                for (int k = kb0; k < kb1; ++k, r.next(S)) {
-                    ok = warp_wait(p, &h.full[r.at], r.phase, abort);
+                const int n = kb1 - kb0;
+                for (int k = 0; k < n; ++k) {
+                    if (!there) ok = warp_wait(p, &h.full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
+                    const uint32_t at = r.at;
+                    r.next(S);
+                    there = k + 1 < n && mbar_test(smem_addr(&h.full[r.at]), r.phase);
                     if (elect_one()) {
-                        const uint64_t a = smem_operand(ring + r.at * kStage);
-                        const uint64_t b = smem_operand(ring + r.at * kStage + kRows * kBlockK);
+                        const uint64_t a = ring_operand + at * (kStage >> 4);
+                        const uint64_t b = a + (kRows * kBlockK >> 4);
 #pragma unroll
                         for (int i = 0; i < kBlockK / 32; ++i)
-                            mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > kb0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.empty[r.at]));
+                            mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0);
+                        mma_commit<CG>(smem_addr(&h.empty[at]));
                     }
                     __syncwarp();
+                    there = __all_sync(0xffffffffu, there);
                 }
             }
             if (ok && elect_one()) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]));
