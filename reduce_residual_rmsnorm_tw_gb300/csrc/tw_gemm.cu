@@ -19,10 +19,9 @@
 //         well, because one byte permute and one packed subtract make an
 //         f16: 0x6400 | (v + 128) is 1024 + 128 + v.
 //
-// With few tokens there are fewer tiles than SMs: a cluster of S CTAs then
-// splits K, and each adds up its share of the token columns from all S
-// accumulators, pushed into its shared memory by the others (in rank order:
-// the same bits every time).
+// With fewer tiles than SMs a cluster of S units splits K, and each adds up its
+// share of the token columns from all S accumulators, copied into its shared
+// memory by the others (and added in rank order: the same bits every time).
 #include <cuda.h>
 
 #include <mutex>
@@ -39,7 +38,6 @@ constexpr int kSlots = 4;        // int8: widened slots (TMEM and shared memory)
 constexpr int kSlotColumns = kUnitK / 2;
 constexpr int kMaxStages = 8;
 constexpr int kTmemColumns = 512;
-constexpr int kMaxSplit = 8;
 
 // Warp roles: 0 TMA, 1 MMA, 4-7 epilogue, from 8 on kGroups of four widen
 // (int8).
@@ -56,21 +54,17 @@ __host__ __device__ constexpr int slot_bytes(int cg, bool int8) {
     return int8 ? max_tokens(cg, int8) / cg * kUnitK * 2 : 0;
 }
 __host__ __device__ constexpr int stages(int cg, bool int8) {
-    return cg == 1 ? (int8 ? 6 : 7) : (int8 ? 5 : 6);
+    return cg == 1 ? (int8 ? 7 : 8) : (int8 ? 5 : 6);
 }
 // Staging of the output: two chunks of 32 tokens (bf16) or 16 (fp32) x 128
-// channels for TMA to store; or, with split K, the accumulators of every CTA
-// of the cluster for this CTA's columns.
+// channels for TMA to store.
 constexpr int kChunkBytes = 8192;
-__host__ __device__ constexpr int out_bytes(int cg, bool int8) {
-    return cg == 1 ? max_tokens(cg, int8) * kRows * 4 : 2 * kChunkBytes;
-}
 
 struct Header {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t wide_full[kSlots], wide_empty[kSlots];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t joined, drained;
+    uint64_t open, joined, drained;
     uint32_t tmem;
     int abort;
     alignas(16) float x_scale[4][256];  // each epilogue warp's copy of its tile's
@@ -80,7 +74,7 @@ static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
 
 __host__ __device__ constexpr int smem_bytes(int cg, bool int8) {
     return 1024 + kHeaderBytes + stages(cg, int8) * stage_bytes(cg, int8) +
-           kSlots * slot_bytes(cg, int8) + out_bytes(cg, int8);
+           kSlots * slot_bytes(cg, int8) + 2 * kChunkBytes;
 }
 static_assert(smem_bytes(1, true) <= 232448 && smem_bytes(1, false) <= 232448 &&
                   smem_bytes(2, true) <= 232448 && smem_bytes(2, false) <= 232448,
@@ -97,7 +91,7 @@ struct GemmParams {
     int channel_tiles; // of kRows * CG
     int tiles;         // channel tiles * token tiles
     int bn;            // tokens per tile
-    int split;         // CTAs that share K (CG 1)
+    int split;         // CTAs or pairs that share K
     int tma_out;       // rows of out are whole 16-byte units: stored by TMA
     int f32;           // output type
 };
@@ -159,36 +153,152 @@ __device__ __forceinline__ void sts16(uint32_t addr, const uint32_t* v) {
                  : "memory");
 }
 
-__device__ __forceinline__ void store_out(const GemmParams& p, int64_t at, float v) {
-    if (p.f32)
-        static_cast<float*>(p.out)[at] = v;
-    else
-        static_cast<__nv_bfloat16*>(p.out)[at] = __float2bfloat16_rn(v);
+// This warp has read its part of an accumulator: hand it back to the leader.
+__device__ __forceinline__ void release_acc(uint64_t& bar, uint32_t lead, int lane) {
+    tcgen05_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(map_to_rank(smem_addr(&bar), lead));
 }
 
-// y[j] = v[j] * x_scale[j] * ws for sixteen tokens (in this order: the product
-// of two small scales alone could lose its bits as a subnormal).
-__device__ __forceinline__ void scale16(float (&y)[16], const uint32_t (&v)[16],
-                                        const float (&xs)[16], float ws) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(v[j]) * xs[j] * ws;
+// The output's way out where its rows allow: through shared memory as
+// [token][channel] and out by TMA, so that the rows of a chunk leave as whole
+// lines beside the next chunk's reads (stored straight from registers, a
+// column costs each warp about 50 clocks).  Two chunks are in turn; the 128
+// threads of the epilogue fill one and call flush together, which sends it and
+// returns with the other free.
+//   fp32  16 tokens x 128 channels, rows of 512 bytes
+//   bf16  32 tokens x 64 channels twice, rows of 128 bytes in the 128-byte
+//         swizzle (16-byte piece i of token t at piece i ^ (t & 7)), which
+//         keeps the transposing stores below free of bank conflicts
+__device__ __forceinline__ void flush(const GemmParams& p, const CUtensorMap* out_map,
+                                      uint32_t staging, int& chunk, int64_t n, int t0, int c,
+                                      int n_tok, int etid) {
+    fence_async_shared();
+    if (etid == 0) bulk_wait_read<0>();  // the other chunk's store, a chunk ago
+    __syncwarp();
+    named_barrier(1, 128);
+    if (etid == 0) {
+        const uint32_t from = staging + chunk * kChunkBytes;
+        if (c < n_tok && n < p.N) {
+            tma_store_2d(out_map, static_cast<int>(n), t0 + c, from);
+            if (!p.f32 && n + 64 < p.N)
+                tma_store_2d(out_map, static_cast<int>(n) + 64, t0 + c, from + kChunkBytes / 2);
+        }
+        bulk_commit();
+    }
+    __syncwarp();
+    chunk ^= 1;
 }
-__device__ __forceinline__ void load16(float (&y)[16], const float* x) {
+
+// The address in a bf16 chunk of token t's 16-byte piece of channels 8 i to
+// 8 i + 7 (of 128).
+__device__ __forceinline__ uint32_t bf16_piece(uint32_t chunk, int t, int i) {
+    return chunk + (i >> 3) * (kChunkBytes / 2) + t * 128 + (((i & 7) ^ (t & 7)) << 4);
+}
+
+// A whole bf16 tile out by TMA.  A warp's 32 channels x 16 tokens come from
+// TMEM as 8x8 fragments (two channels' worth of registers hold neighbouring
+// tokens), are scaled, packed and stored transposed: 2 stores instead of 16
+// narrow ones, in shared memory that the running products keep busy.
+// ws: the scales of channels lane / 4 + 8 i of the warp.  done() after the last
+// read.
+template <class Done>
+__device__ __forceinline__ void emit_bf16(const GemmParams& p, const CUtensorMap* out_map,
+                                          uint32_t staging, int& chunk, const float* x_scale,
+                                          const float (&ws)[4], int64_t n, int t0, int n_tok,
+                                          uint32_t d, int etid, Done done) {
+    const int lane = etid % 32;
+    for (int c = 0; c < p.bn; c += 32) {
+        const uint32_t to = staging + chunk * kChunkBytes;
 #pragma unroll
-    for (int j = 0; j < 16; j += 4) {
-        const float4 q = *reinterpret_cast<const float4*>(x + j);
-        y[j] = q.x;
-        y[j + 1] = q.y;
-        y[j + 2] = q.z;
-        y[j + 3] = q.w;
+        for (int k = 0; k < 32; k += 16) {
+            uint32_t r[2][8];
+            tmem_load_fragments(r[0], d + c + k);
+            tmem_load_fragments(r[1], d + (16u << 16) + c + k);
+            const float2 xs[2] = {
+                *reinterpret_cast<const float2*>(x_scale + c + k + lane % 4 * 2),
+                *reinterpret_cast<const float2*>(x_scale + c + k + 8 + lane % 4 * 2)};
+            tmem_wait_loads();
+            if (k == 16 && c + 32 >= p.bn) done();
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t m[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // Fragment i: channels 16 q + 8 (i % 2) on, tokens 8 (i / 2) on.
+                    const float w = ws[2 * q + i % 2];
+                    const __nv_bfloat162 two =
+                        __floats2bfloat162_rn(__uint_as_float(r[q][2 * i]) * xs[i / 2].x * w,
+                                              __uint_as_float(r[q][2 * i + 1]) * xs[i / 2].y * w);
+                    m[i] = *reinterpret_cast<const uint32_t*>(&two);
+                }
+                // Lane 8 m + j: token 8 (m / 2) + j, channels 8 (m % 2) on.
+                const int t = k + lane / 16 * 8 + lane % 8;
+                store_matrices_transposed(
+                    bf16_piece(to, t, etid / 32 * 4 + 2 * q + lane / 8 % 2), m[0], m[1], m[2], m[3]);
+            }
+        }
+        flush(p, out_map, staging, chunk, n, t0, c, n_tok, etid);
     }
 }
 
-// This warp has read its part of an accumulator: hand it back to the leader.
-__device__ __forceinline__ void release_acc(uint64_t& bar, int cg, uint32_t rank, int lane) {
-    tcgen05_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_pair(map_to_rank(smem_addr(&bar), cg == 2 ? 0u : rank));
+// Columns (tokens) [c0, c1) of a tile on their way out, W at a time: this
+// thread's channel n of them from read(c, v), scaled (first by the token's
+// scale: the product of two small scales alone could lose bits as a
+// subnormal) and stored; done() after the last read.  The 128 threads of the
+// epilogue call it together.
+template <int W, class Read, class Done>
+__device__ __forceinline__ void emit(const GemmParams& p, const CUtensorMap* out_map,
+                                     uint32_t staging, int& chunk, const float* x_scale, float ws,
+                                     int64_t n, int t0, int n_tok, int c0, int c1, int etid,
+                                     Read read, Done done) {
+    for (int c = c0; c < c1; c += W) {
+        float xs[W], y[W];
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+            const float4 q = *reinterpret_cast<const float4*>(x_scale + c + j);
+            xs[j] = q.x;
+            xs[j + 1] = q.y;
+            xs[j + 2] = q.z;
+            xs[j + 3] = q.w;
+        }
+        read(c, y);
+        if (c + W >= c1) done();
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] = y[j] * xs[j] * ws;
+        if (p.tma_out) {
+            const int per_chunk = p.f32 ? 16 : 32, at = (c - c0) % per_chunk;
+            const uint32_t to = staging + chunk * kChunkBytes;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if (p.f32)
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + ((at + j) * kRows + etid) * 4),
+                                 "f"(y[j])
+                                 : "memory");
+                else
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(
+                                     bf16_piece(to, at + j, etid / 8) + etid % 8 * 2),
+                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(y[j])))
+                                 : "memory");
+            }
+            if (at + W == per_chunk)
+                flush(p, out_map, staging, chunk, n, t0, c + W - per_chunk, n_tok, etid);
+            continue;
+        }
+        const int64_t at = (static_cast<int64_t>(t0) + c) * p.N + n;
+        if (p.f32) {
+            float* out = static_cast<float*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (c + j < n_tok && n < p.N) out[j * p.N] = y[j];
+        } else {
+            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+            for (int j = 0; j < W; ++j)
+                if (c + j < n_tok && n < p.N) out[j * p.N] = __float2bfloat16_rn(y[j]);
+        }
+        __syncwarp();
+    }
 }
 
 template <int CG, bool INT8>
@@ -207,22 +317,25 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     Header& h = *reinterpret_cast<Header*>(smem);
     const uint32_t ring = smem_addr(smem) + kHeaderBytes;
     const uint32_t slots = ring + S * kStage;
-    unsigned char* staging = smem + kHeaderBytes + S * kStage + kSlots * kSlot;
+    const uint32_t staging = slots + kSlots * kSlot;
     volatile int* abort = &h.abort;
 
     // A warp index the compiler knows to be the same in all lanes: the MMA
     // warp's operands then live in uniform registers.
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
     const int lane = threadIdx.x % 32;
-    // With CG 2 the cluster is the pair; the even CTA issues its MMAs.  With
-    // CG 1 the cluster's CTAs split K.
+    // The cluster's CTAs (CG 1) or pairs (CG 2) split K: `part` is this one's
+    // share, `half` the CTA of a pair, `lead` the rank that issues its MMAs.
     const uint32_t rank = cluster_cta_rank();
     const uint32_t unit = cluster_id_x(), units = cluster_count_x();
-    const bool leader = CG == 1 || rank == 0;
-    const int split = CG == 1 ? p.split : 1;
-    const int kb0 = CG == 1 ? static_cast<int>(static_cast<int64_t>(p.k_blocks) * rank / split) : 0;
-    const int kb1 = CG == 1 ? static_cast<int>(static_cast<int64_t>(p.k_blocks) * (rank + 1) / split)
-                            : p.k_blocks;
+    const int half = CG == 2 ? static_cast<int>(rank & 1) : 0;
+    const int part = static_cast<int>(rank) / CG;
+    const uint32_t lead = rank - half;
+    const bool leader = half == 0;
+    const uint16_t pair = static_cast<uint16_t>(3u << lead);
+    const int split = p.split;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / split);
+    const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / split);
     const int bn_cta = p.bn / CG;  // token rows this CTA loads
 
     if (threadIdx.x == 0) {
@@ -238,12 +351,14 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             mbar_init(smem_addr(&h.acc_full[b]), 1);
             mbar_init(smem_addr(&h.acc_empty[b]), 4 * CG);
         }
+        mbar_init(smem_addr(&h.open), split);
         mbar_init(smem_addr(&h.joined), 1);
         mbar_init(smem_addr(&h.drained), 1);
         h.abort = 0;
         mbar_init_fence();
         if (split > 1)
-            mbar_arrive_expect_tx(smem_addr(&h.joined), static_cast<uint32_t>(p.bn) * kRows * 4);
+            mbar_arrive_expect_tx(smem_addr(&h.joined), static_cast<uint32_t>(
+                                                            (split - 1) * (p.bn / split) * kRows * 4));
         tensormap_prefetch(&x_map);
         tensormap_prefetch(&w_map);
     }
@@ -265,9 +380,9 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         const uint32_t bytes = static_cast<uint32_t>((kRows + bn_cta) * kBlockK);
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles); tile += units) {
             const int channel = static_cast<int>(tile % p.channel_tiles) * (kRows * CG) +
-                                (CG == 2 ? static_cast<int>(rank) * kRows : 0);
+                                half * kRows;
             const int token = static_cast<int>(tile / p.channel_tiles) * p.bn +
-                              (CG == 2 ? static_cast<int>(rank) * bn_cta : 0);
+                              half * bn_cta;
             for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(S)) {
                 if (!mbar_wait_slice(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
                     gave_up(p, abort);
@@ -278,7 +393,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                 // which alone issues the products; int8: on this CTA's, whose
                 // warps widen them.
                 const uint32_t local = smem_addr(&h.full[r.at]);
-                const uint32_t bar = CG == 2 && !INT8 ? map_to_rank(local, 0) : local;
+                const uint32_t bar = CG == 2 && !INT8 ? map_to_rank(local, lead) : local;
                 if (INT8 || leader) mbar_arrive_expect_tx(local, INT8 ? bytes : bytes * CG);
                 const uint32_t dst = ring + r.at * kStage;
                 tma_load_2d<INT8 ? 1 : CG>(dst, &w_map, kb * kBlockK, channel, bar);
@@ -333,7 +448,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
 #pragma unroll
                         for (int i = 0; i < kUnitK / 16; ++i)
                             mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape, k > 0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.wide_empty[at]));
+                        mma_commit<CG>(smem_addr(&h.wide_empty[at]), pair);
                     }
                     __syncwarp();
                     there = __all_sync(0xffffffffu, there);
@@ -353,18 +468,18 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
 #pragma unroll
                         for (int i = 0; i < kBlockK / 32; ++i)
                             mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.empty[at]));
+                        mma_commit<CG>(smem_addr(&h.empty[at]), pair);
                     }
                     __syncwarp();
                     there = __all_sync(0xffffffffu, there);
                 }
             }
-            if (ok && elect_one()) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]));
+            if (ok && elect_one()) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]), pair);
             __syncwarp();
         }
         if (!ok) {
             // Products in flight still read shared memory and write TMEM.
-            if (elect_one()) mma_commit<CG>(smem_addr(&h.drained));
+            if (elect_one()) mma_commit<CG>(smem_addr(&h.drained), pair);
             if (!mbar_wait_slice(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
         }
     } else if (warp >= kEpilogueWarp && warp < kEpilogueWarp + 4) {
@@ -379,7 +494,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         for (uint32_t tile = unit; tile < static_cast<uint32_t>(p.tiles);
              tile += units, acc.next(2)) {
             const int64_t n = static_cast<int64_t>(tile % p.channel_tiles) * (kRows * CG) +
-                              (CG == 2 ? rank * kRows : 0) + etid;
+                              half * kRows + etid;
             const int t0 = static_cast<int>(tile / p.channel_tiles) * p.bn;
             // Every load of the tile's scales in flight at once.
             const float ws = n < p.N ? p.w_scale[n] : 0.f;
@@ -400,103 +515,87 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * kAcc + lanes;
             const int n_tok = p.M - t0 < p.bn ? p.M - t0 : p.bn;
-            if (CG == 1 && split > 1) {
-                // Push every CTA's columns to it, then add up this CTA's: four
-                // columns of a channel travel as 16 bytes, [source][column /
-                // 4][channel].
-                const int own = p.bn / split;  // a multiple of 4
-                const uint32_t local = smem_addr(staging) +
-                                       (static_cast<uint32_t>(rank) * (own / 4) * kRows + etid) * 16;
-                const uint32_t bar = smem_addr(&h.joined);
-                int to = 0, at = 0;
-                for (int c = 0; c < p.bn; c += 16) {
-                    uint32_t v[16];
-                    tmem_load16(v, d + c);
-                    tmem_wait_loads();
+            const auto hand_back = [&]() { release_acc(h.acc_empty[acc.at], lead, lane); };
+            if (split == 1 && p.tma_out && !p.f32) {
+                float w[4];
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        st_async4(map_to_rank(local + at * (kRows * 4), to), v + j,
-                                  map_to_rank(bar, to));
-                        at += 4;
-                        if (at == own) {
-                            at = 0;
-                            ++to;
-                        }
-                    }
-                }
-                if (!warp_wait<true>(p, &h.joined, 0, abort)) break;
-                const float4* part = reinterpret_cast<const float4*>(staging) + etid;
-                for (int j = 0; j < own; j += 4) {
-                    float4 sum = part[j / 4 * kRows];
-                    for (int s = 1; s < split; ++s) {
-                        const float4 q = part[(s * own + j) / 4 * kRows];
-                        sum.x += q.x;
-                        sum.y += q.y;
-                        sum.z += q.z;
-                        sum.w += q.w;
-                    }
-                    const int c = static_cast<int>(rank) * own + j;
-                    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (c + i < n_tok && n < p.N)
-                            store_out(p, (static_cast<int64_t>(t0) + c + i) * p.N + n,
-                                      v[i] * x_scale[c + i] * ws);
-                }
-                break;  // one tile per cluster
-            }
-            if (p.tma_out) {
-                // Through shared memory, [token][channel], and out by TMA: the
-                // rows of a chunk leave as whole 256- or 512-byte lines beside
-                // the next chunk's loads.
-                const int per_chunk = p.f32 ? 16 : 32;
-                for (int c = 0; c < p.bn; c += per_chunk, chunk ^= 1) {
-                    unsigned char* to = staging + chunk * kChunkBytes;
-                    if (etid == 0) bulk_wait_read<1>();
-                    named_barrier(1, 128);
-                    for (int k = 0; k < per_chunk; k += 16) {
-                        uint32_t v[16];
-                        tmem_load16(v, d + c + k);
-                        float xs16[16], y[16];
-                        load16(xs16, x_scale + c + k);
-                        tmem_wait_loads();
-                        scale16(y, v, xs16, ws);
-                        if (p.f32) {
-                            float* row = reinterpret_cast<float*>(to) + etid;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) row[j * kRows] = y[j];
-                        } else {
-                            __nv_bfloat16* row =
-                                reinterpret_cast<__nv_bfloat16*>(to) + k * kRows + etid;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) row[j * kRows] = __float2bfloat16_rn(y[j]);
-                        }
-                    }
-                    if (c + per_chunk >= p.bn) release_acc(h.acc_empty[acc.at], CG, rank, lane);
-                    fence_async_shared();
-                    named_barrier(1, 128);
-                    if (etid == 0) {
-                        if (c < n_tok && n < p.N)
-                            tma_store_2d(&out_map, static_cast<int>(n), t0 + c, smem_addr(to));
-                        bulk_commit();
-                    }
-                }
+                for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, ws, lane / 4 + 8 * i);
+                emit_bf16(p, &out_map, staging, chunk, x_scale, w, n, t0, n_tok, d, etid,
+                          hand_back);
                 continue;
             }
-            for (int c = 0; c < p.bn; c += 16) {
-                uint32_t v[16];
-                tmem_load16(v, d + c);
-                float xs16[16], y[16];
-                load16(xs16, x_scale + c);
-                tmem_wait_loads();
-                scale16(y, v, xs16, ws);
-                if (c + 16 >= p.bn) release_acc(h.acc_empty[acc.at], CG, rank, lane);
+            if (split == 1) {
+                emit<16>(
+                    p, &out_map, staging, chunk, x_scale, ws, n, t0, n_tok, 0, p.bn, etid,
+                    [&](int c, float (&v)[16]) {
+                        uint32_t r[16];
+                        tmem_load16(r, d + c);
+                        tmem_wait_loads();
 #pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (c + j < n_tok && n < p.N)
-                        store_out(p, (static_cast<int64_t>(t0) + c + j) * p.N + n, y[j]);
-                __syncwarp();
+                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                    },
+                    hand_back);
+                continue;
             }
+            // Split K: unit q of the cluster adds up columns [q own, (q + 1)
+            // own).  The others' columns go to shared memory, four columns of
+            // a channel as 16 bytes ([q][column / 4][channel]), and from there
+            // as one bulk copy each into the ring of the unit they belong to,
+            // once its products are done as well (it says so on `open`).
+            const int own = p.bn / split;  // a multiple of 8
+            const uint32_t block = static_cast<uint32_t>(own * kRows * 4);
+            const uint32_t outgoing = ring, incoming = ring + split * block;
+            if (etid < split)
+                mbar_arrive_cluster(map_to_rank(smem_addr(&h.open),
+                                                static_cast<uint32_t>(etid * CG + half)));
+            for (int c = 0; c < p.bn; c += 8) {
+                if (c / own == part) continue;
+                uint32_t v[8];
+                tmem_load8(v, d + c);
+                tmem_wait_loads();
+                sts16(outgoing + (c / 4 * kRows + etid) * 16, v);
+                sts16(outgoing + ((c / 4 + 1) * kRows + etid) * 16, v + 4);
+            }
+            fence_async_shared();
+            named_barrier(1, 128);
+            if (etid == 0) {
+                if (!mbar_wait_slice<true>(smem_addr(&h.open), 0, abort)) {
+                    gave_up(p, abort);
+                } else {
+                    for (int q = 0; q < split; ++q) {
+                        if (q == part) continue;
+                        const uint32_t dest = static_cast<uint32_t>(q * CG + half);
+                        bulk_push(map_to_rank(incoming + part * block, dest), outgoing + q * block,
+                                  block, map_to_rank(smem_addr(&h.joined), dest));
+                    }
+                }
+            }
+            __syncwarp();
+            const bool in = warp_wait<true>(p, &h.joined, 0, abort);
+            if (named_barrier_or(1, 128, !in)) break;
+            emit<8>(
+                p, &out_map, staging, chunk, x_scale, ws, n, t0, n_tok, part * own,
+                (part + 1) * own, etid,
+                [&](int c, float (&v)[8]) {
+                    uint32_t r[8];
+                    tmem_load8(r, d + c);
+                    tmem_wait_loads();
+                    const uint32_t at = incoming + ((c - part * own) / 4 * kRows + etid) * 16;
+                    for (int q = 0; q < split; ++q) {
+                        uint4 lo = make_uint4(r[0], r[1], r[2], r[3]);
+                        uint4 hi = make_uint4(r[4], r[5], r[6], r[7]);
+                        if (q != part) {
+                            lo = lds16(at + q * block);
+                            hi = lds16(at + q * block + kRows * 16);
+                        }
+                        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            v[j] = q == 0 ? __uint_as_float(w[j]) : v[j] + __uint_as_float(w[j]);
+                    }
+                },
+                []() {});
+            break;  // one tile per cluster
         }
         if (etid == 0) bulk_wait_read<0>();
     } else if (INT8 && warp >= kWidenWarp) {
@@ -519,7 +618,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         for (int i = 0; i < group; ++i) c.next(kSlots);
         for (int i = 0; i < group / 2; ++i) r.next(S);
         for (int64_t u = group; u < n_units; u += kGroups) {
-            const int half = static_cast<int>(u) & 1;
+            const int upper = static_cast<int>(u) & 1;
             if (!warp_wait(p, &h.full[r.at], r.phase, abort)) break;
             const uint32_t stage = ring + r.at * kStage;
             // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
@@ -528,12 +627,12 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             uint4 raw[4 + kTokenChunks];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                raw[i] = lds16(stage + row * kBlockK + (((half * 4 + i) ^ (row & 7)) << 4));
+                raw[i] = lds16(stage + row * kBlockK + (((upper * 4 + i) ^ (row & 7)) << 4));
 #pragma unroll
             for (int i = 0; i < kTokenChunks; ++i)
                 if (i * 32 + x_row0 < bn_cta)
                     raw[4 + i] = lds16(stage + kRows * kBlockK + (i * 32 + x_row) * kBlockK +
-                                       (((half * 4 + x_chunk) ^ (x_row & 7)) << 4));
+                                       (((upper * 4 + x_chunk) ^ (x_row & 7)) << 4));
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) widen16(raw[i], w + 8 * i);
@@ -557,8 +656,8 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             tcgen05_fence_before();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive_pair(map_to_rank(smem_addr(&h.wide_full[c.at]), CG == 2 ? 0u : rank));
-            const int step = (half + kGroups) / 2;  // stages on to unit u + kGroups
+                mbar_arrive_pair(map_to_rank(smem_addr(&h.wide_full[c.at]), lead));
+            const int step = (upper + kGroups) / 2;  // stages on to unit u + kGroups
             for (int i = 0; i < step; ++i) r.next(S);
             for (int i = 0; i < kGroups; ++i) c.next(kSlots);
         }
@@ -584,6 +683,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;
+int g_clusters[2][2][4];  // [CG - 1][int8][log2 of the cluster]
 
 // A dense [rows, columns] tensor moved in boxes of box_columns x box_rows; what
 // lies outside reads as zeros (0 in every type).
@@ -613,6 +713,65 @@ void* gemm_kernel_for(int cg, bool int8) {
                 : reinterpret_cast<void*>(&gemm_kernel<2, false>);
 }
 
+// Launch configuration of `grid` CTAs in clusters; attr[0] is the cluster's.
+void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int cluster, int grid,
+                    int cg, bool int8) {
+    cfg->gridDim = dim3(static_cast<unsigned>(grid));
+    cfg->blockDim = dim3(int8 ? 256 + 128 * kGroups : 256);
+    cfg->dynamicSmemBytes = smem_bytes(cg, int8);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg->attrs = attr;
+}
+
+// How a call is cut up.
+struct Plan {
+    int cg = 0, split = 1, bn = 0;
+    int64_t token_tiles = 0, tiles = 0;
+    double cost = 0;
+};
+
+// The cheapest of the cuts a call allows, by the time (in clocks) its busiest
+// unit takes.  Per ring stage: a pair's two operands' MMAs bound e4m3 (2 bn,
+// measured 520 at bn = 256), what widening W costs and the hand-over of its
+// slots int8 (870 at 128, 1000 at 192); a lone CTA's stages cost about the same
+// at its short tiles.  Then the start (barriers, TMEM, the first bytes), the
+// last tile's way out, and with split K the join.
+Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
+    Plan best;
+    for (int cg = 1; cg <= 2; ++cg) {
+        const int most_bn = max_tokens(cg, int8);
+        const int64_t channel_tiles = (N + kRows * cg - 1) / (kRows * cg);
+        for (int bn = cg == 1 ? 16 : 32; bn <= most_bn; bn += bn < 32 ? 16 : 32) {
+            if (bn >= M + 32 && bn > 32) break;
+            Plan c;
+            c.cg = cg;
+            c.bn = bn;
+            c.token_tiles = (M + bn - 1) / bn;
+            c.tiles = channel_tiles * c.token_tiles;
+            const double stage = int8 ? 600.0 + 2.0 * bn + (cg == 1 ? 2.0 * bn : 0.0)
+                                      : (cg == 2 ? 350.0 + 0.67 * bn : 400.0 + 1.5 * bn);
+            for (int split = 1, log2 = cg - 1; log2 < 4 && split <= k_blocks; split *= 2, ++log2) {
+                int64_t units = sms >> log2;
+                if (units > g_clusters[cg - 1][int8][log2]) units = g_clusters[cg - 1][int8][log2];
+                if (units < 1 || (split > 1 && c.tiles > units)) break;
+                // Whole chunks of the output's staging, or eights of a share.
+                if (bn % (split == 1 ? 32 : 8 * split) != 0) continue;
+                // A join holds its tile twice in the ring.
+                if (split > 1 && bn * kRows * 8 > stages(cg, int8) * stage_bytes(cg, int8)) break;
+                const int64_t waves = (c.tiles + units - 1) / units;
+                c.split = split;
+                c.cost = static_cast<double>(waves * ((k_blocks + split - 1) / split)) * stage +
+                         14.0 * bn + (split > 1 ? 2000.0 + 50.0 * bn / split : 0.0);
+                if (best.cg == 0 || c.cost < best.cost) best = c;
+            }
+        }
+    }
+    return best;
+}
+
 }  // namespace
 
 int gemm_prepare(int smem_optin) {
@@ -623,6 +782,18 @@ int gemm_prepare(int smem_optin) {
                                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  smem_bytes(cg, int8));
             if (e != cudaSuccess) return static_cast<int>(e);
+            // Clusters of 1, 2, 4 and 8 CTAs that run at once (they do not
+            // cross a GPC, so a few SMs can be out of reach).
+            for (int i = 0; i < 4; ++i) {
+                cudaLaunchConfig_t cfg = {};
+                cudaLaunchAttribute attr[1];
+                cluster_config(&cfg, attr, 1 << i, 1 << i, cg, int8);
+                cfg.numAttrs = 1;
+                int n = 0;
+                e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel_for(cg, int8), &cfg);
+                if (e != cudaSuccess) return static_cast<int>(e);
+                g_clusters[cg - 1][int8][i] = n;
+            }
         }
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -638,9 +809,6 @@ int gemm_prepare(int smem_optin) {
 int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream) {
     const bool int8 = g.qtype == TW_INT8;
     const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
-    const int cg = g.M <= max_tokens(1, int8) || sms < 2 ? 1 : 2;
-    const int64_t token_tiles = (g.M + max_tokens(cg, int8) - 1) / max_tokens(cg, int8);
-    const int64_t per_tile = (g.M + token_tiles - 1) / token_tiles;
     GemmParams p{};
     p.x_scale = g.x_scale;
     p.w_scale = g.w_scale;
@@ -650,47 +818,36 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.M = static_cast<int>(g.M);
     p.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
     p.f32 = g.dtype == TW_F32;
-    const int64_t channel_tiles = (g.N + kRows * cg - 1) / (kRows * cg);
-    const int64_t tiles = channel_tiles * token_tiles;
-    if (tiles > (int64_t{1} << 31) - 1 - sms) return static_cast<int>(cudaErrorInvalidValue);
-    p.channel_tiles = static_cast<int>(channel_tiles);
-    p.tiles = static_cast<int>(tiles);
-    p.split = 1;
-    if (cg == 1)
-        while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.split * 2 <= p.k_blocks)
-            p.split *= 2;
-    // Whole chunks of the output's staging, or of each CTA's share of the
-    // columns (never above max_tokens, a multiple of both).
-    const int align = p.split > 1 ? (p.split > 4 ? 4 * p.split : 16) : 32;
-    p.bn = static_cast<int>((per_tile + align - 1) / align * align);
+    const Plan c = plan(g.M, g.N, p.k_blocks, int8, sms);
+    if (c.cg == 0 || c.tiles > (int64_t{1} << 31) - 1 - sms)
+        return static_cast<int>(cudaErrorInvalidValue);
+    const int cg = c.cg;
+    p.tiles = static_cast<int>(c.tiles);
+    p.channel_tiles = static_cast<int>(c.tiles / c.token_tiles);
+    p.split = c.split;
+    p.bn = c.bn;
     const int64_t es = p.f32 ? 4 : 2;
-    p.tma_out = p.split == 1 && g.N * es % 16 == 0;
+    p.tma_out = g.N * es % 16 == 0 && p.bn / p.split % (p.f32 ? 16 : 32) == 0;
     CUtensorMap x_map, w_map, out_map{};
     if (!encode_operand(&x_map, g.x, g.M, g.K, p.bn / cg) ||
         !encode_operand(&w_map, g.w, g.N, g.K, kRows) ||
         (p.tma_out && !encode(&out_map,
                               p.f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                              es, g.out, g.M, g.N, kRows, p.f32 ? 16 : 32,
-                              CU_TENSOR_MAP_SWIZZLE_NONE)))
+                              es, g.out, g.M, g.N, p.f32 ? kRows : kRows / 2, p.f32 ? 16 : 32,
+                              p.f32 ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                    : CU_TENSOR_MAP_SWIZZLE_128B)))
         return static_cast<int>(cudaErrorInvalidValue);
 
-    const int cluster = cg == 1 ? p.split : 2;
+    const int cluster = cg * p.split;
     const int64_t most = sms / cluster;
-    const int64_t units = tiles < most ? tiles : most;
+    const int64_t units = c.tiles < most ? c.tiles : most;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units * cluster));
-    cfg.blockDim = dim3(int8 ? 256 + 128 * kGroups : 256);
-    cfg.dynamicSmemBytes = smem_bytes(cg, int8);
-    cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
+    cluster_config(&cfg, attr, cluster, static_cast<int>(units * cluster), cg, int8);
+    cfg.stream = static_cast<cudaStream_t>(stream);
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = max_sms >= d.sm_count ? 2 : 1;
     void* args[] = {&x_map, &w_map, &out_map, &p};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8), args));

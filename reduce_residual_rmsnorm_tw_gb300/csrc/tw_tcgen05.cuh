@@ -37,6 +37,12 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
     return remote;
 }
+// Arrive on a barrier of another CTA of the cluster, everything this thread
+// has done or seen before it.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
+                 : "memory");
+}
 // Arrive on a barrier of a CTA of the pair for work that stays in this CTA:
 // its own shared-memory writes (already ordered for the async proxy by
 // fence_async_shared) and TMEM accesses (complete, behind
@@ -90,13 +96,15 @@ __device__ __forceinline__ bool mbar_wait_slice(uint32_t bar, uint32_t parity,
         }
     }
 }
-// Four floats into another CTA's shared memory; they count 16 bytes on its
-// barrier `bar` (both shared::cluster addresses) when they have landed.
-__device__ __forceinline__ void st_async4(uint32_t remote, const uint32_t* v, uint32_t bar) {
+// `bytes` (a multiple of 16) of this CTA's shared memory to another's, counted
+// on that CTA's barrier `bar` when they have landed (remote, bar:
+// shared::cluster addresses).
+__device__ __forceinline__ void bulk_push(uint32_t remote, uint32_t local, uint32_t bytes,
+                                          uint32_t bar) {
     asm volatile(
-        "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 "
-        "[%0], {%1, %2, %3, %4}, [%5];" ::"r"(remote),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(bar)
+        "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes "
+        "[%0], [%1], %2, [%3];" ::"r"(remote),
+        "r"(local), "r"(bytes), "r"(bar)
         : "memory");
 }
 // Order this thread's shared-memory writes before later async-proxy reads
@@ -208,6 +216,34 @@ __device__ __forceinline__ void tmem_load16(uint32_t (&r)[16], uint32_t addr) {
         : "r"(addr)
         : "memory");
 }
+__device__ __forceinline__ void tmem_load8(uint32_t (&r)[8], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+// 16 columns of 16 lanes as 8x8 fragments: registers 4 i, 4 i + 1 of thread t
+// hold columns 8 i + 2 (t % 4) and the next of lane t / 4, registers 4 i + 2
+// and 4 i + 3 those of lane t / 4 + 8.
+__device__ __forceinline__ void tmem_load_fragments(uint32_t (&r)[8], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7])
+        : "r"(addr)
+        : "memory");
+}
+// Four 8x8 matrices of 16-bit values, transposed: column i of matrix m to the
+// 16 bytes at the address that lane 8 m + i gives.
+__device__ __forceinline__ void store_matrices_transposed(uint32_t addr, uint32_t m0, uint32_t m1,
+                                                          uint32_t m2, uint32_t m3) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(
+                     addr),
+                 "r"(m0), "r"(m1), "r"(m2), "r"(m3)
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
@@ -270,9 +306,10 @@ __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uin
             : "memory");
 }
 // Arrive on `bar` (CG 2: on the barrier at that offset in both CTAs of the
-// pair) once this thread's MMAs so far are complete.
+// pair, the bits of `pair` being their ranks) once this thread's MMAs so far
+// are complete.
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t pair) {
     if constexpr (CG == 1)
         asm volatile(
             "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -282,7 +319,7 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
             ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(static_cast<uint16_t>(3))
+            "h"(pair)
             : "memory");
 }
 
