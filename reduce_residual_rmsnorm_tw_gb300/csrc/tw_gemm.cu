@@ -39,10 +39,10 @@ constexpr int kSlotColumns = kUnitK / 2;
 constexpr int kMaxStages = 8;
 constexpr int kTmemColumns = 512;
 
-// Warp roles: 0 TMA, 1 MMA, 4-7 epilogue, from 8 on kGroups of four widen
-// (int8).
+// Warp roles: 0 TMA, 1 MMA, 2 (split K) tells the cluster that the products are
+// done, 4-7 epilogue, from 8 on kGroups of four widen (int8).
 constexpr int kGroups = 4;
-constexpr int kEpilogueWarp = 4, kWidenWarp = 8;
+constexpr int kAnnounceWarp = 2, kEpilogueWarp = 4, kWidenWarp = 8;
 
 // Largest token tile: one unit's two accumulators (and, for int8, the widened
 // W) share 512 TMEM columns; a single CTA takes short tiles only.
@@ -160,6 +160,84 @@ __device__ __forceinline__ void release_acc(uint64_t& bar, uint32_t lead, int la
     if (lane == 0) mbar_arrive_pair(map_to_rank(smem_addr(&bar), lead));
 }
 
+// ------------------------------------------------------------- epilogue ---
+// W columns (tokens) of a thread's share of an accumulator, as W registers:
+//   lanes      column c + j of the thread's channel (TMEM lane)
+//   fragments  (W = 16) 8x8 fragments of the warp's 32 channels x 16 columns:
+//              registers 8 q + 4 i + 2 r + e of lane l hold channel
+//              16 q + 8 r + l / 4, column c + 8 i + 2 (l % 4) + e
+template <int W, bool FRAGMENTS>
+__device__ __forceinline__ void read_acc(uint32_t (&v)[W], uint32_t d, int c) {
+    if constexpr (FRAGMENTS) {
+        tmem_load_fragments(reinterpret_cast<uint32_t(&)[8]>(v[0]), d + c);
+        tmem_load_fragments(reinterpret_cast<uint32_t(&)[8]>(v[8]), d + (16u << 16) + c);
+    } else if constexpr (W == 16) {
+        tmem_load16(v, d + c);
+    } else {
+        tmem_load8(v, d + c);
+    }
+    tmem_wait_loads();
+}
+
+// Split K: unit q of the cluster adds up columns [q own, (q + 1) own).  The
+// others' registers for them go to shared memory as they are (16 bytes of each
+// of the 128 threads in turn), and from there as one bulk copy each into the
+// ring of the unit they belong to.
+struct Join {
+    uint32_t outgoing, incoming, block;  // shared memory; bytes of one share
+    int part, split, own;
+};
+
+template <int W, bool FRAGMENTS>
+__device__ __forceinline__ void send_columns(const Join& g, uint32_t d, int etid) {
+    for (int q = 0; q < g.split; ++q) {
+        if (q == g.part) continue;
+        uint32_t to = g.outgoing + q * g.block + etid * 16;
+        for (int c = q * g.own; c < (q + 1) * g.own; c += W, to += W * kRows * 4) {
+            uint32_t v[W];
+            read_acc<W, FRAGMENTS>(v, d, c);
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) sts16(to + i * kRows * 16, v + 4 * i);
+        }
+    }
+}
+
+// The sum over the cluster (in rank order) of columns c to c + W - 1.
+template <int W, bool FRAGMENTS, bool SPLIT>
+__device__ __forceinline__ void read_columns(float (&y)[W], const Join& g, uint32_t d, int c,
+                                             int etid) {
+    uint32_t v[W];
+    read_acc<W, FRAGMENTS>(v, d, c);
+    if constexpr (SPLIT) {
+        const uint32_t from = g.incoming + (c - g.part * g.own) * (kRows * 4) + etid * 16;
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] = 0.f;
+        for (int q = 0; q < g.split; ++q) {
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                const uint4 w = q == g.part
+                                    ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
+                                    : lds16(from + q * g.block + i * kRows * 16);
+                y[4 * i] += __uint_as_float(w.x);
+                y[4 * i + 1] += __uint_as_float(w.y);
+                y[4 * i + 2] += __uint_as_float(w.z);
+                y[4 * i + 3] += __uint_as_float(w.w);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < W; ++j) y[j] = __uint_as_float(v[j]);
+    }
+}
+
+// What an epilogue thread knows of its tile: its channel, the tile's first
+// token and its tokens inside the call, the token scales (shared memory).
+struct Tile {
+    int64_t n;
+    int t0, n_tok, etid;
+    const float* x_scale;
+};
+
 // The output's way out where its rows allow: through shared memory as
 // [token][channel] and out by TMA, so that the rows of a chunk leave as whole
 // lines beside the next chunk's reads (stored straight from registers, a
@@ -171,18 +249,17 @@ __device__ __forceinline__ void release_acc(uint64_t& bar, uint32_t lead, int la
 //         swizzle (16-byte piece i of token t at piece i ^ (t & 7)), which
 //         keeps the transposing stores below free of bank conflicts
 __device__ __forceinline__ void flush(const GemmParams& p, const CUtensorMap* out_map,
-                                      uint32_t staging, int& chunk, int64_t n, int t0, int c,
-                                      int n_tok, int etid) {
+                                      uint32_t staging, int& chunk, const Tile& t, int c) {
     fence_async_shared();
-    if (etid == 0) bulk_wait_read<0>();  // the other chunk's store, a chunk ago
+    if (t.etid == 0) bulk_wait_read<0>();  // the other chunk's store, a chunk ago
     __syncwarp();
     named_barrier(1, 128);
-    if (etid == 0) {
+    if (t.etid == 0) {
         const uint32_t from = staging + chunk * kChunkBytes;
-        if (c < n_tok && n < p.N) {
-            tma_store_2d(out_map, static_cast<int>(n), t0 + c, from);
-            if (!p.f32 && n + 64 < p.N)
-                tma_store_2d(out_map, static_cast<int>(n) + 64, t0 + c, from + kChunkBytes / 2);
+        if (c < t.n_tok && t.n < p.N) {
+            tma_store_2d(out_map, static_cast<int>(t.n), t.t0 + c, from);
+            if (!p.f32 && t.n + 64 < p.N)
+                tma_store_2d(out_map, static_cast<int>(t.n) + 64, t.t0 + c, from + kChunkBytes / 2);
         }
         bulk_commit();
     }
@@ -190,118 +267,112 @@ __device__ __forceinline__ void flush(const GemmParams& p, const CUtensorMap* ou
     chunk ^= 1;
 }
 
-// The address in a bf16 chunk of token t's 16-byte piece of channels 8 i to
-// 8 i + 7 (of 128).
-__device__ __forceinline__ uint32_t bf16_piece(uint32_t chunk, int t, int i) {
-    return chunk + (i >> 3) * (kChunkBytes / 2) + t * 128 + (((i & 7) ^ (t & 7)) << 4);
-}
-
-// A whole bf16 tile out by TMA.  A warp's 32 channels x 16 tokens come from
-// TMEM as 8x8 fragments (two channels' worth of registers hold neighbouring
-// tokens), are scaled, packed and stored transposed: 2 stores instead of 16
-// narrow ones, in shared memory that the running products keep busy.
-// ws: the scales of channels lane / 4 + 8 i of the warp.  done() after the last
-// read.
-template <class Done>
+// Every value is scaled first by its token's scale, then by its channel's (the
+// product of two small scales alone could lose bits as a subnormal).
+//
+// bf16: a warp's fragments are scaled, packed (a register pair holds
+// neighbouring tokens of a channel) and stored transposed: 2 stores per 16
+// tokens instead of 16 narrow ones, in shared memory that the running products
+// keep busy.  ws: the scales of the warp's channels lane / 4 + 8 i.
+template <bool SPLIT, class Done>
 __device__ __forceinline__ void emit_bf16(const GemmParams& p, const CUtensorMap* out_map,
-                                          uint32_t staging, int& chunk, const float* x_scale,
-                                          const float (&ws)[4], int64_t n, int t0, int n_tok,
-                                          uint32_t d, int etid, Done done) {
-    const int lane = etid % 32;
-    for (int c = 0; c < p.bn; c += 32) {
+                                          uint32_t staging, int& chunk, const Tile& t,
+                                          const float (&ws)[4], const Join& g, uint32_t d, int c0,
+                                          int c1, Done done) {
+    const int lane = t.etid % 32;
+    for (int c = c0; c < c1; c += 32) {
         const uint32_t to = staging + chunk * kChunkBytes;
 #pragma unroll
         for (int k = 0; k < 32; k += 16) {
-            uint32_t r[2][8];
-            tmem_load_fragments(r[0], d + c + k);
-            tmem_load_fragments(r[1], d + (16u << 16) + c + k);
+            float y[16];
+            read_columns<16, true, SPLIT>(y, g, d, c + k, t.etid);
             const float2 xs[2] = {
-                *reinterpret_cast<const float2*>(x_scale + c + k + lane % 4 * 2),
-                *reinterpret_cast<const float2*>(x_scale + c + k + 8 + lane % 4 * 2)};
-            tmem_wait_loads();
-            if (k == 16 && c + 32 >= p.bn) done();
+                *reinterpret_cast<const float2*>(t.x_scale + c + k + lane % 4 * 2),
+                *reinterpret_cast<const float2*>(t.x_scale + c + k + 8 + lane % 4 * 2)};
+            if (k == 16 && c + 32 >= c1) done();
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 uint32_t m[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // Fragment i: channels 16 q + 8 (i % 2) on, tokens 8 (i / 2) on.
+                    // Matrix i: channels 16 q + 8 (i % 2) on, tokens 8 (i / 2) on.
                     const float w = ws[2 * q + i % 2];
                     const __nv_bfloat162 two =
-                        __floats2bfloat162_rn(__uint_as_float(r[q][2 * i]) * xs[i / 2].x * w,
-                                              __uint_as_float(r[q][2 * i + 1]) * xs[i / 2].y * w);
+                        __floats2bfloat162_rn(y[8 * q + 2 * i] * xs[i / 2].x * w,
+                                              y[8 * q + 2 * i + 1] * xs[i / 2].y * w);
                     m[i] = *reinterpret_cast<const uint32_t*>(&two);
                 }
-                // Lane 8 m + j: token 8 (m / 2) + j, channels 8 (m % 2) on.
-                const int t = k + lane / 16 * 8 + lane % 8;
-                store_matrices_transposed(
-                    bf16_piece(to, t, etid / 32 * 4 + 2 * q + lane / 8 % 2), m[0], m[1], m[2], m[3]);
+                // Lane 8 m + j gives the place of matrix m's token j.
+                const int row = k + lane / 16 * 8 + lane % 8;
+                const int piece = t.etid / 32 * 4 + 2 * q + lane / 8 % 2;
+                store_matrices_transposed(to + (piece >> 3) * (kChunkBytes / 2) + row * 128 +
+                                              (((piece & 7) ^ (row & 7)) << 4),
+                                          m[0], m[1], m[2], m[3]);
             }
         }
-        flush(p, out_map, staging, chunk, n, t0, c, n_tok, etid);
+        flush(p, out_map, staging, chunk, t, c);
     }
 }
 
-// Columns (tokens) [c0, c1) of a tile on their way out, W at a time: this
-// thread's channel n of them from read(c, v), scaled (first by the token's
-// scale: the product of two small scales alone could lose bits as a
-// subnormal) and stored; done() after the last read.  The 128 threads of the
-// epilogue call it together.
-template <int W, class Read, class Done>
-__device__ __forceinline__ void emit(const GemmParams& p, const CUtensorMap* out_map,
-                                     uint32_t staging, int& chunk, const float* x_scale, float ws,
-                                     int64_t n, int t0, int n_tok, int c0, int c1, int etid,
-                                     Read read, Done done) {
+// y[j] = v[j] * token scale * channel scale for this thread's channel.
+template <int W>
+__device__ __forceinline__ void scale_columns(float (&y)[W], const float* x_scale, float ws) {
+#pragma unroll
+    for (int j = 0; j < W; j += 4) {
+        const float4 xs = *reinterpret_cast<const float4*>(x_scale + j);
+        y[j] = y[j] * xs.x * ws;
+        y[j + 1] = y[j + 1] * xs.y * ws;
+        y[j + 2] = y[j + 2] * xs.z * ws;
+        y[j + 3] = y[j + 3] * xs.w * ws;
+    }
+}
+
+template <bool SPLIT, class Done>
+__device__ __forceinline__ void emit_f32(const GemmParams& p, const CUtensorMap* out_map,
+                                         uint32_t staging, int& chunk, const Tile& t, float ws,
+                                         const Join& g, uint32_t d, int c0, int c1, Done done) {
+    for (int c = c0; c < c1; c += 16) {
+        float y[16];
+        read_columns<16, false, SPLIT>(y, g, d, c, t.etid);
+        if (c + 16 >= c1) done();
+        scale_columns(y, t.x_scale + c, ws);
+        const uint32_t to = staging + chunk * kChunkBytes + t.etid * 4;
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + j * kRows * 4), "f"(y[j]) : "memory");
+        flush(p, out_map, staging, chunk, t, c);
+    }
+}
+
+// Rows of out that are not whole 16-byte units, or shares too short for a
+// chunk: straight from registers.
+template <int W, bool SPLIT, class Done>
+__device__ __forceinline__ void emit_direct(const GemmParams& p, const Tile& t, float ws,
+                                            const Join& g, uint32_t d, int c0, int c1, Done done) {
     for (int c = c0; c < c1; c += W) {
-        float xs[W], y[W];
-#pragma unroll
-        for (int j = 0; j < W; j += 4) {
-            const float4 q = *reinterpret_cast<const float4*>(x_scale + c + j);
-            xs[j] = q.x;
-            xs[j + 1] = q.y;
-            xs[j + 2] = q.z;
-            xs[j + 3] = q.w;
-        }
-        read(c, y);
+        float y[W];
+        read_columns<W, false, SPLIT>(y, g, d, c, t.etid);
         if (c + W >= c1) done();
-#pragma unroll
-        for (int j = 0; j < W; ++j) y[j] = y[j] * xs[j] * ws;
-        if (p.tma_out) {
-            const int per_chunk = p.f32 ? 16 : 32, at = (c - c0) % per_chunk;
-            const uint32_t to = staging + chunk * kChunkBytes;
-#pragma unroll
-            for (int j = 0; j < W; ++j) {
-                if (p.f32)
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(to + ((at + j) * kRows + etid) * 4),
-                                 "f"(y[j])
-                                 : "memory");
-                else
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(
-                                     bf16_piece(to, at + j, etid / 8) + etid % 8 * 2),
-                                 "h"(__bfloat16_as_ushort(__float2bfloat16_rn(y[j])))
-                                 : "memory");
-            }
-            if (at + W == per_chunk)
-                flush(p, out_map, staging, chunk, n, t0, c + W - per_chunk, n_tok, etid);
-            continue;
-        }
-        const int64_t at = (static_cast<int64_t>(t0) + c) * p.N + n;
+        scale_columns(y, t.x_scale + c, ws);
+        const int64_t at = (static_cast<int64_t>(t.t0) + c) * p.N + t.n;
         if (p.f32) {
             float* out = static_cast<float*>(p.out) + at;
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                if (c + j < n_tok && n < p.N) out[j * p.N] = y[j];
+                if (c + j < t.n_tok && t.n < p.N) out[j * p.N] = y[j];
         } else {
             __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + at;
 #pragma unroll
             for (int j = 0; j < W; ++j)
-                if (c + j < n_tok && n < p.N) out[j * p.N] = __float2bfloat16_rn(y[j]);
+                if (c + j < t.n_tok && t.n < p.N) out[j * p.N] = __float2bfloat16_rn(y[j]);
         }
         __syncwarp();
     }
 }
 
-template <int CG, bool INT8>
+// SPLIT: the cluster's units share K (without it the compiler knows the pair's
+// ranks, worth 3 to 7 % of the int8 kernel's time).
+template <int CG, bool INT8, bool SPLIT>
 __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap x_map,
                 const __grid_constant__ CUtensorMap w_map,
@@ -326,14 +397,15 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     const int lane = threadIdx.x % 32;
     // The cluster's CTAs (CG 1) or pairs (CG 2) split K: `part` is this one's
     // share, `half` the CTA of a pair, `lead` the rank that issues its MMAs.
-    const uint32_t rank = cluster_cta_rank();
-    const uint32_t unit = cluster_id_x(), units = cluster_count_x();
+    const uint32_t rank = __shfl_sync(0xffffffffu, cluster_cta_rank(), 0);
+    const uint32_t unit = __shfl_sync(0xffffffffu, cluster_id_x(), 0);
+    const uint32_t units = __shfl_sync(0xffffffffu, cluster_count_x(), 0);
     const int half = CG == 2 ? static_cast<int>(rank & 1) : 0;
-    const int part = static_cast<int>(rank) / CG;
-    const uint32_t lead = rank - half;
+    const int part = SPLIT ? static_cast<int>(rank) / CG : 0;
+    const uint32_t lead = SPLIT || CG == 1 ? rank - half : 0;
     const bool leader = half == 0;
     const uint16_t pair = static_cast<uint16_t>(3u << lead);
-    const int split = p.split;
+    const int split = SPLIT ? p.split : 1;
     const int kb0 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * part / split);
     const int kb1 = static_cast<int>(static_cast<int64_t>(p.k_blocks) * (part + 1) / split);
     const int bn_cta = p.bn / CG;  // token rows this CTA loads
@@ -368,7 +440,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     // The peers' barriers must be initialised before anything arrives there.
     if (CG == 2 || split > 1) cluster_barrier();
     tcgen05_fence_after();
-    const uint32_t tmem = h.tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, h.tmem, 0);
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -482,6 +554,14 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if (elect_one()) mma_commit<CG>(smem_addr(&h.drained), pair);
             if (!mbar_wait_slice(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
         }
+    } else if (SPLIT && warp == kAnnounceWarp) {
+        // This CTA's products are done: its ring is free for the other units'
+        // columns.  (A release at cluster scope takes about 1000 clocks; the
+        // epilogue writes its own columns meanwhile.)
+        if (static_cast<int>(unit) < p.tiles && warp_wait(p, &h.acc_full[0], 0, abort) &&
+            lane < split)
+            mbar_arrive_cluster(
+                map_to_rank(smem_addr(&h.open), static_cast<uint32_t>(lane * CG + half)));
     } else if (warp >= kEpilogueWarp && warp < kEpilogueWarp + 4) {
         // -------------------------------------------------- epilogue -----
         // Thread = channel (TMEM lane), registers = tokens.
@@ -514,88 +594,56 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if (named_barrier_or(1, 128, !ok)) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * kAcc + lanes;
-            const int n_tok = p.M - t0 < p.bn ? p.M - t0 : p.bn;
-            const auto hand_back = [&]() { release_acc(h.acc_empty[acc.at], lead, lane); };
-            if (split == 1 && p.tma_out && !p.f32) {
+            const Tile t{n, t0, p.M - t0 < p.bn ? p.M - t0 : p.bn, etid, x_scale};
+            // Fragments for the transposing stores, lanes otherwise.
+            const bool fragments = p.tma_out && !p.f32;
+            Join g{};
+            if constexpr (SPLIT) {
+                const int own = p.bn / split;  // a multiple of 8 (tma_out: of a chunk)
+                const uint32_t block = static_cast<uint32_t>(own * kRows * 4);
+                g = Join{ring, ring + split * block, block, part, split, own};
+                if (fragments)
+                    send_columns<16, true>(g, d, etid);
+                else
+                    send_columns<8, false>(g, d, etid);
+                fence_async_shared();
+                named_barrier(1, 128);
+                if (etid == 0) {
+                    // Their rings are free once their products are done too.
+                    if (!mbar_wait_slice<true>(smem_addr(&h.open), 0, abort)) {
+                        gave_up(p, abort);
+                    } else {
+                        for (int q = 0; q < split; ++q) {
+                            if (q == part) continue;
+                            const uint32_t dest = static_cast<uint32_t>(q * CG + half);
+                            bulk_push(map_to_rank(g.incoming + part * block, dest),
+                                      g.outgoing + q * block, block,
+                                      map_to_rank(smem_addr(&h.joined), dest));
+                        }
+                    }
+                }
+                __syncwarp();
+                const bool in = warp_wait<true>(p, &h.joined, 0, abort);
+                if (named_barrier_or(1, 128, !in)) break;
+            }
+            const int c0 = SPLIT ? part * g.own : 0, c1 = SPLIT ? c0 + g.own : p.bn;
+            const auto done = [&]() {
+                if constexpr (!SPLIT) release_acc(h.acc_empty[acc.at], lead, lane);
+            };
+            if (fragments) {
                 float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = __shfl_sync(0xffffffffu, ws, lane / 4 + 8 * i);
-                emit_bf16(p, &out_map, staging, chunk, x_scale, w, n, t0, n_tok, d, etid,
-                          hand_back);
-                continue;
+                emit_bf16<SPLIT>(p, &out_map, staging, chunk, t, w, g, d, c0, c1, done);
+            } else if (p.tma_out) {
+                if constexpr (SPLIT)
+                    emit_direct<8, SPLIT>(p, t, ws, g, d, c0, c1, done);
+                else
+                    emit_f32<SPLIT>(p, &out_map, staging, chunk, t, ws, g, d, c0, c1, done);
+            } else {
+                emit_direct<SPLIT ? 8 : 16, SPLIT>(p, t, ws, g, d, c0, c1, done);
             }
-            if (split == 1) {
-                emit<16>(
-                    p, &out_map, staging, chunk, x_scale, ws, n, t0, n_tok, 0, p.bn, etid,
-                    [&](int c, float (&v)[16]) {
-                        uint32_t r[16];
-                        tmem_load16(r, d + c);
-                        tmem_wait_loads();
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                    },
-                    hand_back);
-                continue;
-            }
-            // Split K: unit q of the cluster adds up columns [q own, (q + 1)
-            // own).  The others' columns go to shared memory, four columns of
-            // a channel as 16 bytes ([q][column / 4][channel]), and from there
-            // as one bulk copy each into the ring of the unit they belong to,
-            // once its products are done as well (it says so on `open`).
-            const int own = p.bn / split;  // a multiple of 8
-            const uint32_t block = static_cast<uint32_t>(own * kRows * 4);
-            const uint32_t outgoing = ring, incoming = ring + split * block;
-            if (etid < split)
-                mbar_arrive_cluster(map_to_rank(smem_addr(&h.open),
-                                                static_cast<uint32_t>(etid * CG + half)));
-            for (int c = 0; c < p.bn; c += 8) {
-                if (c / own == part) continue;
-                uint32_t v[8];
-                tmem_load8(v, d + c);
-                tmem_wait_loads();
-                sts16(outgoing + (c / 4 * kRows + etid) * 16, v);
-                sts16(outgoing + ((c / 4 + 1) * kRows + etid) * 16, v + 4);
-            }
-            fence_async_shared();
-            named_barrier(1, 128);
-            if (etid == 0) {
-                if (!mbar_wait_slice<true>(smem_addr(&h.open), 0, abort)) {
-                    gave_up(p, abort);
-                } else {
-                    for (int q = 0; q < split; ++q) {
-                        if (q == part) continue;
-                        const uint32_t dest = static_cast<uint32_t>(q * CG + half);
-                        bulk_push(map_to_rank(incoming + part * block, dest), outgoing + q * block,
-                                  block, map_to_rank(smem_addr(&h.joined), dest));
-                    }
-                }
-            }
-            __syncwarp();
-            const bool in = warp_wait<true>(p, &h.joined, 0, abort);
-            if (named_barrier_or(1, 128, !in)) break;
-            emit<8>(
-                p, &out_map, staging, chunk, x_scale, ws, n, t0, n_tok, part * own,
-                (part + 1) * own, etid,
-                [&](int c, float (&v)[8]) {
-                    uint32_t r[8];
-                    tmem_load8(r, d + c);
-                    tmem_wait_loads();
-                    const uint32_t at = incoming + ((c - part * own) / 4 * kRows + etid) * 16;
-                    for (int q = 0; q < split; ++q) {
-                        uint4 lo = make_uint4(r[0], r[1], r[2], r[3]);
-                        uint4 hi = make_uint4(r[4], r[5], r[6], r[7]);
-                        if (q != part) {
-                            lo = lds16(at + q * block);
-                            hi = lds16(at + q * block + kRows * 16);
-                        }
-                        const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            v[j] = q == 0 ? __uint_as_float(w[j]) : v[j] + __uint_as_float(w[j]);
-                    }
-                },
-                []() {});
-            break;  // one tile per cluster
+            if (SPLIT) break;  // one tile per cluster
         }
         if (etid == 0) bulk_wait_read<0>();
     } else if (INT8 && warp >= kWidenWarp) {
@@ -705,12 +753,15 @@ bool encode_operand(CUtensorMap* m, const void* base, int64_t rows, int64_t K, i
                   CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-void* gemm_kernel_for(int cg, bool int8) {
-    if (cg == 1)
-        return int8 ? reinterpret_cast<void*>(&gemm_kernel<1, true>)
-                    : reinterpret_cast<void*>(&gemm_kernel<1, false>);
-    return int8 ? reinterpret_cast<void*>(&gemm_kernel<2, true>)
-                : reinterpret_cast<void*>(&gemm_kernel<2, false>);
+template <int CG, bool INT8>
+void* gemm_entry(bool split) {
+    return split ? reinterpret_cast<void*>(&gemm_kernel<CG, INT8, true>)
+                 : reinterpret_cast<void*>(&gemm_kernel<CG, INT8, false>);
+}
+
+void* gemm_kernel_for(int cg, bool int8, bool split) {
+    if (cg == 1) return int8 ? gemm_entry<1, true>(split) : gemm_entry<1, false>(split);
+    return int8 ? gemm_entry<2, true>(split) : gemm_entry<2, false>(split);
 }
 
 // Launch configuration of `grid` CTAs in clusters; attr[0] is the cluster's.
@@ -778,10 +829,12 @@ int gemm_prepare(int smem_optin) {
     for (int cg = 1; cg <= 2; ++cg)
         for (bool int8 : {false, true}) {
             if (smem_bytes(cg, int8) > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
-            cudaError_t e = cudaFuncSetAttribute(gemm_kernel_for(cg, int8),
-                                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 smem_bytes(cg, int8));
-            if (e != cudaSuccess) return static_cast<int>(e);
+            cudaError_t e;
+            for (bool split : {false, true})
+                if ((e = cudaFuncSetAttribute(gemm_kernel_for(cg, int8, split),
+                                              cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              smem_bytes(cg, int8))) != cudaSuccess)
+                    return static_cast<int>(e);
             // Clusters of 1, 2, 4 and 8 CTAs that run at once (they do not
             // cross a GPC, so a few SMs can be out of reach).
             for (int i = 0; i < 4; ++i) {
@@ -790,7 +843,7 @@ int gemm_prepare(int smem_optin) {
                 cluster_config(&cfg, attr, 1 << i, 1 << i, cg, int8);
                 cfg.numAttrs = 1;
                 int n = 0;
-                e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel_for(cg, int8), &cfg);
+                e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel_for(cg, int8, (1 << i) > cg), &cfg);
                 if (e != cudaSuccess) return static_cast<int>(e);
                 g_clusters[cg - 1][int8][i] = n;
             }
@@ -850,7 +903,7 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = max_sms >= d.sm_count ? 2 : 1;
     void* args[] = {&x_map, &w_map, &out_map, &p};
-    return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8), args));
+    return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8, p.split > 1), args));
 }
 
 }  // namespace tw
