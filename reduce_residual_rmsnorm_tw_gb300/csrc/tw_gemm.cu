@@ -24,8 +24,6 @@
 // memory by the others (and added in rank order: the same bits every time).
 #include <cuda.h>
 
-#include <mutex>
-
 #include "tw_tcgen05.cuh"
 
 namespace tw {
@@ -46,10 +44,13 @@ constexpr int kAnnounceWarp = 2, kEpilogueWarp = 4, kWidenWarp = 8;
 
 // Largest token tile: one unit's two accumulators (and, for int8, the widened
 // W) share 512 TMEM columns; a single CTA takes short tiles only.
-__host__ __device__ constexpr int max_tokens(int cg, bool int8) { return cg == 1 ? 64 : (int8 ? 192 : 256); }
+__host__ __device__ constexpr int max_tokens(int cg, bool int8) {
+    return cg == 1 ? 64 : (int8 ? 192 : 256);
+}
 // Bytes of the ring, per CTA.
-__host__ __device__ constexpr int x_bytes(int cg, bool int8) { return max_tokens(cg, int8) / cg * kBlockK; }
-__host__ __device__ constexpr int stage_bytes(int cg, bool int8) { return kRows * kBlockK + x_bytes(cg, int8); }
+__host__ __device__ constexpr int stage_bytes(int cg, bool int8) {
+    return kRows * kBlockK + max_tokens(cg, int8) / cg * kBlockK;
+}
 __host__ __device__ constexpr int slot_bytes(int cg, bool int8) {
     return int8 ? max_tokens(cg, int8) / cg * kUnitK * 2 : 0;
 }
@@ -429,8 +430,8 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         h.abort = 0;
         mbar_init_fence();
         if (split > 1)
-            mbar_arrive_expect_tx(smem_addr(&h.joined), static_cast<uint32_t>(
-                                                            (split - 1) * (p.bn / split) * kRows * 4));
+            mbar_arrive_expect_tx(smem_addr(&h.joined),
+                                  static_cast<uint32_t>((p.bn - p.bn / split) * kRows * 4));
         tensormap_prefetch(&x_map);
         tensormap_prefetch(&w_map);
     }
@@ -659,9 +660,9 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
         Ring r, c;
         const int tile_units = 2 * (kb1 - kb0);
-        const int my_tiles = static_cast<int>(unit) < p.tiles
-                                 ? (p.tiles - 1 - static_cast<int>(unit)) / static_cast<int>(units) + 1
-                                 : 0;
+        const int first = static_cast<int>(unit);
+        const int my_tiles =
+            first < p.tiles ? (p.tiles - 1 - first) / static_cast<int>(units) + 1 : 0;
         const int64_t n_units = static_cast<int64_t>(my_tiles) * tile_units;
         for (int i = 0; i < group; ++i) c.next(kSlots);
         for (int i = 0; i < group / 2; ++i) r.next(S);
@@ -784,14 +785,18 @@ struct Plan {
     double cost = 0;
 };
 
-// The cheapest of the cuts a call allows, by the time (in clocks) its busiest
-// unit takes.  Per ring stage: a pair's two operands' MMAs bound e4m3 (2 bn,
-// measured 520 at bn = 256), what widening W costs and the hand-over of its
-// slots int8 (870 at 128, 1000 at 192); a lone CTA's stages cost about the same
-// at its short tiles.  Then the start (barriers, TMEM, the first bytes), the
-// last tile's way out, and with split K the join.
+// The cheapest of the cuts a call allows, by the clocks its busiest unit takes
+// (fitted to sweeps of every cut over 13 shapes from 16 x 8192 x 1024 to
+// 1024 x 8192 x 8192; the cut taken was within 15 % of the best of each).
+//   A ring stage costs what a unit's hand-overs of it do, plus its products:
+//   int8 760 + bn for a pair, 670 + 2.5 bn for a lone CTA; e4m3 390 + 0.85 bn
+//   and 375 + 0.8 bn; together never less than reading W and x once.
+//   The last tile's way out adds 14 clocks per column, a split the join of its
+//   shares (int8 6000 + 15 bn, e4m3 3000 + 15 bn).
 Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
     Plan best;
+    // 6.3 TB/s at 1.9 GHz: 3300 bytes a clock.
+    const double once = static_cast<double>(M + N) * k_blocks * kBlockK / 3300.0;
     for (int cg = 1; cg <= 2; ++cg) {
         const int most_bn = max_tokens(cg, int8);
         const int64_t channel_tiles = (N + kRows * cg - 1) / (kRows * cg);
@@ -802,8 +807,8 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
             c.bn = bn;
             c.token_tiles = (M + bn - 1) / bn;
             c.tiles = channel_tiles * c.token_tiles;
-            const double stage = int8 ? 600.0 + 2.0 * bn + (cg == 1 ? 2.0 * bn : 0.0)
-                                      : (cg == 2 ? 350.0 + 0.67 * bn : 400.0 + 1.5 * bn);
+            const double stage = int8 ? (cg == 2 ? 760.0 + 1.0 * bn : 670.0 + 2.5 * bn)
+                                      : (cg == 2 ? 390.0 + 0.85 * bn : 375.0 + 0.8 * bn);
             for (int split = 1, log2 = cg - 1; log2 < 4 && split <= k_blocks; split *= 2, ++log2) {
                 int64_t units = sms >> log2;
                 if (units > g_clusters[cg - 1][int8][log2]) units = g_clusters[cg - 1][int8][log2];
@@ -814,8 +819,10 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
                 if (split > 1 && bn * kRows * 8 > stages(cg, int8) * stage_bytes(cg, int8)) break;
                 const int64_t waves = (c.tiles + units - 1) / units;
                 c.split = split;
-                c.cost = static_cast<double>(waves * ((k_blocks + split - 1) / split)) * stage +
-                         14.0 * bn + (split > 1 ? 2000.0 + 50.0 * bn / split : 0.0);
+                const double main =
+                    static_cast<double>(waves * ((k_blocks + split - 1) / split)) * stage;
+                c.cost = (main > once ? main : once) + 14.0 * bn +
+                         (split > 1 ? (int8 ? 6000.0 : 3000.0) + 15.0 * bn : 0.0);
                 if (best.cg == 0 || c.cost < best.cost) best = c;
             }
         }
@@ -843,7 +850,8 @@ int gemm_prepare(int smem_optin) {
                 cluster_config(&cfg, attr, 1 << i, 1 << i, cg, int8);
                 cfg.numAttrs = 1;
                 int n = 0;
-                e = cudaOccupancyMaxActiveClusters(&n, gemm_kernel_for(cg, int8, (1 << i) > cg), &cfg);
+                void* fn = gemm_kernel_for(cg, int8, (1 << i) > cg);
+                e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
                 if (e != cudaSuccess) return static_cast<int>(e);
                 g_clusters[cg - 1][int8][i] = n;
             }
@@ -903,7 +911,8 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.numAttrs = max_sms >= d.sm_count ? 2 : 1;
     void* args[] = {&x_map, &w_map, &out_map, &p};
-    return static_cast<int>(cudaLaunchKernelExC(&cfg, gemm_kernel_for(cg, int8, p.split > 1), args));
+    void* fn = gemm_kernel_for(cg, int8, p.split > 1);
+    return static_cast<int>(cudaLaunchKernelExC(&cfg, fn, args));
 }
 
 }  // namespace tw

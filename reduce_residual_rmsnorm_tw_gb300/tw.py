@@ -106,7 +106,9 @@ def _check(rc):
 
 def _stream_handle(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # The current stream's handle without a Stream object around it (a
+        # decode step's kernel is over in the time that takes).
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -250,7 +252,7 @@ tw_fused_reduce_add_rmsnorm_f32 = _typed("tw_fused_reduce_add_rmsnorm_f32",
 def _on_current_device(*tensors):
     dev = torch.cuda.current_device() if tensors[0].is_cuda else None
     for t in tensors:
-        if not t.is_cuda or t.get_device() != dev:
+        if t.get_device() != dev:
             raise ValueError("every tensor must be on the current CUDA device")
 
 
@@ -265,6 +267,18 @@ def _quantised(q, name="out"):
 def _dense(name, t, shape, dtype):
     if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
+
+
+def _pointers(name, tensors, shape, dtype, dev):
+    """The pointers of alike tensors on device ``dev`` as a ctypes array."""
+    ptrs = (ctypes.c_void_p * len(tensors))()
+    for i, t in enumerate(tensors):
+        if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous {list(shape)} {dtype} tensors")
+        if t.get_device() != dev:
+            raise ValueError("every tensor must be on the current CUDA device")
+        ptrs[i] = t.data_ptr()
+    return ptrs
 
 
 def tw_fused_reduce_add_rmsnorm_q8(partials, residual, weight, out, out_scale,
@@ -283,25 +297,23 @@ def tw_fused_reduce_add_rmsnorm_q8(partials, residual, weight, out, out_scale,
     if not n or not n_out or len(out_scale) != n_out:
         raise ValueError("need at least one partial, one destination and a scale tensor for "
                          "each destination")
-    for p in partials:
-        _dense("partials", p, shape, dtype)
+    qt = _quantised(out[0])
+    # The device every tensor has to be on (-1: the tensors are on the CPU,
+    # which _on_current_device refuses once their shapes are checked).
+    dev = torch.cuda.current_device() if residual.is_cuda else -1
+    p_arr = _pointers("partials", partials, shape, dtype, dev)
+    o_arr = _pointers("out", out, shape, out[0].dtype, dev)
+    s_arr = _pointers("out_scale", out_scale, (T,), torch.float32, dev)
     _dense("residual", residual, shape, dtype)
     _dense("residual_out", residual_out, shape, dtype)
     _dense("weight", weight, (H,), dtype)
-    qt = _quantised(out[0])
-    for q, s in zip(out, out_scale):
-        _dense("out", q, shape, out[0].dtype)
-        _dense("out_scale", s, (T,), torch.float32)
-    _on_current_device(residual, weight, residual_out, *partials, *out, *out_scale)
+    _on_current_device(residual, weight, residual_out)
     if T == 0:
         return
-    ptrs = ctypes.c_void_p * n_out
     _check(load().tw_fused_reduce_add_rmsnorm_q8(
-        (ctypes.c_void_p * n)(*[p.data_ptr() for p in partials]), n, residual.data_ptr(),
-        weight.data_ptr(), ptrs(*[q.data_ptr() for q in out]),
-        ptrs(*[s.data_ptr() for s in out_scale]), n_out, residual_out.data_ptr(), T, H, eps, t0,
-        T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
-        _stream_handle(stream), _DTYPES[dtype], qt))
+        p_arr, n, residual.data_ptr(), weight.data_ptr(), o_arr, s_arr, n_out,
+        residual_out.data_ptr(), T, H, eps, t0, T if t1 is None else t1,
+        _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[dtype], qt))
 
 
 def tw_quantize_rows_q8(x, out, out_scale, t0=0, t1=None, max_sms=None, stream=None):
