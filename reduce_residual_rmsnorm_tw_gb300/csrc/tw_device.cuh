@@ -269,6 +269,13 @@ __device__ __forceinline__ float max_abs(float m, float v) {
     return r;
 }
 
+// max(|m|, |a|, |b|), NaN if any is.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
+
 // Largest of the warp's non-negative floats (NaN if any is): the bits of
 // non-negative floats order as unsigned integers, NaN above infinity.
 __device__ __forceinline__ float warp_max_abs(float m) {
@@ -364,7 +371,7 @@ __device__ __forceinline__ float max_abs_product(float m, const float* x, const 
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
         mul2(v + e, x + e, w + e);
-        m = max_abs(max_abs(m, v[e]), v[e + 1]);
+        m = max_abs(m, v[e], v[e + 1]);
     }
     return m;
 }
