@@ -5,7 +5,7 @@ import torch
 
 from reduce_residual_rmsnorm_tw_gb300 import tw
 from tests.parity import SENTINEL
-from tests.q8_reference import check_product, draw_8_bit, f64
+from tests.q8_reference import check_product, draw_8_bit, f64, product, product_bound
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "f32": torch.float32}
@@ -24,13 +24,17 @@ def run(T, N, K, quant, dtype, t0=0, t1=None, max_sms=None, seed=5):
     return out
 
 
-# One token to several tiles of tokens; channels below, at and off a tile's
+# One token to several tiles of tokens; few tiles over a long K (split over
+# clusters, shares of 8 columns up), many tiles; channels below, at and off a tile's
 # edge, down to one; the shortest inner size, sizes off every slice, long ones.
 SHAPES = [(1, 128, 128), (1, 1, 16), (2, 7, 48), (3, 8192, 1024), (8, 1000, 8192),
           (9, 130, 272), (16, 256, 144), (17, 129, 4096), (31, 64, 16), (33, 515, 1040),
           (64, 1024, 8192), (65, 127, 128), (100, 257, 2064), (128, 128, 128),
           (129, 300, 528), (192, 384, 256), (193, 255, 1008), (250, 999, 16), (256, 256, 384),
-          (257, 513, 640), (333, 4090, 5120), (700, 96, 32), (1024, 1024, 1024)]
+          (257, 513, 640), (333, 4090, 5120), (700, 96, 32), (1024, 1024, 1024),
+          (4, 37, 65536), (12, 256, 8192), (40, 200, 8192), (64, 128, 4096), (90, 640, 8192),
+          (120, 2048, 2048), (128, 1032, 6160), (300, 700, 8192), (600, 130, 4112),
+          (2000, 264, 512), (1500, 4104, 256)]
 
 
 @pytest.mark.parametrize("quant", ["int8", "e4m3"])
@@ -50,6 +54,38 @@ def test_ranges_and_budgets(max_sms, quant):
 def test_repeated_calls_give_the_same_bits(quant):
     for T, N, K in ((4, 1024, 4096), (40, 2048, 4096), (400, 2048, 4096)):
         assert torch.equal(run(T, N, K, quant, "f32"), run(T, N, K, quant, "f32"))
+
+
+@pytest.mark.parametrize("quant", ["int8", "e4m3"])
+def test_small_scales_keep_their_bits(quant):
+    # Scales whose product is below fp32's normal range, the result is not.
+    for T in (3, 40, 200):
+        x, _ = draw_8_bit(T, 512, quant, 21)
+        w, _ = draw_8_bit(264, 512, quant, 22)
+        xs, ws = torch.full((T,), 2e-21, device="cuda"), torch.full((264,), 3e-20, device="cuda")
+        out = torch.empty(T, 264, device="cuda")
+        tw.tw_gemm_q8(x, xs, w, ws, out)
+        want, size = product(x, xs, w, ws)
+        raw = np.abs(f64(x)) @ np.abs(f64(w)).T if quant == "int8" else np.full_like(want, np.inf)
+        big = np.abs(want) > 1e-37  # fp32's normal range ends at 1.2e-38
+        # Sums of sum|x w| <= 2^27 times 2e-21 times 3e-20 stay normal at every
+        # step, so the bound of any product holds: e4m3's sum rounds relative
+        # to sum|x w|, which may be far above |want| where terms cancel.
+        err, bound = np.abs(f64(out) - want), product_bound(want, size, raw, 512, out.dtype)
+        assert big.any() and np.all(err[big] <= bound[big])
+
+
+def test_offsets_past_2_to_31():
+    # 2.2e9 output elements; 2.6e9 bytes of x.  Sampled rows.
+    for T, N, K, dtype in ((270000, 8192, 16, "bf16"), (40000, 24, 65536, "f32")):
+        x = torch.randint(-128, 128, (T, K), dtype=torch.int8, device="cuda")
+        w = torch.randint(-128, 128, (N, K), dtype=torch.int8, device="cuda")
+        xs, ws = torch.rand(T, device="cuda"), torch.rand(N, device="cuda")
+        out = torch.empty(T, N, dtype=DT[dtype], device="cuda")
+        tw.tw_gemm_q8(x, xs, w, ws, out)
+        rows = torch.tensor([0, 1, T // 2, T - 130, T - 2, T - 1], device="cuda")
+        check_product(out[rows], x[rows], xs[rows], w, ws, f"{T}x{N}x{K}")
+        del x, w, out
 
 
 def test_int8_is_exact_below_2_to_24():

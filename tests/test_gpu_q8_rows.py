@@ -169,3 +169,22 @@ def test_empty_batches_and_other_streams():
     tw.tw_quantize_rows_q8(x, b, sb, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(a, b) and torch.equal(sa, sb)
+
+
+def test_offsets_past_2_to_31():
+    # 2.3e9 elements a tensor; the last rows against the reference.
+    T, H = 140000, 16384
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda").normal_()
+    q = torch.zeros(T, H, dtype=torch.int8, device="cuda")
+    s = torch.zeros(T, device="cuda")
+    tw.tw_quantize_rows_q8(x, q, s)
+    last = slice(T - 3, T)
+    check_rows(q[last], s[last], inputs.to_f64(x[last]), "int8", np.full(3, 3 * U), "rows")
+    q.zero_()
+    w = torch.ones(H, dtype=torch.bfloat16, device="cuda")
+    r = torch.empty_like(x)
+    tw.tw_fused_reduce_add_rmsnorm_q8([x], x, w, [q], [s], r, 1e-5)
+    v = 2 * inputs.to_f64(x[last])
+    ref = v / np.sqrt((v ** 2).mean(axis=1, keepdims=True) + 1e-5)
+    check_rows(q[last], s[last], ref, "int8", np.full(3, 100 * U), "norm")
+    assert torch.equal(r[last], 2 * x[last])  # exact in bf16
