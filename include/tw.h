@@ -236,21 +236,21 @@ int tw_split_launch(const void* const* partials, int n_parts,
  * 8-bit values q with one fp32 scale s:
  *   s = max_h |v[h]| / top,  q[h] = round(v[h] / s),  v[h] ~ q[h] * s
  * with top = 127 (TW_INT8) or 448 (TW_E4M3), rounded to nearest even.  The
- * kernels multiply by top / max instead of dividing by s, so a quotient within
- * an ulp or two of a rounding boundary may round to its neighbour.  A row
- * whose largest magnitude is below 2^-117 is a zero row: s = 0, q = 0.  A row
- * that holds a NaN or an infinity: s = NaN, q = 0 (it stands for NaN
- * throughout).  8-bit tensors are [T, H] with row stride H bytes, 16-byte
- * aligned; scales are fp32 [T], 4-byte aligned; only rows and scales of tokens
- * [t0, t1) are written.  The other conventions are those at the top. */
+ * quotient is taken as v times top / max in fp32, so one that lies within two
+ * ulp of the middle between two values may go to either.  A row whose largest
+ * magnitude is below 2^-117 is a zero row: s = 0, q = 0.  A row that holds a
+ * NaN or an infinity: s = NaN, q = 0 (it stands for NaN throughout).  8-bit
+ * tensors are [T, H] with row stride H bytes, 16-byte aligned; scales are fp32
+ * [T], 4-byte aligned; only rows and scales of tokens [t0, t1) are written.
+ * The other conventions are those at the top. */
 
 /* The fused step with 8-bit outputs: out[k][t,h] and out_scale[k][t] hold the
- * quantised y[t,:] = x / rms * weight for every destination k (the fp32 row is
- * quantised, not a rounded copy; the largest magnitude is taken of
- * x * weight, so that a row whose product overflows fp32 counts as one that
- * holds an infinity), residual_out[t,:] = x in dtype as
- * ever.  out_scale is a HOST array of n_out DEVICE pointers.  Kernel chosen as
- * by TW_PATH_AUTO.  qtype is a tw_qtype; the alias rule covers the scales. */
+ * quantised y[t,:] = x / rms * weight for every destination k, residual_out[t,:]
+ * = x in dtype as ever.  The fp32 row is quantised, not a rounded copy; its
+ * largest magnitude is taken of x * weight, so that a row whose product
+ * overflows fp32 counts as one that holds an infinity.  out_scale is a HOST
+ * array of n_out DEVICE pointers.  Kernel chosen as by TW_PATH_AUTO.  qtype is a
+ * tw_qtype; the alias rule covers the scales. */
 int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,
                                    const void* residual, const void* weight,
                                    void* const* out, float* const* out_scale,
@@ -267,16 +267,19 @@ int tw_quantize_rows_q8(const void* x, void* out, float* out_scale, int64_t T,
                         void* stream, int dtype, int qtype);
 
 /* A linear layer on 8-bit operands, one scale per token and per channel:
- *   out[t,n] = x_scale[t] * w_scale[n] * sum_k x[t,k] * w[n,k]
+ *   out[t,n] = (sum_k x[t,k] * w[n,k]) * x_scale[t] * w_scale[n]
  * for t in [t0, t1), rounded once to dtype (TW_BF16 or TW_F32).  x [T, K] and
  * w [N, K] are 8-bit of one qtype (int8 values may use all of [-128, 127]),
  * out is [T, N]; all row-major and dense.  Products are exact, their sum is
- * held in fp32: exact for int8 while every partial sum stays within 2^24 (any
- * K <= 1024), otherwise off by a few 2^-24 of the largest partial sum.
- * Rules: K a multiple of 16, 16 <= K <= TW_MAX_K_Q8, 1 <= N < 2^31, T < 2^31;
- * x, w and out 16-byte aligned, the scales 4-byte aligned; any T and N.
- * Written to partials[r] of the fused step, out is a row-parallel layer's
- * partial. */
+ * held in fp32 or 32-bit integers: exact for int8 while every partial sum stays
+ * within 2^24 (any K <= 1024), otherwise off by a few 2^-24 of the largest
+ * partial sum.  The order of the sum depends on the sizes and max_sms, not on
+ * the data or the run.  Written to partials[r] of the fused step, out is a
+ * row-parallel layer's partial.
+ * Rules: K a multiple of 16, 16 <= K <= TW_MAX_K_Q8; T and N at most
+ * 2^31 - 512, N >= 1; x, w and out 16-byte aligned, the scales 4-byte aligned;
+ * out overlaps no input.  T and N need no alignment (rows of out that are
+ * whole 16-byte units are stored faster). */
 int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
                const float* w_scale, void* out, int64_t T, int64_t N, int64_t K,
                int64_t t0, int64_t t1, int max_sms, void* stream, int dtype,

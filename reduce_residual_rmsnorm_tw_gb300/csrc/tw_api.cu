@@ -6,6 +6,7 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 #include <string>
 
@@ -70,6 +71,7 @@ struct DeviceState {
     // free to share SMs; then [log2 cluster][dtype][vectors per thread 1, 2,
     // 4][partials held 2, 4, 8, 16][8-bit outputs].
     int max_clusters[2][4][2][3][4][2] = {};
+    int gemm_clusters[2][2][4] = {};  // see DeviceInfo
     unsigned int* status = nullptr;
     cudaEvent_t fork = nullptr;
     cudaEvent_t join = nullptr;
@@ -120,7 +122,8 @@ int device_state(DeviceState** out) {
         // its first launch, which may wait for running kernels).
         if ((e = static_cast<cudaError_t>(signal_prepare())) != cudaSuccess)
             return cuda_fail(e, "cudaFuncGetAttributes");
-        if ((e = static_cast<cudaError_t>(gemm_prepare(d.smem_optin))) != cudaSuccess ||
+        if ((e = static_cast<cudaError_t>(gemm_prepare(d.smem_optin, d.gemm_clusters))) !=
+                cudaSuccess ||
             (e = static_cast<cudaError_t>(gemv_prepare(d.smem_optin))) != cudaSuccess ||
             (e = static_cast<cudaError_t>(quantize_prepare(d.smem_optin))) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute");
@@ -603,6 +606,7 @@ int device_info(DeviceInfo* out) {
     out->sm_count = d->sm_count;
     out->smem_optin = d->smem_optin;
     out->status = d->status;
+    memcpy(out->gemm_clusters, d->gemm_clusters, sizeof(out->gemm_clusters));
     return TW_OK;
 }
 

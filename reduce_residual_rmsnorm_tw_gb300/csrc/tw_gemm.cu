@@ -732,7 +732,6 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;
-int g_clusters[2][2][4];  // [CG - 1][int8][log2 of the cluster]
 
 // A dense [rows, columns] tensor moved in boxes of box_columns x box_rows; what
 // lies outside reads as zeros (0 in every type).
@@ -793,7 +792,7 @@ struct Plan {
 //   and 375 + 0.8 bn; together never less than reading W and x once.
 //   The last tile's way out adds 14 clocks per column, a split the join of its
 //   shares (int8 6000 + 15 bn, e4m3 3000 + 15 bn).
-Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
+Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const DeviceInfo& d) {
     Plan best;
     // 6.3 TB/s at 1.9 GHz: 3300 bytes a clock.
     const double once = static_cast<double>(M + N) * k_blocks * kBlockK / 3300.0;
@@ -811,7 +810,8 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
                                       : (cg == 2 ? 390.0 + 0.85 * bn : 375.0 + 0.8 * bn);
             for (int split = 1, log2 = cg - 1; log2 < 4 && split <= k_blocks; split *= 2, ++log2) {
                 int64_t units = sms >> log2;
-                if (units > g_clusters[cg - 1][int8][log2]) units = g_clusters[cg - 1][int8][log2];
+                const int at_once = d.gemm_clusters[cg - 1][int8][log2];
+                if (units > at_once) units = at_once;
                 if (units < 1 || (split > 1 && c.tiles > units)) break;
                 // Whole chunks of the output's staging, or eights of a share.
                 if (bn % (split == 1 ? 32 : 8 * split) != 0) continue;
@@ -832,7 +832,7 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms) {
 
 }  // namespace
 
-int gemm_prepare(int smem_optin) {
+int gemm_prepare(int smem_optin, int (*clusters)[2][4]) {
     for (int cg = 1; cg <= 2; ++cg)
         for (bool int8 : {false, true}) {
             if (smem_bytes(cg, int8) > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
@@ -853,7 +853,7 @@ int gemm_prepare(int smem_optin) {
                 void* fn = gemm_kernel_for(cg, int8, (1 << i) > cg);
                 e = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
                 if (e != cudaSuccess) return static_cast<int>(e);
-                g_clusters[cg - 1][int8][i] = n;
+                clusters[cg - 1][int8][i] = n;
             }
         }
     void* fn = nullptr;
@@ -879,7 +879,7 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.M = static_cast<int>(g.M);
     p.k_blocks = static_cast<int>((g.K + kBlockK - 1) / kBlockK);
     p.f32 = g.dtype == TW_F32;
-    const Plan c = plan(g.M, g.N, p.k_blocks, int8, sms);
+    const Plan c = plan(g.M, g.N, p.k_blocks, int8, sms, d);
     if (c.cg == 0 || c.tiles > (int64_t{1} << 31) - 1 - sms)
         return static_cast<int>(cudaErrorInvalidValue);
     const int cg = c.cg;

@@ -88,6 +88,9 @@ struct DeviceInfo {
     int sm_count;
     int smem_optin;
     unsigned int* status;  // device status word
+    // Clusters of 1, 2, 4, 8 CTAs of the product kernels that run at once:
+    // [CTAs per unit - 1][int8][log2 of the cluster].
+    int gemm_clusters[2][2][4];
 };
 int device_info(DeviceInfo* out);
 
@@ -120,7 +123,7 @@ constexpr int kGemvTokens = 8;
 int launch_gemv(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
 int gemv_prepare(int smem_optin);
 int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
-int gemm_prepare(int smem_optin);
+int gemm_prepare(int smem_optin, int (*clusters)[2][4]);
 
 // Record `message` as the calling thread's last error and return `code`.
 int set_last_error(int code, const char* message);

@@ -97,9 +97,9 @@ extern "C" int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
     if (rc != TW_OK) return rc;
     if (!x || !x_scale || !w || !w_scale || !out)
         return refuse(TW_ERR_INVALID_ARG, "NULL pointer argument");
-    constexpr int64_t kMax = (int64_t{1} << 31) - 1;
+    constexpr int64_t kMax = (int64_t{1} << 31) - 512;  // a tile beyond fits 32 bits
     if (T > kMax || N < 1 || N > kMax)
-        return refuse(TW_ERR_INVALID_ARG, "T %lld and N %lld must be below 2^31, N >= 1",
+        return refuse(TW_ERR_INVALID_ARG, "T %lld and N %lld must be at most 2^31 - 512, N >= 1",
                       (long long)T, (long long)N);
     if (K < 1) return refuse(TW_ERR_INVALID_ARG, "K %lld < 1", (long long)K);
     if (K > TW_MAX_K_Q8)

@@ -99,7 +99,8 @@ def gemm(lib, x=BASE, xs=BASE + MB, w=BASE + 2 * MB, ws=BASE + 3 * MB, out=BASE 
 @pytest.mark.parametrize("kwargs,status", [
     ({"x": 0}, INVALID), ({"xs": 0}, INVALID), ({"w": 0}, INVALID), ({"ws": 0}, INVALID),
     ({"out": 0}, INVALID), ({"N": 0}, INVALID), ({"K": 0}, INVALID), ({"K": -16}, INVALID),
-    ({"N": 1 << 31}, INVALID), ({"T": 1 << 31}, INVALID), ({"T": (1 << 31) - 1, "N": 1 << 20}, INVALID),
+    ({"N": 1 << 31}, INVALID), ({"T": 1 << 31}, INVALID), ({"T": (1 << 31) - 511}, INVALID),
+    ({"N": (1 << 31) - 511}, INVALID), ({"T": (1 << 31) - 512, "N": 1 << 20}, INVALID),
     ({"T": -1, "t1": 0}, INVALID), ({"t0": 2, "t1": 1}, INVALID), ({"t1": 5}, INVALID),
     ({"dtype": 2}, INVALID), ({"qtype": 2}, INVALID), ({"max_sms": 0}, INVALID),
     ({"K": 72}, ALIGN), ({"K": 65552}, UNSUP), ({"x": BASE + 8}, ALIGN),
