@@ -30,11 +30,10 @@ namespace tw {
 namespace {
 
 constexpr int kBlockK = 128;     // bytes (= 8-bit elements) of K per ring stage
-constexpr int kUnitK = 64;       // int8: K elements per widened slot
 constexpr int kRows = 128;       // channels per CTA
-constexpr int kSlots = 4;        // int8: widened slots (TMEM and shared memory)
-constexpr int kSlotColumns = kUnitK / 2;
-constexpr int kMaxStages = 8;
+constexpr int kWideSlots = 4;    // int8: widened stages (TMEM and shared memory)
+constexpr int kSlotColumns = kBlockK / 2;
+constexpr int kRingStages = 12;
 constexpr int kTmemColumns = 512;
 
 // Warp roles: 0 TMA, 1 MMA, 2 (split K) tells the cluster that the products are
@@ -42,28 +41,18 @@ constexpr int kTmemColumns = 512;
 constexpr int kGroups = 4;
 constexpr int kAnnounceWarp = 2, kEpilogueWarp = 4, kWidenWarp = 8;
 
-// Largest token tile: one unit's two accumulators (and, for int8, the widened
-// W) share 512 TMEM columns; a single CTA takes short tiles only.
+// Largest token tile: a unit's two accumulators (and, for int8, two slots of
+// widened W) share 512 TMEM columns; a single CTA takes short tiles only.
 __host__ __device__ constexpr int max_tokens(int cg, bool int8) {
     return cg == 1 ? 64 : (int8 ? 192 : 256);
-}
-// Bytes of the ring, per CTA.
-__host__ __device__ constexpr int stage_bytes(int cg, bool int8) {
-    return kRows * kBlockK + max_tokens(cg, int8) / cg * kBlockK;
-}
-__host__ __device__ constexpr int slot_bytes(int cg, bool int8) {
-    return int8 ? max_tokens(cg, int8) / cg * kUnitK * 2 : 0;
-}
-__host__ __device__ constexpr int stages(int cg, bool int8) {
-    return cg == 1 ? (int8 ? 7 : 8) : (int8 ? 5 : 6);
 }
 // Staging of the output: two chunks of 32 tokens (bf16) or 16 (fp32) x 128
 // channels for TMA to store.
 constexpr int kChunkBytes = 8192;
 
 struct Header {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t wide_full[kSlots], wide_empty[kSlots];
+    uint64_t full[kRingStages], empty[kRingStages];
+    uint64_t wide_full[kWideSlots], wide_empty[kWideSlots];
     uint64_t acc_full[2], acc_empty[2];
     uint64_t open, joined, drained;
     uint32_t tmem;
@@ -73,13 +62,11 @@ struct Header {
 constexpr int kHeaderBytes = 5120;
 static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
 
-__host__ __device__ constexpr int smem_bytes(int cg, bool int8) {
-    return 1024 + kHeaderBytes + stages(cg, int8) * stage_bytes(cg, int8) +
-           kSlots * slot_bytes(cg, int8) + 2 * kChunkBytes;
-}
-static_assert(smem_bytes(1, true) <= 232448 && smem_bytes(1, false) <= 232448 &&
-                  smem_bytes(2, true) <= 232448 && smem_bytes(2, false) <= 232448,
-              "over the shared memory of an SM");
+// All of an SM's shared memory: alignment, header, the pool that the ring and
+// the slots are cut from, the output's staging.
+constexpr int kSmemBytes = 232448;
+constexpr int kPoolBytes = kSmemBytes - 1024 - kHeaderBytes - 2 * kChunkBytes;
+static_assert(kPoolBytes % 1024 == 0, "the staging must stay aligned");
 
 struct GemmParams {
     const float* x_scale;
@@ -95,6 +82,12 @@ struct GemmParams {
     int split;         // CTAs or pairs that share K
     int tma_out;       // rows of out are whole 16-byte units: stored by TMA
     int f32;           // output type
+    // Shared memory and TMEM, cut to the tile: a stage holds 128 rows of W and
+    // bn / CG of x, a slot the latter in f16 (two halves of K); accumulators
+    // are acc_columns apart, the slots' W behind them.
+    int stages, stage_bytes;
+    int slots, slot_bytes;
+    int acc_columns;
 };
 
 struct Ring {
@@ -379,17 +372,16 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                 const __grid_constant__ CUtensorMap w_map,
                 const __grid_constant__ CUtensorMap out_map,
                 const __grid_constant__ GemmParams p) {
-    constexpr uint32_t S = stages(CG, INT8);
-    constexpr int kStage = stage_bytes(CG, INT8), kSlot = slot_bytes(CG, INT8);
-    constexpr uint32_t kAcc = max_tokens(CG, INT8);         // TMEM columns between accumulators
-    constexpr uint32_t kWide = 2 * kAcc;                    // first widened slot's column
+    const uint32_t n_stages = p.stages, stage_bytes = p.stage_bytes;
+    [[maybe_unused]] const uint32_t n_slots = p.slots, slot_bytes = p.slot_bytes;
+    const uint32_t acc_columns = p.acc_columns;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* smem = reinterpret_cast<unsigned char*>(
         (reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t{1023});
     Header& h = *reinterpret_cast<Header*>(smem);
     const uint32_t ring = smem_addr(smem) + kHeaderBytes;
-    const uint32_t slots = ring + S * kStage;
-    const uint32_t staging = slots + kSlots * kSlot;
+    [[maybe_unused]] const uint32_t slots = ring + n_stages * stage_bytes;
+    const uint32_t staging = ring + kPoolBytes;
     volatile int* abort = &h.abort;
 
     // A warp index the compiler knows to be the same in all lanes: the MMA
@@ -412,12 +404,12 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     const int bn_cta = p.bn / CG;  // token rows this CTA loads
 
     if (threadIdx.x == 0) {
-        for (uint32_t s = 0; s < S; ++s) {
+        for (uint32_t s = 0; s < n_stages; ++s) {
             mbar_init(smem_addr(&h.full[s]), 1);
             mbar_init(smem_addr(&h.empty[s]), INT8 ? 8 : 1);
         }
-        for (int c = 0; c < kSlots; ++c) {
-            mbar_init(smem_addr(&h.wide_full[c]), 4 * CG);
+        for (int c = 0; c < kWideSlots; ++c) {
+            mbar_init(smem_addr(&h.wide_full[c]), 8 * CG);
             mbar_init(smem_addr(&h.wide_empty[c]), 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -442,6 +434,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     if (CG == 2 || split > 1) cluster_barrier();
     tcgen05_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, h.tmem, 0);
+    [[maybe_unused]] const uint32_t wide = tmem + 2 * acc_columns;
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -456,7 +449,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                                 half * kRows;
             const int token = static_cast<int>(tile / p.channel_tiles) * p.bn +
                               half * bn_cta;
-            for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(S)) {
+            for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(n_stages)) {
                 if (!mbar_wait_slice(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
                     gave_up(p, abort);
                     ok = false;
@@ -468,7 +461,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                 const uint32_t local = smem_addr(&h.full[r.at]);
                 const uint32_t bar = CG == 2 && !INT8 ? map_to_rank(local, lead) : local;
                 if (INT8 || leader) mbar_arrive_expect_tx(local, INT8 ? bytes : bytes * CG);
-                const uint32_t dst = ring + r.at * kStage;
+                const uint32_t dst = ring + r.at * stage_bytes;
                 tma_load_2d<INT8 ? 1 : CG>(dst, &w_map, kb * kBlockK, channel, bar);
                 tma_load_2d<INT8 ? 1 : CG>(dst + kRows * kBlockK, &x_map, kb * kBlockK, token,
                                            bar);
@@ -476,9 +469,9 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         }
         if (*abort && (INT8 || leader)) {
             // The copies in flight must land before the CTA may leave.
-            for (uint32_t k = 0; k < S && k < issued; ++k) {
+            for (uint32_t k = 0; k < n_stages && k < issued; ++k) {
                 if (r.at == 0) {
-                    r.at = S - 1;
+                    r.at = n_stages - 1;
                     r.phase ^= 1u;
                 } else {
                     --r.at;
@@ -495,6 +488,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         Ring r, acc;
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
+        const uint32_t one = elect_one();
         [[maybe_unused]] const uint64_t slot_operand = smem_operand(slots);
         [[maybe_unused]] const uint64_t ring_operand = smem_operand(ring);
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles);
@@ -502,28 +496,26 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             ok = warp_wait(p, &h.acc_empty[acc.at], acc.phase ^ 1u, abort);
             if (!ok) break;
             tcgen05_fence_after();
-            const uint32_t d = tmem + acc.at * kAcc;
+            const uint32_t d = tmem + acc.at * acc_columns;
             // Whether the next slice is there is asked while this one's products
             // issue: an answer takes about 100 clocks, a slice's products 300.
             bool there = false;
             if constexpr (INT8) {
-                const int n = 2 * (kb1 - kb0);
+                const int n = kb1 - kb0;
                 for (int k = 0; k < n; ++k) {
                     if (!there) ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
                     const uint32_t at = r.at;
-                    r.next(kSlots);
+                    r.next(n_slots);
                     there = k + 1 < n && mbar_test(smem_addr(&h.wide_full[r.at]), r.phase);
-                    if (elect_one()) {
-                        const uint64_t b = slot_operand + at * (kSlot >> 4);
-                        const uint32_t a = tmem + kWide + at * kSlotColumns;
+                    const uint64_t b = slot_operand + at * (slot_bytes >> 4);
+                    const uint32_t a = wide + at * kSlotColumns;
 #pragma unroll
-                        for (int i = 0; i < kUnitK / 16; ++i)
-                            mma_f16_tmem<CG>(d, a + 8 * i, b + 2 * i, shape, k > 0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.wide_empty[at]), pair);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < kBlockK / 16; ++i)
+                        mma_f16_tmem<CG>(d, a + 8 * i, b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4),
+                                         shape, k > 0 || i > 0, one);
+                    mma_commit<CG>(smem_addr(&h.wide_empty[at]), pair, one);
                     there = __all_sync(0xffffffffu, there);
                 }
             } else {
@@ -533,26 +525,22 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     if (!ok) break;
                     tcgen05_fence_after();
                     const uint32_t at = r.at;
-                    r.next(S);
+                    r.next(n_stages);
                     there = k + 1 < n && mbar_test(smem_addr(&h.full[r.at]), r.phase);
-                    if (elect_one()) {
-                        const uint64_t a = ring_operand + at * (kStage >> 4);
-                        const uint64_t b = a + (kRows * kBlockK >> 4);
+                    const uint64_t a = ring_operand + at * (stage_bytes >> 4);
+                    const uint64_t b = a + (kRows * kBlockK >> 4);
 #pragma unroll
-                        for (int i = 0; i < kBlockK / 32; ++i)
-                            mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0);
-                        mma_commit<CG>(smem_addr(&h.empty[at]), pair);
-                    }
-                    __syncwarp();
+                    for (int i = 0; i < kBlockK / 32; ++i)
+                        mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0, one);
+                    mma_commit<CG>(smem_addr(&h.empty[at]), pair, one);
                     there = __all_sync(0xffffffffu, there);
                 }
             }
-            if (ok && elect_one()) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]), pair);
-            __syncwarp();
+            if (ok) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]), pair, one);
         }
         if (!ok) {
             // Products in flight still read shared memory and write TMEM.
-            if (elect_one()) mma_commit<CG>(smem_addr(&h.drained), pair);
+            mma_commit<CG>(smem_addr(&h.drained), pair, one);
             if (!mbar_wait_slice(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
         }
     } else if (SPLIT && warp == kAnnounceWarp) {
@@ -594,7 +582,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             const bool ok = warp_wait(p, &h.acc_full[acc.at], acc.phase, abort);
             if (named_barrier_or(1, 128, !ok)) break;
             tcgen05_fence_after();
-            const uint32_t d = tmem + acc.at * kAcc + lanes;
+            const uint32_t d = tmem + acc.at * acc_columns + lanes;
             const Tile t{n, t0, p.M - t0 < p.bn ? p.M - t0 : p.bn, etid, x_scale};
             // Fragments for the transposing stores, lanes otherwise.
             const bool fragments = p.tma_out && !p.f32;
@@ -649,27 +637,29 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         if (etid == 0) bulk_wait_read<0>();
     } else if (INT8 && warp >= kWidenWarp) {
         // ------------------------------------------------- widening ------
-        // Groups of four warps take the 64-element halves of the stages in
-        // turn: row `row` of W into TMEM lane `row`, and the token rows.
+        // Two groups of four warps widen a stage, a 64-element half of K each
+        // (row `row` of W into TMEM lane `row`, and the token rows), the other
+        // two the next one.
         const int group = (warp - kWidenWarp) / 4;
+        const int upper = group % 2;
         const int row = threadIdx.x % 128;
         // 16-byte chunks of the token rows per thread: 32 rows x 4 chunks at
         // a time, this warp's first row x_row0.
         constexpr int kTokenChunks = max_tokens(CG, true) / CG / 32;
         const int x_row0 = row / 32 * 8, x_row = x_row0 + (row & 7), x_chunk = row / 8 % 4;
         const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
-        Ring r, c;
-        const int tile_units = 2 * (kb1 - kb0);
+        Ring r, c;  // of stages, of slots
         const int first = static_cast<int>(unit);
         const int my_tiles =
             first < p.tiles ? (p.tiles - 1 - first) / static_cast<int>(units) + 1 : 0;
-        const int64_t n_units = static_cast<int64_t>(my_tiles) * tile_units;
-        for (int i = 0; i < group; ++i) c.next(kSlots);
-        for (int i = 0; i < group / 2; ++i) r.next(S);
-        for (int64_t u = group; u < n_units; u += kGroups) {
-            const int upper = static_cast<int>(u) & 1;
+        const int64_t n = static_cast<int64_t>(my_tiles) * (kb1 - kb0);
+        if (group >= 2) {
+            r.next(n_stages);
+            c.next(n_slots);
+        }
+        for (int64_t k = group / 2; k < n; k += kGroups / 2) {
             if (!warp_wait(p, &h.full[r.at], r.phase, abort)) break;
-            const uint32_t stage = ring + r.at * kStage;
+            const uint32_t stage = ring + r.at * stage_bytes;
             // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
             // neighbouring threads take one chunk of eight rows (eight
             // different bank groups, read and written).
@@ -689,8 +679,8 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if (lane == 0) mbar_arrive(smem_addr(&h.empty[r.at]));
             if (!warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort)) break;
             tcgen05_fence_after();
-            tmem_store32(tmem + lanes + kWide + c.at * kSlotColumns, w);
-            const uint32_t slot = slots + c.at * kSlot + x_row * 128;
+            tmem_store32(wide + lanes + c.at * kSlotColumns + upper * (kSlotColumns / 2), w);
+            const uint32_t slot = slots + c.at * slot_bytes + upper * (slot_bytes / 2) + x_row * 128;
 #pragma unroll
             for (int i = 0; i < kTokenChunks; ++i)
                 if (i * 32 + x_row0 < bn_cta) {
@@ -706,9 +696,11 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive_pair(map_to_rank(smem_addr(&h.wide_full[c.at]), lead));
-            const int step = (upper + kGroups) / 2;  // stages on to unit u + kGroups
-            for (int i = 0; i < step; ++i) r.next(S);
-            for (int i = 0; i < kGroups; ++i) c.next(kSlots);
+#pragma unroll
+            for (int i = 0; i < kGroups / 2; ++i) {
+                r.next(n_stages);
+                c.next(n_slots);
+            }
         }
     }
     __syncwarp();
@@ -769,7 +761,7 @@ void cluster_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, int clus
                     int cg, bool int8) {
     cfg->gridDim = dim3(static_cast<unsigned>(grid));
     cfg->blockDim = dim3(int8 ? 256 + 128 * kGroups : 256);
-    cfg->dynamicSmemBytes = smem_bytes(cg, int8);
+    cfg->dynamicSmemBytes = kSmemBytes;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
     attr[0].val.clusterDim.y = 1;
@@ -815,8 +807,8 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
                 if (units < 1 || (split > 1 && c.tiles > units)) break;
                 // Whole chunks of the output's staging, or eights of a share.
                 if (bn % (split == 1 ? 32 : 8 * split) != 0) continue;
-                // A join holds its tile twice in the ring.
-                if (split > 1 && bn * kRows * 8 > stages(cg, int8) * stage_bytes(cg, int8)) break;
+                // A join holds its tile twice in the pool.
+                if (split > 1 && bn * kRows * 8 > kPoolBytes) break;
                 const int64_t waves = (c.tiles + units - 1) / units;
                 c.split = split;
                 const double main =
@@ -833,14 +825,14 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
 }  // namespace
 
 int gemm_prepare(int smem_optin, int (*clusters)[2][4]) {
+    if (kSmemBytes > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
     for (int cg = 1; cg <= 2; ++cg)
         for (bool int8 : {false, true}) {
-            if (smem_bytes(cg, int8) > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
             cudaError_t e;
             for (bool split : {false, true})
                 if ((e = cudaFuncSetAttribute(gemm_kernel_for(cg, int8, split),
                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              smem_bytes(cg, int8))) != cudaSuccess)
+                                              kSmemBytes)) != cudaSuccess)
                     return static_cast<int>(e);
             // Clusters of 1, 2, 4 and 8 CTAs that run at once (they do not
             // cross a GPC, so a few SMs can be out of reach).
@@ -887,6 +879,15 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.channel_tiles = static_cast<int>(c.tiles / c.token_tiles);
     p.split = c.split;
     p.bn = c.bn;
+    // As many slots as TMEM has room for behind the accumulators, then as many
+    // stages as fit.
+    p.acc_columns = c.bn < 32 ? 32 : c.bn;
+    p.stage_bytes = (kRows + c.bn / cg) * kBlockK;
+    p.slot_bytes = c.bn / cg * kBlockK * 2;
+    p.slots = int8 ? (kTmemColumns - 2 * p.acc_columns) / kSlotColumns : 0;
+    if (p.slots > kWideSlots) p.slots = kWideSlots;
+    p.stages = (kPoolBytes - p.slots * p.slot_bytes) / p.stage_bytes;
+    if (p.stages > kRingStages) p.stages = kRingStages;
     const int64_t es = p.f32 ? 4 : 2;
     p.tma_out = g.N * es % 16 == 0 && p.bn / p.split % (p.f32 ? 16 : 32) == 0;
     CUtensorMap x_map, w_map, out_map{};

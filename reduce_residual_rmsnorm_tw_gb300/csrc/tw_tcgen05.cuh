@@ -113,15 +113,15 @@ __device__ __forceinline__ void fence_async_shared() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
 
-// One lane of a whole warp (always the same one).
-__device__ __forceinline__ bool elect_one() {
+// 1 in one lane of a whole warp (always the same one), 0 in the others.
+__device__ __forceinline__ uint32_t elect_one() {
     uint32_t one;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "elect.sync _|p, 0xffffffff;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(one));
-    return one != 0;
+    return one;
 }
 
 // ----------------------------------------------------------------- TMA ---
@@ -271,55 +271,62 @@ __device__ __forceinline__ uint64_t smem_operand(uint32_t addr) {
 __device__ __forceinline__ uint32_t mma_shape(uint32_t m, uint32_t n) {
     return (1u << 4) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
+// The whole warp calls what follows; the lane whose `one` is not zero (exactly
+// one: elect_one) issues.  As a predicate rather than a branch, so that the
+// operands stay in the warp's uniform registers.
+//
 // D (TMEM) = A (TMEM, f16) * B (shared memory, f16) + D where `add`.
 template <int CG>
 __device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape,
-                                             bool add) {
+                                             bool add, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
             : "memory");
 }
 // D (TMEM) = A * B (both shared memory, e4m3) + D where `add`.
 template <int CG>
 __device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t shape,
-                                         bool add) {
+                                         bool add, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add))
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
             : "memory");
 }
 // Arrive on `bar` (CG 2: on the barrier at that offset in both CTAs of the
-// pair, the bits of `pair` being their ranks) once this thread's MMAs so far
-// are complete.
+// pair, the bits of `pair` being their ranks) once the issuing lane's MMAs so
+// far are complete.
 template <int CG>
-__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t pair) {
+__device__ __forceinline__ void mma_commit(uint32_t bar, uint16_t pair, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                bar)
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::
+                "r"(bar),
+            "r"(one)
             : "memory");
     else
         asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
-            ".multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"(pair)
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster"
+            ".multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+            "h"(pair), "r"(one)
             : "memory");
 }
 
