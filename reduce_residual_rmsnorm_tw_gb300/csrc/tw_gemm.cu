@@ -39,6 +39,8 @@ constexpr int kTmemColumns = 512;
 // Warp roles: 0 TMA, 1 MMA, 2 (split K) tells the cluster that the products are
 // done, 4-7 epilogue, from 8 on kGroups of four widen (int8).
 constexpr int kGroups = 4;
+// Groups two apart work on neighbouring stages and slots (Ring::skip).
+static_assert((kTmemColumns - 2 * 192) / kSlotColumns >= kGroups / 2, "too few slots");
 constexpr int kAnnounceWarp = 2, kEpilogueWarp = 4, kWidenWarp = 8;
 
 // Largest token tile: a unit's two accumulators (and, for int8, two slots of
@@ -95,6 +97,14 @@ struct Ring {
     __device__ __forceinline__ void next(uint32_t n) {
         if (++at == n) {
             at = 0;
+            phase ^= 1u;
+        }
+    }
+    // On by k places, k <= n.
+    __device__ __forceinline__ void skip(uint32_t k, uint32_t n) {
+        at += k;
+        if (at >= n) {
+            at -= n;
             phase ^= 1u;
         }
     }
@@ -482,9 +492,11 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         }
     } else if (warp == 1 && leader) {
         // ------------------------------------------------------- MMA -----
-        // The whole warp walks the slices and one elected lane issues: with
-        // the operands in warp-uniform code a slice's four MMAs issue in a
-        // fraction of the time a lone lane takes.
+        // The whole warp walks the stages and one elected lane issues: with
+        // the operands in warp-uniform code a stage's MMAs issue in a fraction
+        // of the time a lone lane takes.  (int8: beside sixteen widening warps
+        // every instruction of this one counts; one hand-over per 128 elements
+        // of K instead of 64 took 512 x 8192 x 8192 from 62.6 to 57.1 us.)
         Ring r, acc;
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
@@ -497,43 +509,32 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if (!ok) break;
             tcgen05_fence_after();
             const uint32_t d = tmem + acc.at * acc_columns;
-            // Whether the next slice is there is asked while this one's products
-            // issue: an answer takes about 100 clocks, a slice's products 300.
-            bool there = false;
             if constexpr (INT8) {
                 const int n = kb1 - kb0;
-                for (int k = 0; k < n; ++k) {
-                    if (!there) ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
+                for (int k = 0; k < n; ++k, r.next(n_slots)) {
+                    ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t at = r.at;
-                    r.next(n_slots);
-                    there = k + 1 < n && mbar_test(smem_addr(&h.wide_full[r.at]), r.phase);
-                    const uint64_t b = slot_operand + at * (slot_bytes >> 4);
-                    const uint32_t a = wide + at * kSlotColumns;
+                    const uint64_t b = slot_operand + r.at * (slot_bytes >> 4);
+                    const uint32_t a = wide + r.at * kSlotColumns;
 #pragma unroll
                     for (int i = 0; i < kBlockK / 16; ++i)
                         mma_f16_tmem<CG>(d, a + 8 * i, b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4),
                                          shape, k > 0 || i > 0, one);
-                    mma_commit<CG>(smem_addr(&h.wide_empty[at]), pair, one);
-                    there = __all_sync(0xffffffffu, there);
+                    mma_commit<CG>(smem_addr(&h.wide_empty[r.at]), pair, one);
                 }
             } else {
                 const int n = kb1 - kb0;
-                for (int k = 0; k < n; ++k) {
-                    if (!there) ok = warp_wait(p, &h.full[r.at], r.phase, abort);
+                for (int k = 0; k < n; ++k, r.next(n_stages)) {
+                    ok = warp_wait(p, &h.full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t at = r.at;
-                    r.next(n_stages);
-                    there = k + 1 < n && mbar_test(smem_addr(&h.full[r.at]), r.phase);
-                    const uint64_t a = ring_operand + at * (stage_bytes >> 4);
+                    const uint64_t a = ring_operand + r.at * (stage_bytes >> 4);
                     const uint64_t b = a + (kRows * kBlockK >> 4);
 #pragma unroll
                     for (int i = 0; i < kBlockK / 32; ++i)
                         mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0, one);
-                    mma_commit<CG>(smem_addr(&h.empty[at]), pair, one);
-                    there = __all_sync(0xffffffffu, there);
+                    mma_commit<CG>(smem_addr(&h.empty[r.at]), pair, one);
                 }
             }
             if (ok) mma_commit<CG>(smem_addr(&h.acc_full[acc.at]), pair, one);
@@ -648,30 +649,34 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         constexpr int kTokenChunks = max_tokens(CG, true) / CG / 32;
         const int x_row0 = row / 32 * 8, x_row = x_row0 + (row & 7), x_chunk = row / 8 % 4;
         const uint32_t lanes = static_cast<uint32_t>(row / 32 * 32) << 16;
+        // Where this thread reads in a stage (16-byte chunk i of row R lies at
+        // chunk i ^ (R & 7): neighbouring chunks are an exclusive or of 16
+        // apart) and writes in a slot.  Eight neighbouring threads take one
+        // chunk of eight rows: eight different bank groups, read and written.
+        const uint32_t w_at = row * kBlockK + (((upper * 4) ^ (row & 7)) << 4);
+        const uint32_t x_at = kRows * kBlockK + x_row * kBlockK +
+                              (((upper * 4 + x_chunk) ^ (x_row & 7)) << 4);
+        const uint32_t slot_at = slots + upper * (slot_bytes / 2) + x_row * 128 +
+                                 (((2 * x_chunk) ^ (x_row & 7)) << 4);
+        const uint32_t wide_at = wide + lanes + upper * (kSlotColumns / 2);
+        const uint32_t full_to = map_to_rank(smem_addr(&h.wide_full[0]), lead);
         Ring r, c;  // of stages, of slots
         const int first = static_cast<int>(unit);
         const int my_tiles =
             first < p.tiles ? (p.tiles - 1 - first) / static_cast<int>(units) + 1 : 0;
         const int64_t n = static_cast<int64_t>(my_tiles) * (kb1 - kb0);
-        if (group >= 2) {
-            r.next(n_stages);
-            c.next(n_slots);
-        }
+        r.skip(group / 2, n_stages);
+        c.skip(group / 2, n_slots);
         for (int64_t k = group / 2; k < n; k += kGroups / 2) {
             if (!warp_wait(p, &h.full[r.at], r.phase, abort)) break;
             const uint32_t stage = ring + r.at * stage_bytes;
-            // 16-byte chunk i of row R lies at chunk i ^ (R & 7).  Eight
-            // neighbouring threads take one chunk of eight rows (eight
-            // different bank groups, read and written).
             uint4 raw[4 + kTokenChunks];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                raw[i] = lds16(stage + row * kBlockK + (((upper * 4 + i) ^ (row & 7)) << 4));
+            for (int i = 0; i < 4; ++i) raw[i] = lds16((stage + w_at) ^ (i << 4));
 #pragma unroll
             for (int i = 0; i < kTokenChunks; ++i)
                 if (i * 32 + x_row0 < bn_cta)
-                    raw[4 + i] = lds16(stage + kRows * kBlockK + (i * 32 + x_row) * kBlockK +
-                                       (((upper * 4 + x_chunk) ^ (x_row & 7)) << 4));
+                    raw[4 + i] = lds16(stage + x_at + i * 32 * kBlockK);
             uint32_t w[32];
 #pragma unroll
             for (int i = 0; i < 4; ++i) widen16(raw[i], w + 8 * i);
@@ -679,28 +684,23 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if (lane == 0) mbar_arrive(smem_addr(&h.empty[r.at]));
             if (!warp_wait(p, &h.wide_empty[c.at], c.phase ^ 1u, abort)) break;
             tcgen05_fence_after();
-            tmem_store32(wide + lanes + c.at * kSlotColumns + upper * (kSlotColumns / 2), w);
-            const uint32_t slot = slots + c.at * slot_bytes + upper * (slot_bytes / 2) + x_row * 128;
+            tmem_store32(wide_at + c.at * kSlotColumns, w);
+            const uint32_t slot = slot_at + c.at * slot_bytes;
 #pragma unroll
             for (int i = 0; i < kTokenChunks; ++i)
                 if (i * 32 + x_row0 < bn_cta) {
                     uint32_t x[8];
                     widen16(raw[4 + i], x);
-                    const uint32_t to = slot + i * 32 * 128;
-                    sts16(to + (((2 * x_chunk) ^ (x_row & 7)) << 4), x);
-                    sts16(to + (((2 * x_chunk + 1) ^ (x_row & 7)) << 4), x + 4);
+                    sts16(slot + i * 32 * 128, x);
+                    sts16((slot + i * 32 * 128) ^ 16, x + 4);
                 }
             fence_async_shared();
             tmem_wait_stores();
             tcgen05_fence_before();
             __syncwarp();
-            if (lane == 0)
-                mbar_arrive_pair(map_to_rank(smem_addr(&h.wide_full[c.at]), lead));
-#pragma unroll
-            for (int i = 0; i < kGroups / 2; ++i) {
-                r.next(n_stages);
-                c.next(n_slots);
-            }
+            if (lane == 0) mbar_arrive_pair(full_to + c.at * 8);
+            r.skip(kGroups / 2, n_stages);
+            c.skip(kGroups / 2, n_slots);
         }
     }
     __syncwarp();
@@ -780,10 +780,10 @@ struct Plan {
 // (fitted to sweeps of every cut over 13 shapes from 16 x 8192 x 1024 to
 // 1024 x 8192 x 8192; the cut taken was within 15 % of the best of each).
 //   A ring stage costs what a unit's hand-overs of it do, plus its products:
-//   int8 760 + bn for a pair, 670 + 2.5 bn for a lone CTA; e4m3 390 + 0.85 bn
-//   and 375 + 0.8 bn; together never less than reading W and x once.
+//   int8 560 + 1.9 bn for a pair, 590 + 2 bn for a lone CTA; e4m3 390 + 0.85 bn
+//   and 390 + 0.8 bn; together never less than reading W and x once.
 //   The last tile's way out adds 14 clocks per column, a split the join of its
-//   shares (int8 6000 + 15 bn, e4m3 3000 + 15 bn).
+//   shares (int8 6500 + 20 bn, e4m3 4000 + 15 bn).
 Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const DeviceInfo& d) {
     Plan best;
     // 6.3 TB/s at 1.9 GHz: 3300 bytes a clock.
@@ -798,8 +798,9 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
             c.bn = bn;
             c.token_tiles = (M + bn - 1) / bn;
             c.tiles = channel_tiles * c.token_tiles;
-            const double stage = int8 ? (cg == 2 ? 760.0 + 1.0 * bn : 670.0 + 2.5 * bn)
-                                      : (cg == 2 ? 390.0 + 0.85 * bn : 375.0 + 0.8 * bn);
+            const double stage = int8 ? (cg == 2 ? 560.0 + 1.9 * bn : 590.0 + 2.0 * bn)
+                                      : (cg == 2 ? 390.0 + 0.85 * bn : 390.0 + 0.8 * bn);
+            const double join = int8 ? 6500.0 + 20.0 * bn : 4000.0 + 15.0 * bn;
             for (int split = 1, log2 = cg - 1; log2 < 4 && split <= k_blocks; split *= 2, ++log2) {
                 int64_t units = sms >> log2;
                 const int at_once = d.gemm_clusters[cg - 1][int8][log2];
@@ -814,7 +815,7 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
                 const double main =
                     static_cast<double>(waves * ((k_blocks + split - 1) / split)) * stage;
                 c.cost = (main > once ? main : once) + 14.0 * bn +
-                         (split > 1 ? (int8 ? 6000.0 : 3000.0) + 15.0 * bn : 0.0);
+                         (split > 1 ? join : 0.0);
                 if (best.cg == 0 || c.cost < best.cost) best = c;
             }
         }
@@ -886,6 +887,7 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.slot_bytes = c.bn / cg * kBlockK * 2;
     p.slots = int8 ? (kTmemColumns - 2 * p.acc_columns) / kSlotColumns : 0;
     if (p.slots > kWideSlots) p.slots = kWideSlots;
+    // (Two slots at bn = 192, five stages.)
     p.stages = (kPoolBytes - p.slots * p.slot_bytes) / p.stage_bytes;
     if (p.stages > kRingStages) p.stages = kRingStages;
     const int64_t es = p.f32 ? 4 : 2;

@@ -65,18 +65,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
         : "memory");
     return done != 0;
 }
-// Whether the phase is complete, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
 // As mbar_wait, for the waits of a product's slices: the abort flag and the
 // clock are looked at once in 64 tries.  CLUSTER: see what the cluster's other
 // CTAs released (their writes into this CTA's shared memory); without it the
