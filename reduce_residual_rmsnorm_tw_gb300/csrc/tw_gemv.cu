@@ -16,10 +16,11 @@
 //         simply the 16 bytes it loaded: lane (g, q) holds bytes 16 q ..
 //         16 q + 15 of a 64-byte block of rows g and g + 8 of W and of token g,
 //         and the four MMAs of the block use four K elements of them each.
-// x 8192 x 8192 in int8: one token 12.7 us by DOT and 15.6 by MMA, eight
-// tokens 18.1 and 16.0 (the integer MMA is slow on this GPU: 15.0).
+// x 8192 x 8192 in int8: one token 12.2 us (5.5 TB/s, 81 % of the measured copy
+// rate; 32768 channels 42.4 us, 6.3 TB/s) by DOT against 15.6 by MMA, eight
+// tokens 15.7 by MMA against 18.1 (the integer MMA, slow on this GPU: 15.0).
 //
-// A CTA owns 16 R channels; its 16 warps take the 64-byte blocks of K in turn
+// A CTA owns 16 R channels; its warps take the 64-byte blocks of K in turn
 // (so that the CTA reads long contiguous pieces of a row) and add their sums up
 // through shared memory in warp order.
 #include <cuda_fp16.h>
@@ -31,7 +32,6 @@
 namespace tw {
 namespace {
 
-constexpr int kWarps = 16;
 constexpr int kBlock = 64;  // bytes of K per block
 
 // Sixteen 8-bit values as f16 (exact), in an order that is the same for W and
@@ -118,20 +118,27 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
 // of W per lane and one of x.
 __host__ __device__ constexpr int ahead(int r) { return r == 2 ? 4 : 7; }
 __host__ __device__ constexpr int step_bytes(int r) { return (2 * r + 1) * 32 * 16; }
-__host__ __device__ constexpr int fifo_bytes(int r) { return kWarps * ahead(r) * step_bytes(r); }
-__host__ __device__ constexpr int gemv_smem(int r) {
-    return fifo_bytes(r) + kWarps * 8 * (16 * r + 1) * 4;
+__host__ __device__ constexpr int fifo_bytes(int warps, int r) {
+    return warps * ahead(r) * step_bytes(r);
+}
+__host__ __device__ constexpr int gemv_smem(int warps, int r) {
+    return fifo_bytes(warps, r) + warps * 8 * (16 * r + 1) * 4;
 }
 
-// MT: at most this many tokens (1, 2, 4: DOT; 8: MMA); R: 16-channel tiles per CTA.
+// MT: at most this many tokens (1, 2, 4: DOT; 8: MMA); R: 16-channel tiles per
+// CTA; kWarps: 8, two CTAs to an SM, or 16, one.  Two smaller CTAs keep the SM
+// reading while one reduces a group, and the next launch's start beside the
+// last groups (one token int8, 8192 x 1024: 5.1 -> 4.1 us, 5120 x 5120:
+// 8.2 -> 6.9 us); one of 16 where there are not enough channel groups for two
+// (4096 x 4096: 5.0 us against 5.4), and under an SM budget.
 //
 // The bytes in flight are what the HBM rate follows, so the loads go through a
 // FIFO in shared memory instead of registers, `ahead` steps deep: 128 KB of W
 // per SM.  Each lane reads back the pieces of W it copied itself.  The steps
 // run on across the CTA's channel groups, so that a group's reduction does not
 // drain the FIFO.
-template <bool INT8, int MT, int R>
-__global__ void __launch_bounds__(32 * kWarps, 1)
+template <bool INT8, int MT, int R, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, 16 / kWarps)
     gemv_kernel(const __grid_constant__ GemmArgs g) {
     constexpr bool DOT = INT8 && MT < 8;
     static_assert(DOT || MT == 8, "the MMA's tokens come in eights");
@@ -139,7 +146,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     constexpr int kChannels = 16 * R, D = ahead(R);
     extern __shared__ __align__(16) unsigned char smem[];
     Sum(*part)[MT][kChannels + 1] =
-        reinterpret_cast<Sum(*)[MT][kChannels + 1]>(smem + fifo_bytes(R));
+        reinterpret_cast<Sum(*)[MT][kChannels + 1]>(smem + fifo_bytes(kWarps, R));
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int row = lane / 4, piece = warp * kBlock + lane % 4 * 16;
     const int M = static_cast<int>(g.M), K = static_cast<int>(g.K);
@@ -258,21 +265,22 @@ __global__ void __launch_bounds__(32 * kWarps, 1)
     }
 }
 
-// The instantiation for mt = 1, 2, 4, 8 tokens and r = 1, 2 tiles.
-void* gemv_kernel_for(bool int8, int mt, int r) {
-    if (!int8)
-        return r == 1 ? reinterpret_cast<void*>(&gemv_kernel<false, 8, 1>)
-                      : reinterpret_cast<void*>(&gemv_kernel<false, 8, 2>);
-    switch (mt * 4 + r) {
-        case 1 * 4 + 1: return reinterpret_cast<void*>(&gemv_kernel<true, 1, 1>);
-        case 1 * 4 + 2: return reinterpret_cast<void*>(&gemv_kernel<true, 1, 2>);
-        case 2 * 4 + 1: return reinterpret_cast<void*>(&gemv_kernel<true, 2, 1>);
-        case 2 * 4 + 2: return reinterpret_cast<void*>(&gemv_kernel<true, 2, 2>);
-        case 4 * 4 + 1: return reinterpret_cast<void*>(&gemv_kernel<true, 4, 1>);
-        case 4 * 4 + 2: return reinterpret_cast<void*>(&gemv_kernel<true, 4, 2>);
-        case 8 * 4 + 1: return reinterpret_cast<void*>(&gemv_kernel<true, 8, 1>);
-        default: return reinterpret_cast<void*>(&gemv_kernel<true, 8, 2>);
+template <int R, int WARPS>
+void* gemv_entry(bool int8, int mt) {
+    if (!int8) return reinterpret_cast<void*>(&gemv_kernel<false, 8, R, WARPS>);
+    switch (mt) {
+        case 1: return reinterpret_cast<void*>(&gemv_kernel<true, 1, R, WARPS>);
+        case 2: return reinterpret_cast<void*>(&gemv_kernel<true, 2, R, WARPS>);
+        case 4: return reinterpret_cast<void*>(&gemv_kernel<true, 4, R, WARPS>);
+        default: return reinterpret_cast<void*>(&gemv_kernel<true, 8, R, WARPS>);
     }
+}
+
+// The instantiation for mt = 1, 2, 4, 8 tokens, r = 1, 2 tiles and 8 or 16
+// warps.
+void* gemv_kernel_for(bool int8, int mt, int r, int warps) {
+    if (warps == 8) return r == 1 ? gemv_entry<1, 8>(int8, mt) : gemv_entry<2, 8>(int8, mt);
+    return r == 1 ? gemv_entry<1, 16>(int8, mt) : gemv_entry<2, 16>(int8, mt);
 }
 
 }  // namespace
@@ -280,27 +288,32 @@ void* gemv_kernel_for(bool int8, int mt, int r) {
 int gemv_prepare(int smem_optin) {
     for (bool int8 : {false, true})
         for (int mt = 1; mt <= 8; mt *= 2)
-            for (int r = 1; r <= 2; ++r) {
-                if (gemv_smem(r) > smem_optin) return static_cast<int>(cudaErrorInvalidValue);
-                cudaError_t e = cudaFuncSetAttribute(gemv_kernel_for(int8, mt, r),
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     gemv_smem(r));
-                if (e != cudaSuccess) return static_cast<int>(e);
-            }
+            for (int r = 1; r <= 2; ++r)
+                for (int warps = 8; warps <= 16; warps *= 2) {
+                    if (gemv_smem(warps, r) > smem_optin)
+                        return static_cast<int>(cudaErrorInvalidValue);
+                    cudaError_t e = cudaFuncSetAttribute(
+                        gemv_kernel_for(int8, mt, r, warps),
+                        cudaFuncAttributeMaxDynamicSharedMemorySize, gemv_smem(warps, r));
+                    if (e != cudaSuccess) return static_cast<int>(e);
+                }
     return 0;
 }
 
 int launch_gemv(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream) {
     const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
+    const bool whole = max_sms >= d.sm_count;
     int mt = 1;
     while (mt < g.M) mt *= 2;
     // Two channel tiles per CTA halve what each channel pays for x; one where
     // that leaves SMs without work.
     const int r = g.N > 16 * sms ? 2 : 1;
+    const int warps = whole && g.N > 32 * sms ? 8 : 16;
     const int64_t groups = (g.N + 16 * r - 1) / (16 * r);
-    const int grid = static_cast<int>(groups < sms ? groups : sms);
-    return launch_with_pdl(gemv_kernel_for(g.qtype == TW_INT8, mt, r), g, grid, 32 * kWarps,
-                           gemv_smem(r), max_sms >= d.sm_count, stream);
+    const int64_t most = warps == 8 ? 2 * sms : sms;
+    const int grid = static_cast<int>(groups < most ? groups : most);
+    return launch_with_pdl(gemv_kernel_for(g.qtype == TW_INT8, mt, r, warps), g, grid, 32 * warps,
+                           gemv_smem(warps, r), whole, stream);
 }
 
 }  // namespace tw
