@@ -118,12 +118,20 @@ __device__ __forceinline__ void gave_up(const GemmParams& p, volatile int* abort
 // A whole warp's wait: all lanes go on or all give up, so that the warp stays
 // whole for the .aligned instructions that follow.
 template <bool CLUSTER = false>
-__device__ __forceinline__ bool warp_wait(const GemmParams& p, uint64_t* bar, uint32_t parity,
-                                          volatile int* abort) {
-    const bool ok = mbar_wait_slice<CLUSTER>(smem_addr(bar), parity, abort);
+__device__ __noinline__ bool warp_wait_slow(const GemmParams& p, uint32_t bar, uint32_t parity,
+                                            volatile int* abort) {
+    const bool ok = mbar_wait_slice<CLUSTER>(bar, parity, abort);
     if (__all_sync(0xffffffffu, ok)) return true;
     gave_up(p, abort);
     return false;
+}
+template <bool CLUSTER = false>
+__device__ __forceinline__ bool warp_wait(const GemmParams& p, uint64_t* bar, uint32_t parity,
+                                          volatile int* abort) {
+    const uint32_t at = smem_addr(bar);
+    // Mostly there already: a try and a vote.
+    if (!CLUSTER && __all_sync(0xffffffffu, mbar_try_wait(at, parity))) return true;
+    return warp_wait_slow<CLUSTER>(p, at, parity, abort);
 }
 
 // Four int8 as two pairs of f16.
