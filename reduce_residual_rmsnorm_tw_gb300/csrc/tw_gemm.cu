@@ -13,8 +13,9 @@
 //   int8  sm_103a has no integer tcgen05.  Integers to 2^11 are exact in f16
 //         and the products accumulate in fp32, so the operands are widened to
 //         f16 on the way: W into TMEM (the MMA's A operand may live there, and
-//         shared memory, which bounds this kernel, sees W once in 8 bits
-//         instead of three times), x into a second ring in shared memory.
+//         shared memory sees W once, in 8 bits: its write and two reads by
+//         the MMAs of a pair in 16 bits fall away), x into a second ring in
+//         shared memory.
 //         f16 rather than bf16, whose 8 bits of mantissa hold -128..127 as
 //         well, because one byte permute and one packed subtract make an
 //         f16: 0x6400 | (v + 128) is 1024 + 128 + v.
@@ -22,6 +23,18 @@
 // With fewer tiles than SMs a cluster of S units splits K, and each adds up its
 // share of the token columns from all S accumulators, copied into its shared
 // memory by the others (and added in rank order: the same bits every time).
+//
+// Measured (N = K = 8192, bf16 out, inputs in HBM or L2 as a loop leaves them):
+//   tokens       16     64    512   1024   4096
+//   int8       17.5   19.1     52     94    335  us
+//   e4m3       14.4   14.9     25     46    190  us
+// What bounds it: at 16 and 64 tokens the 67 MB of weights (4.7 TB/s in e4m3 with
+// launch, ramp and join in the time).  e4m3 at 4096 tokens (2.8 to 3.0 PFLOP/s):
+// the board's power, which takes the SM clock to 1.5 to 1.6 GHz; a stage's MMAs
+// take 520 clocks of their ideal 512.  e4m3 at 1024: 1.7 waves of tiles on 76
+// pairs, run as two.  int8 (1.4 to 1.6 PFLOP/s, f16's rate being 2): the widening,
+// a chain of shared loads, permutes, TMEM and shared stores of about 1880 clocks
+// per group and stage, 82 % of the MMAs' pace in long calls.
 #include <cuda.h>
 
 #include "tw_tcgen05.cuh"
@@ -527,8 +540,9 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     const uint32_t a = wide + r.at * kSlotColumns;
 #pragma unroll
                     for (int i = 0; i < kBlockK / 16; ++i)
-                        mma_f16_tmem<CG>(d, a + 8 * i, b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4),
-                                         shape, k > 0 || i > 0, one);
+                        mma_f16_tmem<CG>(d, a + 8 * i,
+                                         b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4), shape,
+                                         k > 0 || i > 0, one);
                     mma_commit<CG>(smem_addr(&h.wide_empty[r.at]), pair, one);
                 }
             } else {

@@ -16,7 +16,7 @@ constexpr int kQuantThreads = 256;
 
 // AHEAD: a CTA keeps the next row's loads in flight while it reduces and
 // stores one (launches held to few SMs, whose CTAs are alone there: 512 x 8192
-// on 8 SMs 67 -> 47 us; with eight CTAs on an SM the others do that already,
+// on 8 SMs 67 -> 42 us; with eight CTAs on an SM the others do that already,
 // and the registers cost 3 %).
 template <typename T, int VPT, int W, bool AHEAD>
 __global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)

@@ -32,8 +32,8 @@ SHAPES = [(1, 128, 128), (1, 1, 16), (2, 7, 48), (3, 8192, 1024), (8, 1000, 8192
           (64, 1024, 8192), (65, 127, 128), (100, 257, 2064), (128, 128, 128),
           (129, 300, 528), (192, 384, 256), (193, 255, 1008), (250, 999, 16), (256, 256, 384),
           (257, 513, 640), (333, 4090, 5120), (700, 96, 32), (1024, 1024, 1024),
-          (4, 37, 65536), (12, 256, 8192), (40, 200, 8192), (64, 128, 4096), (90, 640, 8192),
-          (120, 2048, 2048), (128, 1032, 6160), (300, 700, 8192), (600, 130, 4112),
+          (4, 37, 65536), (20, 40, 65536), (12, 256, 8192), (40, 200, 8192), (64, 128, 4096),
+          (90, 640, 8192), (120, 2048, 2048), (128, 1032, 6160), (300, 700, 8192), (600, 130, 4112),
           (2000, 264, 512), (1500, 4104, 256)]
 
 
