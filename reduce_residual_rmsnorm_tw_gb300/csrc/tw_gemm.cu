@@ -903,15 +903,22 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.split = c.split;
     p.bn = c.bn;
     // As many slots as TMEM has room for behind the accumulators, then as many
-    // stages as fit.
+    // stages as fit (two slots and five stages at bn = 192).
     p.acc_columns = c.bn < 32 ? 32 : c.bn;
     p.stage_bytes = (kRows + c.bn / cg) * kBlockK;
     p.slot_bytes = c.bn / cg * kBlockK * 2;
     p.slots = int8 ? (kTmemColumns - 2 * p.acc_columns) / kSlotColumns : 0;
     if (p.slots > kWideSlots) p.slots = kWideSlots;
-    // (Two slots at bn = 192, five stages.)
-    p.stages = (kPoolBytes - p.slots * p.slot_bytes) / p.stage_bytes;
-    if (p.stages > kRingStages) p.stages = kRingStages;
+    for (;; --p.slots) {
+        p.stages = (kPoolBytes - p.slots * p.slot_bytes) / p.stage_bytes;
+        if (p.stages > kRingStages) p.stages = kRingStages;
+        // An odd number of stages hands a place of the ring from one pair of
+        // widening groups to the other, and a wait by parity must not look at
+        // it before the other's load k has landed.  Who is about to widen
+        // stage k + stages has seen the products of k + stages - 2 - slots
+        // done, which must not lie before k.
+        if (!int8 || p.stages % 2 == 0 || p.stages >= p.slots + 2) break;
+    }
     const int64_t es = p.f32 ? 4 : 2;
     p.tma_out = g.N * es % 16 == 0 && p.bn / p.split % (p.f32 ? 16 : 32) == 0;
     CUtensorMap x_map, w_map, out_map{};
