@@ -49,12 +49,13 @@ constexpr int kSlotColumns = kBlockK / 2;
 constexpr int kRingStages = 12;
 constexpr int kTmemColumns = 512;
 
-// Warp roles: 0 TMA, 1 MMA, 2 (split K) tells the cluster that the products are
-// done, 4-7 epilogue, from 8 on kGroups of four widen (int8).
+// Warp roles: 0 loads W, 1 MMA, 2 (split K) tells the cluster that the products
+// are done, 3 loads x, 4-7 epilogue, from 8 on kGroups of four widen (int8).
 constexpr int kGroups = 4;
 // Groups two apart work on neighbouring stages and slots (Ring::skip).
 static_assert((kTmemColumns - 2 * 192) / kSlotColumns >= kGroups / 2, "too few slots");
-constexpr int kAnnounceWarp = 2, kEpilogueWarp = 4, kWidenWarp = 8;
+constexpr int kWeightWarp = 0, kAnnounceWarp = 2, kTokenWarp = 3, kEpilogueWarp = 4,
+              kWidenWarp = 8;
 
 // Largest token tile: a unit's two accumulators (and, for int8, two slots of
 // widened W) share 512 TMEM columns; a single CTA takes short tiles only.
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
 
     if (threadIdx.x == 0) {
         for (uint32_t s = 0; s < n_stages; ++s) {
-            mbar_init(smem_addr(&h.full[s]), 1);
+            mbar_init(smem_addr(&h.full[s]), 2);  // W, x
             mbar_init(smem_addr(&h.empty[s]), INT8 ? 8 : 1);
         }
         for (int c = 0; c < kWideSlots; ++c) {
@@ -469,36 +470,37 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    if (warp == 0 && lane == 0) {
+    if (warp == kWeightWarp || warp == kTokenWarp) {
         // ------------------------------------------------------- TMA -----
+        // One warp loads W, one x.  As in the MMA warp, the whole warp walks
+        // and one lane issues.
+        const bool weights = warp == kWeightWarp;
+        const CUtensorMap* map = weights ? &w_map : &x_map;
+        const uint32_t place = ring + (weights ? 0 : kRows * kBlockK);
+        const uint32_t bytes = static_cast<uint32_t>((weights ? kRows : bn_cta) * kBlockK);
+        const uint32_t one = elect_one();
         Ring r;
         uint32_t issued = 0;
         bool ok = true;
-        const uint32_t bytes = static_cast<uint32_t>((kRows + bn_cta) * kBlockK);
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles); tile += units) {
-            const int channel = static_cast<int>(tile % p.channel_tiles) * (kRows * CG) +
-                                half * kRows;
-            const int token = static_cast<int>(tile / p.channel_tiles) * p.bn +
-                              half * bn_cta;
+            const int row = weights ? static_cast<int>(tile % p.channel_tiles) * (kRows * CG) +
+                                          half * kRows
+                                    : static_cast<int>(tile / p.channel_tiles) * p.bn +
+                                          half * bn_cta;
             for (int kb = kb0; kb < kb1; ++kb, ++issued, r.next(n_stages)) {
-                if (!mbar_wait_slice(smem_addr(&h.empty[r.at]), r.phase ^ 1u, abort)) {
-                    gave_up(p, abort);
-                    ok = false;
-                    break;
-                }
+                ok = warp_wait(p, &h.empty[r.at], r.phase ^ 1u, abort);
+                if (!ok) break;
                 // e4m3 pairs: both CTAs' copies count on the leader's barrier,
                 // which alone issues the products; int8: on this CTA's, whose
                 // warps widen them.
                 const uint32_t local = smem_addr(&h.full[r.at]);
                 const uint32_t bar = CG == 2 && !INT8 ? map_to_rank(local, lead) : local;
-                if (INT8 || leader) mbar_arrive_expect_tx(local, INT8 ? bytes : bytes * CG);
-                const uint32_t dst = ring + r.at * stage_bytes;
-                tma_load_2d<INT8 ? 1 : CG>(dst, &w_map, kb * kBlockK, channel, bar);
-                tma_load_2d<INT8 ? 1 : CG>(dst + kRows * kBlockK, &x_map, kb * kBlockK, token,
-                                           bar);
+                if (INT8 || leader) mbar_arrive_expect_tx(local, INT8 ? bytes : bytes * CG, one);
+                tma_load_2d<INT8 ? 1 : CG>(place + r.at * stage_bytes, map, kb * kBlockK, row,
+                                           bar, one);
             }
         }
-        if (*abort && (INT8 || leader)) {
+        if (lane == 0 && *abort && (INT8 || leader)) {
             // The copies in flight must land before the CTA may leave.
             for (uint32_t k = 0; k < n_stages && k < issued; ++k) {
                 if (r.at == 0) {

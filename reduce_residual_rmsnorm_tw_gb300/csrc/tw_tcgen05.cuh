@@ -116,23 +116,35 @@ __device__ __forceinline__ uint32_t elect_one() {
 __device__ __forceinline__ void tensormap_prefetch(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(m) : "memory");
 }
-// One box of a 2-D tensor to this CTA's shared memory.  CG 2: `bar` may be a
-// barrier of either CTA of the pair (a shared::cluster address).
+// One box of a 2-D tensor to this CTA's shared memory, issued by the lane whose
+// `one` is not zero (see the MMAs below).  CG 2: `bar` may be a barrier of
+// either CTA of the pair (a shared::cluster address).
 template <int CG>
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                            uint32_t bar) {
+                                            uint32_t bar, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar)
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+            ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
             : "memory");
     else
         asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-            ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-            "l"(map), "r"(x), "r"(y), "r"(bar)
+            "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile"
+            ".mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
+                dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
             : "memory");
+}
+// As mbar_arrive_expect_tx, by that lane.
+__device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(one)
+        : "memory");
 }
 
 // One box from this CTA's shared memory to a 2-D tensor (parts outside it are
