@@ -524,8 +524,8 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
         const uint32_t one = elect_one();
-        [[maybe_unused]] const uint64_t slot_operand = smem_operand(slots);
-        [[maybe_unused]] const uint64_t ring_operand = smem_operand(ring);
+        [[maybe_unused]] const uint32_t slot_operand = smem_operand(slots);
+        [[maybe_unused]] const uint32_t ring_operand = smem_operand(ring);
         for (uint32_t tile = unit; ok && tile < static_cast<uint32_t>(p.tiles);
              tile += units, acc.next(2)) {
             ok = warp_wait(p, &h.acc_empty[acc.at], acc.phase ^ 1u, abort);
@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     ok = warp_wait(p, &h.wide_full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint64_t b = slot_operand + r.at * (slot_bytes >> 4);
+                    const uint32_t b = slot_operand + r.at * (slot_bytes >> 4);
                     const uint32_t a = wide + r.at * kSlotColumns;
 #pragma unroll
                     for (int i = 0; i < kBlockK / 16; ++i)
@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     ok = warp_wait(p, &h.full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint64_t a = ring_operand + r.at * (stage_bytes >> 4);
-                    const uint64_t b = a + (kRows * kBlockK >> 4);
+                    const uint32_t a = ring_operand + r.at * (stage_bytes >> 4);
+                    const uint32_t b = a + (kRows * kBlockK >> 4);
 #pragma unroll
                     for (int i = 0; i < kBlockK / 32; ++i)
                         mma_e4m3<CG>(d, a + 2 * i, b + 2 * i, shape, k > 0 || i > 0, one);

@@ -262,9 +262,12 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const uint32_t (&r)[
 // Shared-memory operand, K-major rows of 128 bytes in the 128-byte swizzle
 // (what a TMA box 128 bytes wide writes): eight rows are 1024 bytes apart from
 // the next eight.  A step of 32 bytes along K adds 2.
-__device__ __forceinline__ uint64_t smem_operand(uint32_t addr) {
-    return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (uint64_t{1} << 16) |
-           (uint64_t{1024 >> 4} << 32) | (uint64_t{1} << 46) | (uint64_t{2} << 61);
+// Only the low word depends on the address; it travels alone, so that a step
+// costs one 32-bit addition (64-bit ones made the int8 product 3 to 5 % slower:
+// beside the widening warps its MMA warp is short of issue slots).
+constexpr uint32_t kOperandHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t smem_operand(uint32_t addr) {
+    return ((addr & 0x3ffffu) >> 4) | (1u << 16);
 }
 // Both operands K-major, fp32 accumulator, and operand format 0 for both: f16
 // under kind::f16, e4m3 under kind::f8f6f4.
@@ -277,36 +280,46 @@ __device__ __forceinline__ uint32_t mma_shape(uint32_t m, uint32_t n) {
 //
 // D (TMEM) = A (TMEM, f16) * B (shared memory, f16) + D where `add`.
 template <int CG>
-__device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape,
+__device__ __forceinline__ void mma_f16_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
                                              bool add, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(kOperandHigh), "r"(shape), "r"(static_cast<uint32_t>(add)),
+            "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-            "r"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(kOperandHigh), "r"(shape), "r"(static_cast<uint32_t>(add)),
+            "r"(one)
             : "memory");
 }
 // D (TMEM) = A * B (both shared memory, e4m3) + D where `add`.
 template <int CG>
-__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t shape,
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint32_t a, uint32_t b, uint32_t shape,
                                          bool add, uint32_t one) {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(kOperandHigh), "r"(shape), "r"(static_cast<uint32_t>(add)),
+            "r"(one)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-            "l"(a), "l"(b), "r"(shape), "r"(static_cast<uint32_t>(add)), "r"(one)
+            "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+            "setp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+            "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+            "r"(a), "r"(b), "r"(kOperandHigh), "r"(shape), "r"(static_cast<uint32_t>(add)),
+            "r"(one)
             : "memory");
 }
 // Arrive on `bar` (CG 2: on the barrier at that offset in both CTAs of the
