@@ -802,14 +802,21 @@ struct Plan {
 
 // The cheapest of the cuts a call allows, by the clocks its busiest unit takes
 // (fitted to sweeps of every cut over 13 shapes from 16 x 8192 x 1024 to
-// 1024 x 8192 x 8192; the cut taken was within 15 % of the best of each).
-//   A ring stage costs what a unit's hand-overs of it do, plus its products:
-//   int8 560 + 1.9 bn for a pair, 590 + 2 bn for a lone CTA; e4m3 390 + 0.85 bn
-//   and 390 + 0.8 bn; together never less than reading W and x once.
-//   The last tile's way out adds 14 clocks per column, a split the join of its
-//   shares (int8 6500 + 20 bn, e4m3 4000 + 15 bn).
+// 1024 x 8192 x 8192, the times off by 9 % for int8 and 15 % for e4m3; the cut
+// taken was the best of each but for three, 1 to 3 % behind).
+//   A ring stage costs what a unit's hand-overs of it do, plus its products
+//   (Costs: lone CTA, pair); together never less than reading W and x once.
+//   The last tile's way out adds a cost per column, a split the join of its
+//   shares.
+struct Costs {
+    double stage[2], stage_column[2], out_column, join, join_part, join_column;
+};
+constexpr Costs kCosts[2] = {
+    {{350, 340}, {0.88, 1.26}, 15, 860, 520, 20},   // e4m3; lone CTA, pair
+    {{580, 570}, {0.8, 1.1}, 70, 4600, 390, 11}};   // int8
 Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const DeviceInfo& d) {
     Plan best;
+    const Costs& k = kCosts[int8];
     // 6.3 TB/s at 1.9 GHz: 3300 bytes a clock.
     const double once = static_cast<double>(M + N) * k_blocks * kBlockK / 3300.0;
     for (int cg = 1; cg <= 2; ++cg) {
@@ -822,9 +829,7 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
             c.bn = bn;
             c.token_tiles = (M + bn - 1) / bn;
             c.tiles = channel_tiles * c.token_tiles;
-            const double stage = int8 ? (cg == 2 ? 560.0 + 1.9 * bn : 590.0 + 2.0 * bn)
-                                      : (cg == 2 ? 390.0 + 0.85 * bn : 390.0 + 0.8 * bn);
-            const double join = int8 ? 6500.0 + 20.0 * bn : 4000.0 + 15.0 * bn;
+            const double stage = k.stage[cg - 1] + k.stage_column[cg - 1] * bn;
             for (int split = 1, log2 = cg - 1; log2 < 4 && split <= k_blocks; split *= 2, ++log2) {
                 int64_t units = sms >> log2;
                 const int at_once = d.gemm_clusters[cg - 1][int8][log2];
@@ -838,8 +843,9 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
                 c.split = split;
                 const double main =
                     static_cast<double>(waves * ((k_blocks + split - 1) / split)) * stage;
-                c.cost = (main > once ? main : once) + 14.0 * bn +
-                         (split > 1 ? join : 0.0);
+                c.cost = (main > once ? main : once) + k.out_column * bn;
+                if (split > 1)
+                    c.cost += k.join + k.join_part * split + k.join_column * bn;
                 if (best.cg == 0 || c.cost < best.cost) best = c;
             }
         }
