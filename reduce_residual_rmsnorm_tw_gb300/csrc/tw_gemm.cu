@@ -24,17 +24,18 @@
 // share of the token columns from all S accumulators, copied into its shared
 // memory by the others (and added in rank order: the same bits every time).
 //
-// Measured (N = K = 8192, bf16 out, inputs in HBM or L2 as a loop leaves them):
-//   tokens       16     64    512   1024   4096
-//   int8       17.5   19.1     52     94    335  us
-//   e4m3       14.4   14.9     25     46    190  us
+// Measured (N = K = 8192, bf16 out, inputs larger than L2 in turn):
+//   tokens       16     64    256    512   1024   4096
+//   int8       17.9   18.9   26.9     49     87    325  us
+//   e4m3       14.2   14.7   17.3     25     46    180  us
 // What bounds it: at 16 and 64 tokens the 67 MB of weights (4.7 TB/s in e4m3 with
-// launch, ramp and join in the time).  e4m3 at 4096 tokens (2.8 to 3.0 PFLOP/s):
-// the board's power, which takes the SM clock to 1.5 to 1.6 GHz; a stage's MMAs
-// take 520 clocks of their ideal 512.  e4m3 at 1024: 1.7 waves of tiles on 76
-// pairs, run as two.  int8 (1.4 to 1.6 PFLOP/s, f16's rate being 2): the widening,
-// a chain of shared loads, permutes, TMEM and shared stores of about 1880 clocks
-// per group and stage, 82 % of the MMAs' pace in long calls.
+// launch, ramp and join in the time).  From 512 tokens on the board's power: back
+// to back the SM clock falls to 1.5 to 1.9 GHz; with pauses between calls it
+// stays at 2.07 and 1024 tokens take 82 us (int8) and 43 (e4m3), 4096 tokens 300
+// (1.83 PFLOP/s) and 151 (3.63).  e4m3 at 1024: 1.7 waves of tiles on 76 pairs,
+// run as two.  int8 below 512 tokens: the MMA warp, which takes about 700 clocks
+// for a stage's wait, eight MMAs and commit beside sixteen widening warps (with
+// half the MMAs 256 tokens take 25.6 us, without the widening's arithmetic 24.2).
 #include <cuda.h>
 
 #include "tw_tcgen05.cuh"

@@ -142,6 +142,41 @@ def test_captured_and_replayed_on_new_inputs():
     assert torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("quant", ["int8", "e4m3"])
+def test_two_streams_at_once_give_the_same_bits(quant):
+    # Products of different cuts (lone CTAs, pairs, split K, few tokens) queued
+    # on two streams without a pause, the GPU's caches holding neither's inputs.
+    shapes = [(256, 2304, 4096), (128, 520, 8192), (6, 4096, 4096), (60, 300, 8192),
+              (700, 1000, 2064)]
+    ops, want, outs = [], [], []
+    for i, (T, N, K) in enumerate(shapes):
+        x, xs = draw_8_bit(T, K, quant, 50 + i)
+        w, ws = draw_8_bit(N, K, quant, 70 + i)
+        out = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+        tw.tw_gemm_q8(x, xs, w, ws, out)
+        torch.cuda.synchronize()
+        check_product(out, x, xs, w, ws, f"{T}x{N}x{K} {quant}")
+        ops.append((x, xs, w, ws))
+        want.append(out)
+        outs.append([torch.empty_like(out) for _ in range(2)])
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    flush = torch.empty(1 << 26, dtype=torch.int32, device="cuda")
+    for _ in range(8):
+        flush.fill_(1)
+        for pair in outs:
+            for o in pair:
+                o.zero_()
+        torch.cuda.synchronize()
+        for i in range(len(shapes)):
+            tw.tw_gemm_q8(*ops[i], outs[i][0], stream=streams[0])
+            j = len(shapes) - 1 - i
+            tw.tw_gemm_q8(*ops[j], outs[j][1], stream=streams[1])
+        torch.cuda.synchronize()
+        for w, pair in zip(want, outs):
+            assert all(torch.equal(w, o) for o in pair)
+    assert tw.tw_device_status() == 0
+
+
 def test_empty_batch():
     x, xs = draw_8_bit(4, 64, "int8", 1)
     tw.tw_gemm_q8(x[:0], xs[:0], x, xs, torch.empty(0, 4, device="cuda"))
