@@ -138,6 +138,14 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
             "l"(map), "r"(x), "r"(y), "r"(bar), "r"(one)
             : "memory");
 }
+// The same box into L2 only.
+__device__ __forceinline__ void tma_warm_2d(const CUtensorMap* map, int x, int y, uint32_t one) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+        "@q cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];\n\t}" ::"l"(map),
+        "r"(x), "r"(y), "r"(one)
+        : "memory");
+}
 // As mbar_arrive_expect_tx, by that lane.
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint32_t bar, uint32_t bytes, uint32_t one) {
     asm volatile(
