@@ -26,8 +26,8 @@
 //
 // Measured (N = K = 8192, bf16 out, inputs larger than L2 in turn):
 //   tokens       16     64    256    512   1024   4096
-//   int8       17.9   18.9   26.9     49     87    325  us
-//   e4m3       14.2   14.7   17.3     25     46    180  us
+//   int8       17.1   18.1   26.9     48     87    325  us
+//   e4m3       14.0   14.5   17.3     25     46    180  us
 // What bounds it: at 16 and 64 tokens the 67 MB of weights (4.7 TB/s in e4m3 with
 // launch, ramp and join in the time).  From 512 tokens on the board's power: back
 // to back the SM clock falls to 1.5 to 1.9 GHz; with pauses between calls it
