@@ -50,19 +50,21 @@ constexpr int kSlotColumns = kBlockK / 2;
 constexpr int kRingStages = 12;
 constexpr int kTmemColumns = 512;
 
-// Warp roles: 0 loads W, 1 MMA, 2 (split K) tells the cluster that the products
-// are done, 3 loads x, 4-7 epilogue, from 8 on kGroups of four widen (int8).
+// Warp roles: 0 loads W, 1 MMA, 3 loads x, 4-7 epilogue, from 8 on kGroups of
+// four widen (int8).
 constexpr int kGroups = 4;
 // Groups two apart work on neighbouring stages and slots (Ring::skip).
 static_assert((kTmemColumns - 2 * 192) / kSlotColumns >= kGroups / 2, "too few slots");
-constexpr int kWeightWarp = 0, kAnnounceWarp = 2, kTokenWarp = 3, kEpilogueWarp = 4,
-              kWidenWarp = 8;
+constexpr int kWeightWarp = 0, kTokenWarp = 3, kEpilogueWarp = 4, kWidenWarp = 8;
 
 // Largest token tile: a unit's two accumulators (and, for int8, two slots of
 // widened W) share 512 TMEM columns; a single CTA takes short tiles only.
 __host__ __device__ constexpr int max_tokens(int cg, bool int8) {
     return cg == 1 ? 64 : (int8 ? 192 : 256);
 }
+// Largest token tile whose K is split: a join keeps room for it beside the ring
+// (wider tiles were never the best cut).
+constexpr int kJoinTokens = 128;
 // Staging of the output: two chunks of 32 tokens (bf16) or 16 (fp32) x 128
 // channels for TMA to store.
 constexpr int kChunkBytes = 8192;
@@ -77,7 +79,7 @@ struct Header {
     uint64_t full[kRingStages], empty[kRingStages];
     uint64_t wide_full[kWideSlots], wide_empty[kWideSlots];
     uint64_t acc_full[2], acc_empty[2];
-    uint64_t open, joined, drained;
+    uint64_t joined, drained;
     uint32_t tmem;
     int abort;
     alignas(16) float x_scale[4][256];  // each epilogue warp's copy of its tile's
@@ -215,11 +217,17 @@ __device__ __forceinline__ void read_acc(uint32_t (&v)[W], uint32_t d, int c) {
 
 // Split K: unit q of the cluster adds up columns [q own, (q + 1) own).  The
 // others' registers for them go to shared memory as they are (16 bytes of each
-// of the 128 threads in turn), and from there as one bulk copy each into the
-// ring of the unit they belong to.
+// of the 128 threads in turn; the ring, which their own products have left), and
+// from there as one bulk copy each to a place that the unit they belong to keeps
+// for them (in its ring they would have to ask first whether its products are
+// done, with a release at cluster scope of about 1000 clocks).
 struct Join {
     uint32_t outgoing, incoming, block;  // shared memory; bytes of one share
     int part, split, own;
+    // Where sender q's share lies among the split - 1 of receiver r.
+    __device__ __forceinline__ uint32_t place(int q, int r) const {
+        return incoming + static_cast<uint32_t>(q < r ? q : q - 1) * block;
+    }
 };
 
 template <int W, bool FRAGMENTS>
@@ -243,7 +251,7 @@ __device__ __forceinline__ void read_columns(float (&y)[W], const Join& g, uint3
     uint32_t v[W];
     read_acc<W, FRAGMENTS>(v, d, c);
     if constexpr (SPLIT) {
-        const uint32_t from = g.incoming + (c - g.part * g.own) * (kRows * 4) + etid * 16;
+        const uint32_t from = (c - g.part * g.own) * (kRows * 4) + etid * 16;
 #pragma unroll
         for (int j = 0; j < W; ++j) y[j] = 0.f;
         for (int q = 0; q < g.split; ++q) {
@@ -251,7 +259,7 @@ __device__ __forceinline__ void read_columns(float (&y)[W], const Join& g, uint3
             for (int i = 0; i < W / 4; ++i) {
                 const uint4 w = q == g.part
                                     ? make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3])
-                                    : lds16(from + q * g.block + i * kRows * 16);
+                                    : lds16(g.place(q, g.part) + from + i * kRows * 16);
                 y[4 * i] += __uint_as_float(w.x);
                 y[4 * i + 1] += __uint_as_float(w.y);
                 y[4 * i + 2] += __uint_as_float(w.z);
@@ -465,7 +473,6 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             mbar_init(smem_addr(&h.acc_full[b]), 1);
             mbar_init(smem_addr(&h.acc_empty[b]), 4 * CG);
         }
-        mbar_init(smem_addr(&h.open), split);
         mbar_init(smem_addr(&h.joined), 1);
         mbar_init(smem_addr(&h.drained), 1);
         h.abort = 0;
@@ -585,14 +592,6 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             mma_commit<CG>(smem_addr(&h.drained), pair, one);
             if (!mbar_wait_slice(smem_addr(&h.drained), 0, nullptr)) atomicOr(p.status, 2u);
         }
-    } else if (SPLIT && warp == kAnnounceWarp) {
-        // This CTA's products are done: its ring is free for the other units'
-        // columns.  (A release at cluster scope takes about 1000 clocks; the
-        // epilogue writes its own columns meanwhile.)
-        if (static_cast<int>(unit) < p.tiles && warp_wait(p, &h.acc_full[0], 0, abort) &&
-            lane < split)
-            mbar_arrive_cluster(
-                map_to_rank(smem_addr(&h.open), static_cast<uint32_t>(lane * CG + half)));
     } else if (warp >= kEpilogueWarp && warp < kEpilogueWarp + 4) {
         // -------------------------------------------------- epilogue -----
         // Thread = channel (TMEM lane), registers = tokens.
@@ -632,7 +631,7 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
             if constexpr (SPLIT) {
                 const int own = p.bn / split;  // a multiple of 8 (tma_out: of a chunk)
                 const uint32_t block = static_cast<uint32_t>(own * kRows * 4);
-                g = Join{ring, ring + split * block, block, part, split, own};
+                g = Join{ring, staging - (split - 1) * block, block, part, split, own};
                 if (fragments)
                     send_columns<16, true>(g, d, etid);
                 else
@@ -640,17 +639,11 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                 fence_async_shared();
                 named_barrier(1, 128);
                 if (etid == 0) {
-                    // Their rings are free once their products are done too.
-                    if (!mbar_wait_slice<true>(smem_addr(&h.open), 0, abort)) {
-                        gave_up(p, abort);
-                    } else {
-                        for (int q = 0; q < split; ++q) {
-                            if (q == part) continue;
-                            const uint32_t dest = static_cast<uint32_t>(q * CG + half);
-                            bulk_push(map_to_rank(g.incoming + part * block, dest),
-                                      g.outgoing + q * block, block,
-                                      map_to_rank(smem_addr(&h.joined), dest));
-                        }
+                    for (int q = 0; q < split; ++q) {
+                        if (q == part) continue;
+                        const uint32_t dest = static_cast<uint32_t>(q * CG + half);
+                        bulk_push(map_to_rank(g.place(part, q), dest), g.outgoing + q * block,
+                                  block, map_to_rank(smem_addr(&h.joined), dest));
                     }
                 }
                 __syncwarp();
@@ -854,8 +847,7 @@ Plan plan(int64_t M, int64_t N, int k_blocks, bool int8, int64_t sms, const Devi
                 if (units < 1 || (split > 1 && c.tiles > units)) break;
                 // Whole chunks of the output's staging, or eights of a share.
                 if (bn % (split == 1 ? 32 : 8 * split) != 0) continue;
-                // A join holds its tile twice in the pool.
-                if (split > 1 && bn * kRows * 8 > kPoolBytes) break;
+                if (split > 1 && bn > kJoinTokens) break;
                 const int64_t waves = (c.tiles + units - 1) / units;
                 c.split = split;
                 const double main =
@@ -934,15 +926,18 @@ int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
     p.slot_bytes = c.bn / cg * kBlockK * 2;
     p.slots = int8 ? (kTmemColumns - 2 * p.acc_columns) / kSlotColumns : 0;
     if (p.slots > kWideSlots) p.slots = kWideSlots;
+    const int pool = kPoolBytes - (c.bn - c.bn / c.split) * kRows * 4;  // less the join's
     for (;; --p.slots) {
-        p.stages = (kPoolBytes - p.slots * p.slot_bytes) / p.stage_bytes;
+        p.stages = (pool - p.slots * p.slot_bytes) / p.stage_bytes;
         if (p.stages > kRingStages) p.stages = kRingStages;
         // An odd number of stages hands a place of the ring from one pair of
         // widening groups to the other, and a wait by parity must not look at
         // it before the other's load k has landed.  Who is about to widen
         // stage k + stages has seen the products of k + stages - 2 - slots
         // done, which must not lie before k.
-        if (!int8 || p.stages % 2 == 0 || p.stages >= p.slots + 2) break;
+        // (An even number is fine if it is more than the slots: 4 and 4 were 5 %
+        // slower than 6 and 3.)
+        if (!int8 || p.stages >= p.slots + 2 || (p.stages % 2 == 0 && p.stages > p.slots)) break;
     }
     const int64_t es = p.f32 ? 4 : 2;
     p.tma_out = g.N * es % 16 == 0 && p.bn / p.split % (p.f32 ? 16 : 32) == 0;

@@ -37,12 +37,6 @@ __device__ __forceinline__ uint32_t map_to_rank(uint32_t local, uint32_t rank) {
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local), "r"(rank));
     return remote;
 }
-// Arrive on a barrier of another CTA of the cluster, everything this thread
-// has done or seen before it.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar)
-                 : "memory");
-}
 // Arrive on a barrier of a CTA of the pair for work that stays in this CTA:
 // its own shared-memory writes (already ordered for the async proxy by
 // fence_async_shared) and TMEM accesses (complete, behind
