@@ -26,8 +26,8 @@
 //
 // Measured (N = K = 8192, bf16 out, inputs larger than L2 in turn):
 //   tokens       16     64    256    512   1024   4096
-//   int8       17.1   18.1   26.9     48     87    325  us
-//   e4m3       14.0   14.5   17.3     25     46    180  us
+//   int8       16.7   18.0   26.9     48     87    325  us
+//   e4m3       13.9   14.5   17.3     25     46    180  us
 // What bounds it: at 16 and 64 tokens the 67 MB of weights (4.7 TB/s in e4m3 with
 // launch, ramp and join in the time).  From 512 tokens on the board's power: back
 // to back the SM clock falls to 1.5 to 1.9 GHz; with pauses between calls it
@@ -812,8 +812,8 @@ struct Plan {
 
 // The cheapest of the cuts a call allows, by the clocks its busiest unit takes
 // (fitted to sweeps of every cut over 13 shapes from 16 x 8192 x 1024 to
-// 1024 x 8192 x 8192, the times off by 9 % for int8 and 15 % for e4m3; the cut
-// taken was the best of each but for three, 1 to 3 % behind).
+// 1024 x 8192 x 8192; over these and four more the cut taken was the best or
+// within 4 % of it, but for e4m3 200 x 2048 x 5120, 8 % behind).
 //   A ring stage costs what a unit's hand-overs of it do, plus its products
 //   (Costs: lone CTA, pair); together never less than reading W and x once.
 //   The last tile's way out adds a cost per column, a split the join of its
