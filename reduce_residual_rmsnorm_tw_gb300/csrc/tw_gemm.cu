@@ -26,16 +26,17 @@
 //
 // Measured (N = K = 8192, bf16 out, inputs larger than L2 in turn):
 //   tokens       16     64    256    512   1024   4096
-//   int8       16.7   18.0   26.9     48     87    325  us
-//   e4m3       13.9   14.5   17.3     25     46    180  us
+//   int8       16.5   17.4   25.9     47     87    325  us
+//   e4m3       13.6   14.3   17.3     25     45    178  us
 // What bounds it: at 16 and 64 tokens the 67 MB of weights (4.7 TB/s in e4m3 with
 // launch, ramp and join in the time).  From 512 tokens on the board's power: back
 // to back the SM clock falls to 1.5 to 1.9 GHz; with pauses between calls it
 // stays at 2.07 and 1024 tokens take 82 us (int8) and 43 (e4m3), 4096 tokens 300
 // (1.83 PFLOP/s) and 151 (3.63).  e4m3 at 1024: 1.7 waves of tiles on 76 pairs,
-// run as two.  int8 below 512 tokens: the MMA warp, which takes about 700 clocks
-// for a stage's wait, eight MMAs and commit beside sixteen widening warps (with
-// half the MMAs 256 tokens take 25.6 us, without the widening's arithmetic 24.2).
+// run as two.  int8 below 512 tokens: issue slots, for which the MMA warp (about
+// 650 clocks for a stage's wait, eight MMAs and commit) and sixteen widening warps
+// compete (when 256 tokens took 28.3 us, half the MMAs took it to 25.6, leaving
+// out the widening's arithmetic to 24.2).
 #include <cuda.h>
 
 #include "tw_tcgen05.cuh"
@@ -541,9 +542,12 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
         // ------------------------------------------------------- MMA -----
         // The whole warp walks the stages and one elected lane issues: with
         // the operands in warp-uniform code a stage's MMAs issue in a fraction
-        // of the time a lone lane takes.  (int8: beside sixteen widening warps
-        // every instruction of this one counts; one hand-over per 128 elements
-        // of K instead of 64 took 512 x 8192 x 8192 from 62.6 to 57.1 us.)
+        // of the time a lone lane takes.
+        // int8: beside sixteen widening warps every instruction of this one
+        // counts.  One hand-over per 128 elements of K instead of 64 took 512 x
+        // 8192 x 8192 from 62.6 to 57.1 us; issuing in a branch of its own, not
+        // under a predicate of each MMA, took it from 49 to 46.5 (e4m3, whose
+        // warp has no such neighbours, was 5 % slower so).
         Ring r, acc;
         bool ok = true;
         const uint32_t shape = mma_shape(kRows * CG, static_cast<uint32_t>(p.bn));
@@ -564,12 +568,14 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     tcgen05_fence_after();
                     const uint32_t b = slot_operand + r.at * (slot_bytes >> 4);
                     const uint32_t a = wide + r.at * kSlotColumns;
+                    if (one) {
 #pragma unroll
-                    for (int i = 0; i < kBlockK / 16; ++i)
-                        mma_f16_tmem<CG>(d, a + 8 * i,
-                                         b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4), shape,
-                                         k > 0 || i > 0, one);
-                    mma_commit<CG>(smem_addr(&h.wide_empty[r.at]), pair, one);
+                        for (int i = 0; i < kBlockK / 16; ++i)
+                            mma_f16_tmem<CG>(d, a + 8 * i,
+                                             b + (i / 4) * (slot_bytes >> 5) + 2 * (i % 4), shape,
+                                             k > 0 || i > 0, 1u);
+                        mma_commit<CG>(smem_addr(&h.wide_empty[r.at]), pair, 1u);
+                    }
                 }
             } else {
                 const int n = kb1 - kb0;
@@ -577,7 +583,9 @@ __global__ void __launch_bounds__(INT8 ? 256 + 128 * kGroups : 256, 1)
                     ok = warp_wait(p, &h.full[r.at], r.phase, abort);
                     if (!ok) break;
                     tcgen05_fence_after();
-                    const uint32_t a = ring_operand + r.at * (stage_bytes >> 4);
+                    // (The maximum of equal numbers: a warp-uniform one.)
+                    const uint32_t at = __reduce_max_sync(0xffffffffu, r.at);
+                    const uint32_t a = ring_operand + at * (stage_bytes >> 4);
                     const uint32_t b = a + (kRows * kBlockK >> 4);
 #pragma unroll
                     for (int i = 0; i < kBlockK / 32; ++i)
