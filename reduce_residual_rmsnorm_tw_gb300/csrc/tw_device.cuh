@@ -253,7 +253,7 @@ __device__ __forceinline__ void sum_squares(float (&ss2)[2], const float (&x)[E]
 // A row v quantised to 8 bits with one scale: scale = max|v| / top and
 // q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  The kernels multiply
 // by mul = top / max|v|, so that no element pays a division; a quotient that
-// lands within an ulp of a rounding boundary may then round to the neighbour.
+// lands within two ulp of a rounding boundary may then round to the neighbour.
 // Rows whose largest magnitude is below kQuantTiny (so small that top / max
 // would overflow or the scale lose bits as a subnormal) count as zero rows:
 // scale 0, values 0.  A row that holds a NaN or an infinity has no scale:
@@ -295,7 +295,12 @@ __device__ __forceinline__ bool quant_finite(float m) {
 __device__ __forceinline__ RowQuant row_quant(float m, float top) {
     RowQuant r;
     r.zero = !quant_finite(m) || m < kQuantTiny;
-    r.mul = r.zero ? 0.f : __fdiv_rn(top, m);
+    // The approximate reciprocal is off by at most an ulp; of m / 4, so that it
+    // is a normal number for every m from kQuantTiny up (an exact division cost
+    // 1 to 2 % of a norm: 2 x 2048 x 4096 13.5 us against 13.25).
+    float inverse;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(m * 0.25f));
+    r.mul = r.zero ? 0.f : (top * 0.25f) * inverse;
     return r;
 }
 
