@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)
             for (int w = 0; w < W; ++w) m = max_abs(m, warp_max[buf][slot * W + w]);
             buf ^= 1;
         }
-        const RowQuant rq = row_quant(m, top);
+        const RowQuant rq = row_quant<true>(m, top);
         if (live && rtid == 0) p.out_scale[t] = row_scale(m, 1.f, top);
         void* out[1] = {p.out};
 #pragma unroll

@@ -59,9 +59,8 @@ class Chain:
         check_norm_stage(self.wl, self.parts, self.res, self.weight, self.q[0], self.s[0],
                          self.res1, self.quant, "first norm")
         check_product(self.mid, self.q[0], self.s[0], self.up, self.up_s, "up")
-        # Reciprocal (an ulp, 2 U), factor and value multiplies (U each).
         check_rows(self.q[1], self.s[1], inputs.to_f64(self.mid), self.quant,
-                   np.full(self.T, 4 * U), "quantised")
+                   np.full(self.T, 3 * U), "quantised")
         check_product(self.down_out, self.q[1], self.s[1], self.down, self.down_s, "down")
         check_norm_stage(self.wl, [self.parts[0], self.down_out], self.res1, self.weight,
                          self.q[2], self.s[2], self.res2, self.quant, "second norm")
