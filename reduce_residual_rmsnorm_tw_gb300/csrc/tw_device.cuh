@@ -251,9 +251,9 @@ __device__ __forceinline__ void sum_squares(float (&ss2)[2], const float (&x)[E]
 
 // ------------------------------------------------------ 8-bit outputs ---
 // A row v quantised to 8 bits with one scale: scale = max|v| / top and
-// q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  The kernels multiply
-// by mul = top / max|v|, so that no element pays a division; a quotient that
-// lands within two ulp of a rounding boundary may then round to the neighbour.
+// q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  Row quantisation takes
+// the quotient as a division would (RowDivision); the norm multiplies by top /
+// max|v| (RowQuant).
 // Rows whose largest magnitude is below kQuantTiny (so small that top / max
 // would overflow or the scale lose bits as a subnormal) count as zero rows:
 // scale 0, values 0.  A row that holds a NaN or an infinity has no scale:
@@ -282,44 +282,8 @@ __device__ __forceinline__ float warp_max_abs(float m) {
     return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
 }
 
-struct RowQuant {
-    float mul;  // top / max|v|; 0 where every value is 0 by rule
-    bool zero;  // every value of the row is 0
-};
-
 __device__ __forceinline__ bool quant_finite(float m) {
     return m <= 3.402823466e38f;  // false for NaN too
-}
-
-// How a row is quantised, m = max|v| (NaN or infinite where the row holds one).
-// EXACT: top / max rounded to nearest.  Otherwise an approximate reciprocal, off
-// by at most an ulp; of m / 4, so that it is a normal number for every m from
-// kQuantTiny up.  The norm takes the latter (2 x 2048 x 4096 13.25 us against
-// 13.5): its fp32 values seldom lie in the very middle of two 8-bit ones.  bf16
-// values often do, and the better factor leaves more of them where an exact
-// quotient would (of 4096 x 8192 in e4m3 a difference of 0.06 % instead of 0.3),
-// for nothing in time.
-template <bool EXACT>
-__device__ __forceinline__ RowQuant row_quant(float m, float top) {
-    RowQuant r;
-    r.zero = !quant_finite(m) || m < kQuantTiny;
-    if constexpr (EXACT) {
-        r.mul = r.zero ? 0.f : __fdiv_rn(top, m);
-    } else {
-        float inverse;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(m * 0.25f));
-        r.mul = r.zero ? 0.f : (top * 0.25f) * inverse;
-    }
-    return r;
-}
-
-// The scale of the row whose elements are gain * v: the gain (a norm's 1 / rms)
-// cancels out of q.  For the one thread that stores it: a second division in
-// every thread cost a norm of 2 x 2048 x 4096 3 % (13.8 us against 13.45), 5 %
-// on 8 SMs.
-__device__ __forceinline__ float row_scale(float m, float gain, float top) {
-    if (!quant_finite(m)) return __uint_as_float(0x7fffffffu);
-    return m < kQuantTiny ? 0.f * gain : __fdiv_rn(m * gain, top);
 }
 
 // Four values times mul, rounded to nearest even, as four int8 (|v * mul| is
@@ -341,27 +305,130 @@ __device__ __forceinline__ uint32_t pack_int8(const float* v, float mul) {
     return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// Four values times mul as four e4m3 (nearest even, saturating at 448).
-__device__ __forceinline__ uint32_t pack_e4m3(const float* v, float mul) {
+// Four values as four e4m3 (nearest even, saturating at 448).
+__device__ __forceinline__ uint32_t pack_e4m3(float v0, float v1, float v2, float v3) {
     uint32_t r;
     asm("{\n\t.reg .b16 lo, hi;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
         "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
         "mov.b32 %0, {lo, hi};\n\t}"
         : "=r"(r)
-        : "f"(v[0] * mul), "f"(v[1] * mul), "f"(v[2] * mul), "f"(v[3] * mul));
+        : "f"(v0), "f"(v1), "f"(v2), "f"(v3));
     return r;
 }
 
+// How the norm quantises a row, m = max|v| (NaN or infinite where the row holds
+// one): q = rne(v * mul), mul = top / m, so that no element pays a division; a
+// quotient within two ulp of the middle of two codes may go to either.  The
+// reciprocal is an approximate one, off by at most an ulp; of m / 4, so that it is a
+// normal number for every m from kQuantTiny up (2 x 2048 x 4096 13.25 us against
+// 13.5 with a division).  The norm's fp32 values seldom lie in the very middle of
+// two 8-bit ones.
+struct RowQuant {
+    float mul;  // top / max|v|; 0 where every value is 0 by rule
+    bool zero;  // every value of the row is 0
+
+    RowQuant() = default;
+    __device__ __forceinline__ RowQuant(float m, float top) {
+        zero = !quant_finite(m) || m < kQuantTiny;
+        float inverse;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(m * 0.25f));
+        mul = zero ? 0.f : (top * 0.25f) * inverse;
+    }
+    __device__ __forceinline__ uint32_t codes(const float* v, int qtype) const {
+        return qtype == TW_INT8
+                   ? pack_int8(v, mul)
+                   : pack_e4m3(v[0] * mul, v[1] * mul, v[2] * mul, v[3] * mul);
+    }
+};
+
+// How row quantisation does it: q = rne(v / s) with s = m / top as it is stored
+// and the quotient rounded as fp32 division rounds it.  bf16 rows hold many values in
+// the very middle of two codes (a v * mul that is not rounded first sends all of a
+// row's to the same side: 0.07 % of the codes of 1024 x 8192 normal values differed
+// from the definition's, against 0.015 % of a division's).
+//   s: by Markstein's quotient (IBM J. Res. Dev. 34, 1990), p = rn(m c) with c = rn(1 /
+// top), then rn(p + (m - p top) c), the remainder being exact in a fused multiply-add:
+// what the division gives for every fp32 m from kQuantTiny up.
+//   q: 1 / s is kept to some 45 bits as hi + lo, hi an approximate reciprocal and lo
+// the rest (1 - s hi is exact in a fused multiply-add).  rn(v hi + rn(v lo)) is then
+// off v / s by at most half an ulp and 2^-21 of one, and right wherever v / s is a
+// float, the middle of two codes in particular: two packed operations for two elements
+// instead of two divisions.  For lo to keep its bits, a row above 2^60 and its scale
+// are divided by 2^64 first (`huge`; values so small that this rounds them are 0 in 8
+// bits).  4096 x 8192 16.1 us, as with one multiplication by top / m.
+struct RowDivision {
+    float scale, hi, lo;
+    bool zero;  // every value of the row is 0
+    bool huge;  // quotients() takes v * 2^-64
+
+    __device__ __forceinline__ RowDivision(float m, float top) {
+        const float c = top == 127.f ? 1.f / 127.f : 1.f / 448.f;
+        const float p = m * c;
+        scale = fmaf(fmaf(-p, top, m), c, p);
+        huge = m > 0x1p60f;
+        zero = !quant_finite(m) || m < kQuantTiny;
+        const float s = huge ? scale * 0x1p-64f : scale;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(s));
+        lo = fmaf(-s, hi, 1.f) * hi;
+        if (zero) scale = quant_finite(m) ? 0.f : __uint_as_float(0x7fffffffu);
+    }
+    // q[0..1] = v[0..1] / s.
+    __device__ __forceinline__ void quotients(float* q, const float* v) const {
+        asm("{\n\t.reg .b64 a, p, h, l;\n\t"
+            "mov.b64 a, {%2, %3};\n\t"
+            "mov.b64 h, {%4, %4};\n\t"
+            "mov.b64 l, {%5, %5};\n\t"
+            "mul.rn.f32x2 p, a, l;\n\t"
+            "fma.rn.f32x2 p, a, h, p;\n\t"
+            "mov.b64 {%0, %1}, p;\n\t}"
+            : "=f"(q[0]), "=f"(q[1])
+            : "f"(v[0]), "f"(v[1]), "f"(hi), "f"(lo));
+    }
+    __device__ __forceinline__ uint32_t codes(const float* v, int qtype) const {
+        float q[4];
+        quotients(q, v);
+        quotients(q + 2, v + 2);
+        return qtype == TW_INT8 ? pack_int8(q, 1.f) : pack_e4m3(q[0], q[1], q[2], q[3]);
+    }
+};
+
+// The scale of the row whose elements are gain * v: the gain (a norm's 1 / rms)
+// cancels out of q.  For the one thread that stores it: a second division in
+// every thread cost a norm of 2 x 2048 x 4096 3 % (13.8 us against 13.45), 5 %
+// on 8 SMs.
+__device__ __forceinline__ float row_scale(float m, float gain, float top) {
+    if (!quant_finite(m)) return __uint_as_float(0x7fffffffu);
+    return m < kQuantTiny ? 0.f * gain : __fdiv_rn(m * gain, top);
+}
+
+// max(|m|, |v|) over one vector's elements, NaN if any is.  bf16: two maxima side by
+// side in the halves of m (signs are of no meaning), without widening; max_abs_of
+// joins them.
+__device__ __forceinline__ void max_abs_vec(uint32_t& m, const uint4& v, __nv_bfloat16*) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm("max.NaN.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[i]));
+}
+__device__ __forceinline__ void max_abs_vec(uint32_t& m, const uint4& v, float*) {
+    const float a = max_abs(__uint_as_float(m), __uint_as_float(v.x), __uint_as_float(v.y));
+    m = __float_as_uint(max_abs(a, __uint_as_float(v.z), __uint_as_float(v.w)));
+}
+__device__ __forceinline__ float max_abs_of(uint32_t m, __nv_bfloat16*) {
+    return max_abs(0.f, __uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+__device__ __forceinline__ float max_abs_of(uint32_t m, float*) { return __uint_as_float(m); }
+
 // The E elements (8 or 4) of one 16-byte vector's worth of a row, quantised
 // and stored at p (E bytes, E-byte aligned) in each of n destinations.
-template <int E>
+template <int E, class Row>
 __device__ __forceinline__ void store_q8(void* const* out, int n, int64_t off, const float* v,
-                                         const RowQuant& q, int qtype) {
+                                         const Row& q, int qtype) {
     uint32_t b[E / 4];
 #pragma unroll
     for (int i = 0; i < E / 4; ++i) {
-        b[i] = qtype == TW_INT8 ? pack_int8(v + 4 * i, q.mul) : pack_e4m3(v + 4 * i, q.mul);
+        b[i] = q.codes(v + 4 * i, qtype);
         if (q.zero) b[i] = 0;
     }
     for (int k = 0; k < n; ++k) {

@@ -1,12 +1,12 @@
 // tw_quant.cu -- rows quantised to 8 bits with one scale per token.
 //
-// s_t = max_h |x[t,h]| / top, q[t,h] = rne(x[t,h] * top / max): a row must be
+// s_t = max_h |x[t,h]| / top, q[t,h] = rne(x[t,h] / s_t): a row must be
 // seen whole before its first value is written, and is read only once: its
 // 16-byte vectors stay in registers between the two.  A row belongs to W
 // warps (W * 32 threads holding VPT vectors each), so short rows share a CTA
 // and long ones spread over it; one shuffle-free warp maximum, and for W > 1
 // one exchange through shared memory.  Bound by HBM: row_bytes in, H + 4 out
-// (4096 x 8192 bf16: 15.9 us, 6.3 TB/s).
+// (4096 x 8192 bf16: 16.1 us, 6.2 TB/s).
 #include "tw_device.cuh"
 
 namespace tw {
@@ -18,8 +18,13 @@ constexpr int kQuantThreads = 256;
 // stores one (launches held to few SMs, whose CTAs are alone there: 512 x 8192
 // on 8 SMs 67 -> 42 us; with eight CTAs on an SM the others do that already,
 // and the registers cost 3 %).
+// CTAs per SM: enough to keep rows' loads in flight while others reduce (4096 x
+// 8192 with three instead of four 19.1 us).
+__host__ __device__ constexpr int quantize_ctas(int vpt, int elems, bool ahead) {
+    return ahead ? 1 : vpt <= 2 ? 8 : vpt == 4 ? (elems == 8 ? 4 : 5) : 1;
+}
 template <typename T, int VPT, int W, bool AHEAD>
-__global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)
+__global__ void __launch_bounds__(kQuantThreads, quantize_ctas(VPT, Vec<T>::kElems, AHEAD))
     quantize_kernel(const __grid_constant__ QuantParams p) {
     constexpr int E = Vec<T>::kElems;
     constexpr int kRows = kQuantThreads / 32 / W;  // rows per CTA at a time
@@ -62,15 +67,10 @@ __global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)
         } else {
             load(raw, t);
         }
-        float m = 0.f;
+        uint32_t most = 0;
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            float f[E];
-            Vec<T>::to_float(raw[k], f);
-#pragma unroll
-            for (int e = 0; e < E; e += 2) m = max_abs(m, f[e], f[e + 1]);
-        }
-        m = warp_max_abs(m);
+        for (int k = 0; k < VPT; ++k) max_abs_vec(most, raw[k], static_cast<T*>(nullptr));
+        float m = warp_max_abs(max_abs_of(most, static_cast<T*>(nullptr)));
         if constexpr (W > 1) {
             if ((threadIdx.x & 31) == 0) warp_max[buf][warp] = m;
             __syncthreads();
@@ -79,8 +79,18 @@ __global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)
             for (int w = 0; w < W; ++w) m = max_abs(m, warp_max[buf][slot * W + w]);
             buf ^= 1;
         }
-        const RowQuant rq = row_quant<true>(m, top);
-        if (live && rtid == 0) p.out_scale[t] = row_scale(m, 1.f, top);
+        const RowDivision rd(m, top);
+        if (live && rtid == 0) p.out_scale[t] = rd.scale;
+        if (rd.huge) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
+                float f[E];
+                Vec<T>::to_float(raw[k], f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) f[e] *= 0x1p-64f;
+                raw[k] = Vec<T>::from_float(f);
+            }
+        }
         void* out[1] = {p.out};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -88,7 +98,7 @@ __global__ void __launch_bounds__(kQuantThreads, !AHEAD && VPT <= 2 ? 8 : 1)
             if (live && v < nvec) {
                 float f[E];
                 Vec<T>::to_float(raw[k], f);
-                store_q8<E>(out, 1, t * p.H + static_cast<int64_t>(v) * E, f, rq, p.qtype);
+                store_q8<E>(out, 1, t * p.H + static_cast<int64_t>(v) * E, f, rd, p.qtype);
             }
         }
     }
