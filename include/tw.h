@@ -271,11 +271,13 @@ int tw_quantize_rows_q8(const void* x, void* out, float* out_scale, int64_t T,
  *   out[t,n] = (sum_k x[t,k] * w[n,k]) * x_scale[t] * w_scale[n]
  * for t in [t0, t1), rounded once to dtype (TW_BF16 or TW_F32).  x [T, K] and
  * w [N, K] are 8-bit of one qtype (int8 values may use all of [-128, 127]),
- * out is [T, N]; all row-major and dense.  Products are exact, their sum is
- * held in fp32 or 32-bit integers: exact for int8 while every partial sum stays
- * within 2^24 (any K <= 1024), otherwise off by a few 2^-24 of the largest
- * partial sum.  The order of the sum depends on the sizes and max_sms, not on
- * the data or the run.  Written to partials[r] of the fused step, out is a
+ * out is [T, N]; all row-major and dense.  Products are exact.  int8 sums of
+ * up to 4 tokens a call are 32-bit integers, rounded to fp32 once; all others are
+ * held in fp32: exact for int8 while every partial sum stays within 2^24 (any K <=
+ * 1024), otherwise off by at most (K / 16 + 32) * 2^-23 * sum_k |x[t,k] w[n,k]| (a
+ * rounding or truncation at each of K / 16 steps, which grows with K; with terms of one
+ * sign 9 * 2^-24 of the sum was seen at K = 8192 and 250 * 2^-24 at 65536).  The
+ * order of the sum depends on the sizes and max_sms, not on the data or the run.  Written to partials[r] of the fused step, out is a
  * row-parallel layer's partial.
  * Rules: K a multiple of 16, 16 <= K <= TW_MAX_K_Q8; T and N at most
  * 2^31 - 512, N >= 1; x, w and out 16-byte aligned, the scales 4-byte aligned;

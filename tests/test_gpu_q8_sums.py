@@ -1,5 +1,6 @@
 """The sums of the 8-bit product where fp32 is short of bits: whole numbers up to
-2^24 with odd low bits are exact.  3 tokens take the dot-product or the few-token matrix path, 7 the latter,
+2^24 with odd low bits (exact), and terms of one sign over a long K (the stated
+bound).  3 tokens take the dot-product or the few-token matrix path, 7 the latter,
 40 a split of K, 300 pairs of CTAs."""
 import numpy as np
 import pytest
@@ -52,3 +53,25 @@ def test_sums_that_climb_and_cancel_are_exact(T):
     partial = np.cumsum(f64(x)[:, None, :] * f64(w)[None, :20, :], axis=2)
     assert np.abs(partial).max() < 2 ** 24 and np.abs(want).max() < 2 ** 22
     assert np.array_equal(run(x, w), want)
+
+
+@pytest.mark.parametrize("quant", ["int8", "e4m3"])
+@pytest.mark.parametrize("K", [1024, 8192, 65536])
+@pytest.mark.parametrize("T", TOKENS)
+def test_terms_of_one_sign_keep_the_stated_bound(T, K, quant):
+    # Each running sum rounds or truncates by up to 2^-23 of itself at each of
+    # its K / 16 steps (and the joins, fewer than 32); terms of one sign keep it as
+    # large as it can be.  Unit scales, fp32 out: the last rounding is in the 32.
+    g = torch.Generator()
+    g.manual_seed(K + T)
+    N = 136
+    if quant == "int8":
+        x, w = whole(T, K, 1, 127, g), whole(N, K, 1, 127, g)
+    else:
+        x, w = (torch.rand(n, K, generator=g).mul(440).add(1).to(torch.float8_e4m3fn)
+                for n in (T, N))
+    want = f64(x) @ f64(w).T
+    err = np.abs(run(x, w) - want)
+    worst = (err / want).max() * 2 ** 24
+    print(f"{quant} T {T} K {K}: off by {worst:.2f} x 2^-24 of the sum")
+    assert (err <= (K / 16 + 32) * 2.0 ** -23 * want).all()
