@@ -248,8 +248,9 @@ int tw_split_launch(const void* const* partials, int n_parts,
 /* The fused step with 8-bit outputs: out[k][t,h] and out_scale[k][t] hold the
  * quantised y[t,:] = x / rms * weight for every destination k, residual_out[t,:]
  * = x in dtype as ever.  The fp32 row is quantised, not a rounded copy; its
- * largest magnitude is taken of x * weight, so that a row whose product
- * overflows fp32 counts as one that holds an infinity.  out_scale is a HOST
+ * largest magnitude is taken as max_h |x * weight| times 1 / rms, so that a row whose
+ * product overflows fp32 counts as one that holds an infinity, and one whose
+ * max_h |x * weight| is below 2^-117 as a zero row whatever its rms.  out_scale is a HOST
  * array of n_out DEVICE pointers.  Kernel chosen as by TW_PATH_AUTO.  qtype is a
  * tw_qtype; the alias rule covers the scales. */
 int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,

@@ -211,9 +211,9 @@ __global__ void __launch_bounds__(kClusterThreads)
         if constexpr (Q8) {
             float m = 0.f;
             for (uint32_t r = 0; r < csize; ++r) m = max_abs(m, cta_max[buf][r]);
-            rq = RowQuant(m, quant_top(p.qtype));
+            rq = RowQuant(m, inv, quant_top(p.qtype));
             if (crank == 0 && tid < p.n_out)
-                p.out_scale[tid][t] = row_scale(m, inv, quant_top(p.qtype));
+                p.out_scale[tid][t] = row_scale(rq.y, quant_top(p.qtype), rq.zero);
         }
         buf ^= 1;
 

@@ -254,11 +254,10 @@ __device__ __forceinline__ void sum_squares(float (&ss2)[2], const float (&x)[E]
 // q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  Row quantisation takes
 // the quotient as a division would (RowDivision); the norm multiplies by top /
 // max|v| (RowQuant).
-// Rows whose largest magnitude is below kQuantTiny (so small that top / max
-// would overflow or the scale lose bits as a subnormal) count as zero rows:
-// scale 0, values 0.  A row that holds a NaN or an infinity has no scale:
-// scale NaN, values 0.
-constexpr float kQuantTiny = 6.0185e-36f;  // 2^-117
+// Rows whose largest magnitude is below kQuantTiny (their scale would be a
+// subnormal and lose bits) count as zero rows: scale 0, values 0.  A row that holds
+// a NaN or an infinity has no scale: scale NaN, values 0.
+constexpr float kQuantTiny = 0x1p-117f;
 
 __device__ __forceinline__ float quant_top(int qtype) { return qtype == TW_INT8 ? 127.f : 448.f; }
 
@@ -317,23 +316,39 @@ __device__ __forceinline__ uint32_t pack_e4m3(float v0, float v1, float v2, floa
     return r;
 }
 
-// How the norm quantises a row, m = max|v| (NaN or infinite where the row holds
-// one): q = rne(v * mul), mul = top / m, so that no element pays a division; a
+// The scale of a row whose largest magnitude is m: m / top, the division's result
+// by Markstein's quotient (IBM J. Res. Dev. 34, 1990): p = rn(m c) with c = rn(1 /
+// top), then rn(p + (m - p top) c), the remainder being exact in a fused multiply-add
+// (equal to m / top for every fp32 m from kQuantTiny up).
+__device__ __forceinline__ float row_scale(float m, float top, bool zero) {
+    const float c = top == 127.f ? 1.f / 127.f : 1.f / 448.f;
+    const float p = m * c;
+    const float s = fmaf(fmaf(-p, top, m), c, p);
+    return !quant_finite(m) ? __uint_as_float(0x7fffffffu) : zero ? 0.f : s;
+}
+
+// How the norm quantises a row y = gain * v, m = max|v| (NaN or infinite where the
+// row holds one), gain = 1 / rms: the gain cancels out of q = rne(v * mul), mul = top
+// / m, and no element pays a division.  Whether the row is a zero row or holds an
+// infinity goes by max|y| = m * gain (a sum of squares that leaves fp32 makes the
+// gain 0 or infinite); by m as well where the row is that small before the gain.  A
 // quotient within two ulp of the middle of two codes may go to either.  The
 // reciprocal is an approximate one, off by at most an ulp; of m / 4, so that it is a
-// normal number for every m from kQuantTiny up (2 x 2048 x 4096 13.25 us against
-// 13.5 with a division).  The norm's fp32 values seldom lie in the very middle of
-// two 8-bit ones.
+// normal number for every m from kQuantTiny up (2 x 2048 x 4096 13.1 us, with a
+// division in every thread 2 % more).  The norm's fp32 values seldom lie in the very
+// middle of two 8-bit ones.
 struct RowQuant {
-    float mul;  // top / max|v|; 0 where every value is 0 by rule
-    bool zero;  // every value of the row is 0
+    float mul;  // top / max|v|
+    float y;    // max|y|
+    bool zero;  // every value of the row is 0, whatever mul makes of it
 
     RowQuant() = default;
-    __device__ __forceinline__ RowQuant(float m, float top) {
-        zero = !quant_finite(m) || m < kQuantTiny;
+    __device__ __forceinline__ RowQuant(float m, float gain, float top) {
+        y = m * gain;
+        zero = !(fminf(m, y) >= kQuantTiny && quant_finite(y));
         float inverse;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inverse) : "f"(m * 0.25f));
-        mul = zero ? 0.f : (top * 0.25f) * inverse;
+        mul = (top * 0.25f) * inverse;
     }
     __device__ __forceinline__ uint32_t codes(const float* v, int qtype) const {
         return qtype == TW_INT8
@@ -342,15 +357,12 @@ struct RowQuant {
     }
 };
 
-// How row quantisation does it: q = rne(v / s) with s = m / top as it is stored
+// How row quantisation does it: q = rne(v / s) with s the scale that it stores
 // and the quotient rounded as fp32 division rounds it.  bf16 rows hold many values in
 // the very middle of two codes (a v * mul that is not rounded first sends all of a
 // row's to the same side: 0.07 % of the codes of 1024 x 8192 normal values differed
 // from the definition's, against 0.015 % of a division's).
-//   s: by Markstein's quotient (IBM J. Res. Dev. 34, 1990), p = rn(m c) with c = rn(1 /
-// top), then rn(p + (m - p top) c), the remainder being exact in a fused multiply-add:
-// what the division gives for every fp32 m from kQuantTiny up.
-//   q: 1 / s is kept to some 45 bits as hi + lo, hi an approximate reciprocal and lo
+//   1 / s is kept to some 45 bits as hi + lo, hi an approximate reciprocal and lo
 // the rest (1 - s hi is exact in a fused multiply-add).  rn(v hi + rn(v lo)) is then
 // off v / s by at most half an ulp and 2^-21 of one, and right wherever v / s is a
 // float, the middle of two codes in particular: two packed operations for two elements
@@ -363,15 +375,12 @@ struct RowDivision {
     bool huge;  // quotients() takes v * 2^-64
 
     __device__ __forceinline__ RowDivision(float m, float top) {
-        const float c = top == 127.f ? 1.f / 127.f : 1.f / 448.f;
-        const float p = m * c;
-        scale = fmaf(fmaf(-p, top, m), c, p);
         huge = m > 0x1p60f;
         zero = !quant_finite(m) || m < kQuantTiny;
+        scale = row_scale(m, top, zero);
         const float s = huge ? scale * 0x1p-64f : scale;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(s));
         lo = fmaf(-s, hi, 1.f) * hi;
-        if (zero) scale = quant_finite(m) ? 0.f : __uint_as_float(0x7fffffffu);
     }
     // q[0..1] = v[0..1] / s.
     __device__ __forceinline__ void quotients(float* q, const float* v) const {
@@ -392,15 +401,6 @@ struct RowDivision {
         return qtype == TW_INT8 ? pack_int8(q, 1.f) : pack_e4m3(q[0], q[1], q[2], q[3]);
     }
 };
-
-// The scale of the row whose elements are gain * v: the gain (a norm's 1 / rms)
-// cancels out of q.  For the one thread that stores it: a second division in
-// every thread cost a norm of 2 x 2048 x 4096 3 % (13.8 us against 13.45), 5 %
-// on 8 SMs.
-__device__ __forceinline__ float row_scale(float m, float gain, float top) {
-    if (!quant_finite(m)) return __uint_as_float(0x7fffffffu);
-    return m < kQuantTiny ? 0.f * gain : __fdiv_rn(m * gain, top);
-}
 
 // max(|m|, |v|) over one vector's elements, NaN if any is.  bf16: two maxima side by
 // side in the halves of m (signs are of no meaning), without widening; max_abs_of

@@ -506,9 +506,9 @@ __global__ void __launch_bounds__(kRowsBlock, 1)
 #pragma unroll
                 for (int w = 0; w < kConsumerWarps; ++w)
                     m = max_abs(m, max_unit[j * kConsumerWarps + w]);
-                rq = RowQuant(m, quant_top(p.qtype));
+                rq = RowQuant(m, inv, quant_top(p.qtype));
                 if (tid < p.n_out && alive)
-                    p.out_scale[tid][t + j] = row_scale(m, inv, quant_top(p.qtype));
+                    p.out_scale[tid][t + j] = row_scale(rq.y, quant_top(p.qtype), rq.zero);
             }
 #pragma unroll
             for (int jj = 0; jj < NV; ++jj) {
@@ -802,9 +802,9 @@ __global__ void __launch_bounds__(kRowsBlock, 1)
 #pragma unroll
                 for (int w = 0; w < kGroupWarps; ++w)
                     m = max_abs(m, max_unit[j * kGroupWarps + w]);
-                rq = RowQuant(m, quant_top(p.qtype));
+                rq = RowQuant(m, inv, quant_top(p.qtype));
                 if (gtid < p.n_out && alive)
-                    p.out_scale[gtid][t + j] = row_scale(m, inv, quant_top(p.qtype));
+                    p.out_scale[gtid][t + j] = row_scale(rq.y, quant_top(p.qtype), rq.zero);
             }
 #pragma unroll
             for (int jj = 0; jj < NV; ++jj) {
