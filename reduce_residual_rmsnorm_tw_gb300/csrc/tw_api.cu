@@ -64,8 +64,10 @@ struct DeviceState {
     bool ready = false;
     int sm_count = 0;
     int smem_optin = 0;
-    bool cluster_ready = false;
-    const char* cluster_error = "";
+    bool cluster_ready[2] = {};  // without, with 8-bit outputs
+    const char* cluster_error[2] = {"", ""};
+    // Set-up of the 8-bit operators (cudaError_t as int, see DeviceInfo).
+    int norm_q8_error = 0, quantize_error = 0, gemv_error = 0, gemm_error = 0;
     // Clusters of 1, 2, 4, 8 CTAs that run at once, per kernel instantiation:
     // [0] with every CTA alone on its SM (budgeted launches), [1] with CTAs
     // free to share SMs; then [log2 cluster][dtype][vectors per thread 1, 2,
@@ -114,7 +116,8 @@ int device_state(DeviceState** out) {
         if (d.smem_optin < kExclusiveSmemBytes)
             return fail(TW_ERR_UNSUPPORTED, "device %d allows only %d bytes of shared memory",
                         dev, d.smem_optin);
-        if ((e = static_cast<cudaError_t>(rows_set_smem_limit(d.smem_optin))) != cudaSuccess ||
+        if ((e = static_cast<cudaError_t>(rows_set_smem_limit(d.smem_optin, false))) !=
+                cudaSuccess ||
             (e = static_cast<cudaError_t>(warp_set_smem_limit(d.smem_optin))) != cudaSuccess)
             return cuda_fail(e, "cudaFuncSetAttribute");
         // Every kernel of the library is loaded here, before any of them can
@@ -122,25 +125,29 @@ int device_state(DeviceState** out) {
         // its first launch, which may wait for running kernels).
         if ((e = static_cast<cudaError_t>(signal_prepare())) != cudaSuccess)
             return cuda_fail(e, "cudaFuncGetAttributes");
-        if ((e = static_cast<cudaError_t>(gemm_prepare(d.smem_optin, d.gemm_clusters))) !=
-                cudaSuccess ||
-            (e = static_cast<cudaError_t>(gemv_prepare(d.smem_optin))) != cudaSuccess ||
-            (e = static_cast<cudaError_t>(quantize_prepare(d.smem_optin))) != cudaSuccess)
-            return cuda_fail(e, "cudaFuncSetAttribute");
-        // The cluster kernel is optional: if it cannot be configured, that
-        // path reports TW_ERR_UNSUPPORTED and the others still run.
-        e = static_cast<cudaError_t>(cluster_set_attributes(d.smem_optin));
-        d.cluster_ready = e == cudaSuccess;
-        if (e != cudaSuccess) {
-            d.cluster_error = cudaGetErrorName(e);
-            (void)cudaGetLastError();  // clear the (non-sticky) launch-API error
+        // The 8-bit operators and the cluster kernel are optional: what cannot
+        // be configured reports TW_ERR_UNSUPPORTED and everything else still
+        // runs.  (cudaGetLastError clears the non-sticky launch-API error.)
+        const auto optional = [](int err) {
+            if (err != cudaSuccess) (void)cudaGetLastError();
+            return err;
+        };
+        d.norm_q8_error = optional(rows_set_smem_limit(d.smem_optin, true));
+        d.quantize_error = optional(quantize_prepare(d.smem_optin));
+        d.gemv_error = optional(gemv_prepare(d.smem_optin));
+        d.gemm_error = optional(gemm_prepare(d.smem_optin, d.gemm_clusters));
+        for (int q8 = 0; q8 < 2; ++q8) {
+            const int err = optional(cluster_set_attributes(d.smem_optin, q8 != 0));
+            d.cluster_ready[q8] = err == cudaSuccess;
+            d.cluster_error[q8] = cudaGetErrorName(static_cast<cudaError_t>(err));
         }
         for (int shared = 0; shared < 2; ++shared)
-            for (int i = 0; d.cluster_ready && i < 4; ++i)
+            for (int i = 0; i < 4; ++i)
                 for (int dt = 0; dt < 2; ++dt)
                     for (int v = 0; v < 3; ++v)
                         for (int q = 0; q < 4; ++q)
                             for (int q8 = 0; q8 < 2; ++q8) {
+                                if (!d.cluster_ready[q8]) continue;
                                 int n = 0;
                                 if (cluster_max_active(1 << i, shared ? 0 : kExclusiveSmemBytes,
                                                        dt, 1 << v, 2 << q, q8 != 0, &n) !=
@@ -367,6 +374,9 @@ int launch_range(const Args& a, DeviceState& d, int64_t t0, int64_t t1, int path
     // kernel's drain; a budgeted launch does not, so that at no time more than
     // max_sms SMs hold its CTAs.
     const bool pdl = a.max_sms >= d.sm_count;
+    if (a.q8 && d.norm_q8_error)
+        return fail(TW_ERR_UNSUPPORTED, "8-bit outputs unavailable on this device (%s)",
+                    cudaGetErrorName(static_cast<cudaError_t>(d.norm_q8_error)));
     Params p = make_params(a, d, t0, t1, smid_log);
     // L2 warming is for device memory; host-resident rows are read once,
     // in place.
@@ -375,7 +385,7 @@ int launch_range(const Args& a, DeviceState& d, int64_t t0, int64_t t1, int path
     int cluster = 1;
     while (cluster * 2 <= 8 && cluster * 2 <= sms) cluster *= 2;
     const bool cluster_ok =
-        d.cluster_ready && cluster_vectors_per_thread(p.row_bytes, cluster) != 0;
+        d.cluster_ready[a.q8] && cluster_vectors_per_thread(p.row_bytes, cluster) != 0;
     if (a.colsplit || a.ready) {
         if (path != TW_PATH_AUTO && path != TW_PATH_ROWS)
             return fail(TW_ERR_UNSUPPORTED,
@@ -452,9 +462,9 @@ int launch_range(const Args& a, DeviceState& d, int64_t t0, int64_t t1, int path
             staged && xs > static_cast<size_t>(kExclusiveSmemBytes) ? xs : kExclusiveSmemBytes;
         err = launch_warp(p, a.dtype, grid, smem, staged, pdl, stream);
     } else if (path == TW_PATH_CLUSTER) {
-        if (!d.cluster_ready)
+        if (!d.cluster_ready[a.q8])
             return fail(TW_ERR_UNSUPPORTED, "cluster kernel unavailable on this device (%s)",
-                        d.cluster_error);
+                        d.cluster_error[a.q8]);
         if (!cluster_ok)
             return fail(TW_ERR_UNSUPPORTED, "row of %lld bytes too long for a cluster of %d",
                         (long long)p.row_bytes, cluster);
@@ -604,8 +614,10 @@ int device_info(DeviceInfo* out) {
     const int rc = device_state(&d);
     if (rc != TW_OK) return rc;
     out->sm_count = d->sm_count;
-    out->smem_optin = d->smem_optin;
     out->status = d->status;
+    out->quantize_error = d->quantize_error;
+    out->gemv_error = d->gemv_error;
+    out->gemm_error = d->gemm_error;
     memcpy(out->gemm_clusters, d->gemm_clusters, sizeof(out->gemm_clusters));
     return TW_OK;
 }

@@ -292,19 +292,18 @@ int cluster_vectors_per_thread(int64_t row_bytes, int cluster) {
     return 0;
 }
 
-int cluster_set_attributes(int smem_optin) {
+int cluster_set_attributes(int smem_optin, bool q8) {
     // The kernel has a few bytes of static shared memory, so its dynamic
     // request stays at the exclusive-SM amount, not the full opt-in limit.
     if (smem_optin < kExclusiveSmemBytes + 1024) return static_cast<int>(cudaErrorInvalidValue);
     for (int dt = 0; dt < 2; ++dt)
         for (int v = 1; v <= kClusterMaxVpt; v *= 2)
-            for (int np = 2; np <= 16; np *= 2)
-                for (bool q8 : {false, true}) {
-                    cudaError_t e = cudaFuncSetAttribute(
-                        cluster_kernel_for(dt, v, np, q8),
-                        cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
-                    if (e != cudaSuccess) return static_cast<int>(e);
-                }
+            for (int np = 2; np <= 16; np *= 2) {
+                cudaError_t e = cudaFuncSetAttribute(cluster_kernel_for(dt, v, np, q8),
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kExclusiveSmemBytes);
+                if (e != cudaSuccess) return static_cast<int>(e);
+            }
     return 0;
 }
 

@@ -86,8 +86,10 @@ struct Params {
 // (set up on first use; tw_status, with the error recorded).
 struct DeviceInfo {
     int sm_count;
-    int smem_optin;
     unsigned int* status;  // device status word
+    // What setting an operator's kernels up answered (cudaError_t as int); where it
+    // is not 0 its calls report TW_ERR_UNSUPPORTED and everything else still runs.
+    int quantize_error, gemv_error, gemm_error;
     // Clusters of 1, 2, 4, 8 CTAs of the product kernels that run at once:
     // [CTAs per unit - 1][int8][log2 of the cluster].
     int gemm_clusters[2][2][4];
@@ -155,11 +157,11 @@ bool rows_two_pipes_fit(const Params& p, bool budgeted);
 // Instantiations with 8-bit outputs (nullptr: none).
 void* rows_q8_entry(int dtype, int nv, int unit, int mode);
 void* rows2_q8_entry(int dtype, int nv, int unit);
-// Raise the dynamic shared memory limit of every kernel instantiation on the
-// current device (cudaError_t as int).
-int rows_set_smem_limit(int smem_optin);
+// Raise the dynamic shared memory limit of every kernel instantiation with or
+// without 8-bit outputs on the current device (cudaError_t as int).
+int rows_set_smem_limit(int smem_optin, bool q8);
 int warp_set_smem_limit(int smem_optin);
-int cluster_set_attributes(int smem_optin);
+int cluster_set_attributes(int smem_optin, bool q8);
 // Load the readiness-flag producer kernel (tw_set_ready) on the current
 // device (cudaError_t as int).
 int signal_prepare();

@@ -27,6 +27,13 @@ int launch_status(int err, const char* what) {
     return refuse(TW_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
+// An operator whose kernels could not be set up on this device.
+int check_set_up(int err, const char* what) {
+    if (err == cudaSuccess) return TW_OK;
+    return refuse(TW_ERR_UNSUPPORTED, "%s unavailable on this device (%s)", what,
+                  cudaGetErrorName(static_cast<cudaError_t>(err)));
+}
+
 bool misaligned(const void* p, uintptr_t bytes) {
     return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) != 0;
 }
@@ -83,7 +90,9 @@ extern "C" int tw_quantize_rows_q8(const void* x, void* out, float* out_scale, i
         return refuse(TW_ERR_ALIAS, "x, out and out_scale overlap");
     if (t0 == t1) return TW_OK;
     tw::DeviceInfo d;
-    if ((rc = tw::device_info(&d)) != TW_OK) return rc;
+    if ((rc = tw::device_info(&d)) != TW_OK ||
+        (rc = tw::check_set_up(d.quantize_error, "row quantisation")) != TW_OK)
+        return rc;
     const tw::QuantParams p{x, out, out_scale, t0, t1, H, H * es, qtype};
     return tw::launch_status(tw::launch_quantize(p, dtype, max_sms, d.sm_count, stream),
                              "quantize_rows launch");
@@ -122,7 +131,10 @@ extern "C" int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
         return refuse(TW_ERR_ALIAS, "out overlaps an input");
     if (t0 == t1) return TW_OK;
     tw::DeviceInfo d;
-    if ((rc = tw::device_info(&d)) != TW_OK) return rc;
+    const bool few = t1 - t0 <= tw::kGemvTokens;
+    if ((rc = tw::device_info(&d)) != TW_OK ||
+        (rc = tw::check_set_up(few ? d.gemv_error : d.gemm_error, "8-bit product")) != TW_OK)
+        return rc;
     const tw::GemmArgs g{static_cast<const char*>(x) + t0 * K,
                          x_scale + t0,
                          w,
@@ -133,7 +145,7 @@ extern "C" int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
                          K,
                          dtype,
                          qtype};
-    const int err = g.M <= tw::kGemvTokens ? tw::launch_gemv(g, max_sms, d, stream)
-                                           : tw::launch_gemm(g, max_sms, d, stream);
+    const int err = few ? tw::launch_gemv(g, max_sms, d, stream)
+                        : tw::launch_gemm(g, max_sms, d, stream);
     return tw::launch_status(err, "gemm_q8 launch");
 }

@@ -101,22 +101,21 @@ bool rows_two_pipes_fit(const Params& p, bool budgeted) {
     return budgeted || stages_per_unit <= p.stages / 2;
 }
 
-int rows_set_smem_limit(int smem_optin) {
+int rows_set_smem_limit(int smem_optin, bool q8) {
     for (int dt = 0; dt < 2; ++dt)
-        for (bool q8 : {false, true})
-            for (int nv = 1; nv <= kRowsMaxVecs; ++nv)
-                for (int unit = 1; unit <= kRowsMaxUnit; unit *= 2) {
-                    void* fns[] = {rows_kernel_for(dt, nv, unit, kFixed, q8),
-                                   rows_kernel_for(dt, nv, unit, kClaim, q8),
-                                   rows_kernel_for(dt, nv, unit, kFlags, q8),
-                                   rows2_kernel_for(dt, nv, unit, q8)};
-                    for (void* fn : fns) {
-                        if (!fn) continue;
-                        cudaError_t e = cudaFuncSetAttribute(
-                            fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
-                        if (e != cudaSuccess) return static_cast<int>(e);
-                    }
+        for (int nv = 1; nv <= kRowsMaxVecs; ++nv)
+            for (int unit = 1; unit <= kRowsMaxUnit; unit *= 2) {
+                void* fns[] = {rows_kernel_for(dt, nv, unit, kFixed, q8),
+                               rows_kernel_for(dt, nv, unit, kClaim, q8),
+                               rows_kernel_for(dt, nv, unit, kFlags, q8),
+                               rows2_kernel_for(dt, nv, unit, q8)};
+                for (void* fn : fns) {
+                    if (!fn) continue;
+                    cudaError_t e = cudaFuncSetAttribute(
+                        fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
+                    if (e != cudaSuccess) return static_cast<int>(e);
                 }
+            }
     return 0;
 }
 
