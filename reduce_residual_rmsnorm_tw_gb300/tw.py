@@ -22,6 +22,10 @@ STATUS_NAMES = {0: "TW_OK", -1: "TW_ERR_INVALID_ARG", -2: "TW_ERR_ALIGNMENT",
 _DTYPES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32}
 TW_INT8, TW_E4M3 = 0, 1
 _QTYPES = {torch.int8: TW_INT8, torch.float8_e4m3fn: TW_E4M3}
+# The current stream's handle without a Stream object around it (a decode step's
+# kernel is over in the time that takes).  The call is private to torch: where it
+# is missing, the public one serves.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _ALL_SMS = 1 << 30  # clamped to the device's SM count by the library
 
 
@@ -106,9 +110,9 @@ def _check(rc):
 
 def _stream_handle(stream):
     if stream is None:
-        # The current stream's handle without a Stream object around it (a
-        # decode step's kernel is over in the time that takes).
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
