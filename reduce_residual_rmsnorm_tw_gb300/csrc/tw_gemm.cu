@@ -33,9 +33,9 @@
 // to back the SM clock falls to 1.5 to 1.9 GHz; with pauses between calls it
 // stays at 2.07 and 1024 tokens take 82 us (int8) and 43 (e4m3), 4096 tokens 300
 // (1.83 PFLOP/s) and 151 (3.63).  e4m3 at 1024: 1.7 waves of tiles on 76 pairs,
-// run as two.  int8 below 512 tokens: issue slots, for which the MMA warp (about
-// 650 clocks for a stage's wait, eight MMAs and commit) and sixteen widening warps
-// compete (when 256 tokens took 28.3 us, half the MMAs took it to 25.6, leaving
+// run as two.  int8 below 512 tokens: issue slots, for which the MMA warp (its wait,
+// eight MMAs and commit of a stage take about 680 clocks at 96 tokens to a tile, the
+// products 384) and sixteen widening warps compete (when 256 tokens took 28.3 us, half the MMAs took it to 25.6, leaving
 // out the widening's arithmetic to 24.2).
 #include <cuda.h>
 
@@ -63,8 +63,10 @@ constexpr int kWeightWarp = 0, kTokenWarp = 3, kEpilogueWarp = 4, kWidenWarp = 8
 __host__ __device__ constexpr int max_tokens(int cg, bool int8) {
     return cg == 1 ? 64 : (int8 ? 192 : 256);
 }
-// Largest token tile whose K is split: a join keeps room for it beside the ring
-// (wider tiles were never the best cut).
+// Largest token tile whose K is split: what a join receives takes its room from the
+// ring (32 to 56 KB at 128 columns).  256 columns over two pairs, not measured, would
+// cost 256 x 8192 x 8192 in e4m3 32.1 thousand clocks by the model below, the cut taken
+// (128 columns, K whole) 34.0.
 constexpr int kJoinTokens = 128;
 // Staging of the output: two chunks of 32 tokens (bf16) or 16 (fp32) x 128
 // channels for TMA to store.

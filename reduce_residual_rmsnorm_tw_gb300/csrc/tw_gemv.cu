@@ -119,8 +119,8 @@ __device__ __forceinline__ int dot16(const uint4& a, const uint4& b, int c) {
 // 8192 x 1024: 3.64 -> 3.05; 1024 bytes 15.2, 8192 bytes 17.5 and 3.05).
 constexpr int kWarm = 2048;
 
-// Blocks a warp has in flight, by what one costs in shared memory: 2 R pieces
-// of W per lane and one of x.
+// Slots of a warp's FIFO, by what a step costs in shared memory: 2 R pieces of W
+// per lane and one of x.  One slot is being read, so one step fewer is in flight.
 __host__ __device__ constexpr int ahead(int r) { return r == 2 ? 4 : 7; }
 __host__ __device__ constexpr int step_bytes(int r) { return (2 * r + 1) * 32 * 16; }
 __host__ __device__ constexpr int fifo_bytes(int warps, int r) {
@@ -138,8 +138,8 @@ __host__ __device__ constexpr int gemv_smem(int warps, int r) {
 // (4096 x 4096: 5.0 us against 5.4), and under an SM budget.
 //
 // The bytes in flight are what the HBM rate follows, so the loads go through a
-// FIFO in shared memory instead of registers, `ahead` steps deep: 128 KB of W
-// per SM.  Each lane reads back the pieces of W it copied itself.  The steps
+// FIFO in shared memory instead of registers, with ahead(R) - 1 steps in flight: 96
+// KB of W per SM.  Each lane reads back the pieces of W it copied itself.  The steps
 // run on across the CTA's channel groups, so that a group's reduction does not
 // drain the FIFO.
 template <bool INT8, int MT, int R, int kWarps>
