@@ -236,9 +236,10 @@ int tw_split_launch(const void* const* partials, int n_parts,
  * 8-bit values q with one fp32 scale s:
  *   s = max_h |v[h]| / top,  q[h] = round(v[h] / s),  v[h] ~ q[h] * s
  * with top = 127 (TW_INT8) or 448 (TW_E4M3), rounded to nearest even.
- * tw_quantize_rows_q8 rounds the fp32 quotient of v[h] and the s it stores.  The
- * norm takes v times top / max in fp32, so that a quotient within two ulp of the
- * middle between two values may go to either.  A row whose largest
+ * tw_quantize_rows_q8 rounds v times top / max to fp32 first (correctly but for 2^-20
+ * of an ulp, 2^-4 in rows above 2^100): of bf16 rows every q is the formula's, of fp32 rows a quotient within
+ * half an ulp of the middle between two values counts as the middle.  The norm's
+ * may go to either value within two ulp of the middle.  A row whose largest
  * magnitude is below 2^-117 is a zero row: s = 0, q = 0.  A row that holds a
  * NaN or an infinity: s = NaN, q = 0 (it stands for NaN throughout).  8-bit
  * tensors are [T, H] with row stride H bytes, 16-byte aligned; scales are fp32

@@ -251,9 +251,8 @@ __device__ __forceinline__ void sum_squares(float (&ss2)[2], const float (&x)[E]
 
 // ------------------------------------------------------ 8-bit outputs ---
 // A row v quantised to 8 bits with one scale: scale = max|v| / top and
-// q = rne(v / scale), top = 127 (int8) or 448 (e4m3).  Row quantisation takes
-// the quotient as a division would (RowDivision); the norm multiplies by top /
-// max|v| (RowQuant).
+// q = rne(v * top / max|v|), top = 127 (int8) or 448 (e4m3).  The norm multiplies
+// by a rounded top / max|v| (RowQuant), row quantisation by one of 44 bits (RowExact).
 // Rows whose largest magnitude is below kQuantTiny (their scale would be a
 // subnormal and lose bits) count as zero rows: scale 0, values 0.  A row that holds
 // a NaN or an infinity has no scale: scale NaN, values 0.
@@ -357,32 +356,35 @@ struct RowQuant {
     }
 };
 
-// How row quantisation does it: q = rne(v / s) with s the scale that it stores
-// and the quotient rounded as fp32 division rounds it.  bf16 rows hold many values in
-// the very middle of two codes (a v * mul that is not rounded first sends all of a
-// row's to the same side: 0.07 % of the codes of 1024 x 8192 normal values differed
-// from the definition's, against 0.015 % of a division's).
-//   1 / s is kept to some 45 bits as hi + lo, hi an approximate reciprocal and lo
-// the rest (1 - s hi is exact in a fused multiply-add).  rn(v hi + rn(v lo)) is then
-// off v / s by at most half an ulp and 2^-21 of one, and right wherever v / s is a
-// float, the middle of two codes in particular: two packed operations for two elements
-// instead of two divisions.  For lo to keep its bits, a row above 2^60 and its scale
-// are divided by 2^64 first (`huge`; values so small that this rounds them are 0 in 8
-// bits).  4096 x 8192 16.1 us, as with one multiplication by top / m.
-struct RowDivision {
-    float scale, hi, lo;
+// How row quantisation does it: q = rne(rn(v * top / m)), the quotient as good as
+// exact before it is rounded to fp32.  bf16 rows hold many values in the very middle
+// of two codes: multiplied by a rounded top / m, or divided by a rounded scale, they go
+// to the side that its rounding points to, a whole row's to the same (of the codes of
+// 1024 x 8192 normal values 0.055 % in int8 and 0.08 % in e4m3 are then off the
+// definition's, by a division 0.003 % and 0.016 %).
+//   top / m is kept to 44 bits as hi + lo: hi = rn(top r) with r an approximate
+// reciprocal of m, lo the rest, rn((top - m hi) r), all of m / 4 and top / 4, so that r
+// is a normal number for every m from kQuantTiny up.  rn(v hi + rn(v lo)) is right
+// wherever v * top / m is an fp32 number, the middle of two codes in particular, and
+// elsewhere rounds what is off by 2^-44 (rows above 2^100, whose lo is a subnormal:
+// 2^-28).  So every code of bf16 rows is the definition's (checked for all mantissas and
+// exponents), and of fp32 rows where the quotient is not within half an ulp of a
+// middle.  Two packed operations for two elements: 4096 x 8192 16.15 us, as with one
+// multiplication.
+struct RowExact {
+    float hi, lo;
     bool zero;  // every value of the row is 0
-    bool huge;  // quotients() takes v * 2^-64
 
-    __device__ __forceinline__ RowDivision(float m, float top) {
-        huge = m > 0x1p60f;
+    __device__ __forceinline__ RowExact(float m, float top) {
         zero = !quant_finite(m) || m < kQuantTiny;
-        scale = row_scale(m, top, zero);
-        const float s = huge ? scale * 0x1p-64f : scale;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(hi) : "f"(s));
-        lo = fmaf(-s, hi, 1.f) * hi;
+        m *= 0.25f;
+        top *= 0.25f;
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(m));
+        hi = top * r;
+        lo = fmaf(-m, hi, top) * r;
     }
-    // q[0..1] = v[0..1] / s.
+    // q[0..1] = v[0..1] * top / m.
     __device__ __forceinline__ void quotients(float* q, const float* v) const {
         asm("{\n\t.reg .b64 a, p, h, l;\n\t"
             "mov.b64 a, {%2, %3};\n\t"

@@ -1,6 +1,6 @@
 // tw_quant.cu -- rows quantised to 8 bits with one scale per token.
 //
-// s_t = max_h |x[t,h]| / top, q[t,h] = rne(x[t,h] / s_t): a row must be
+// s_t = max_h |x[t,h]| / top, q[t,h] = rne(x[t,h] * top / max): a row must be
 // seen whole before its first value is written, and is read only once: its
 // 16-byte vectors stay in registers between the two.  A row belongs to W
 // warps (W * 32 threads holding VPT vectors each), so short rows share a CTA
@@ -79,18 +79,11 @@ __global__ void __launch_bounds__(kQuantThreads, quantize_ctas(VPT, Vec<T>::kEle
             for (int w = 0; w < W; ++w) m = max_abs(m, warp_max[buf][slot * W + w]);
             buf ^= 1;
         }
-        const RowDivision rd(m, top);
-        if (live && rtid == 0) p.out_scale[t] = rd.scale;
-        if (rd.huge) {
-#pragma unroll
-            for (int k = 0; k < VPT; ++k) {
-                float f[E];
-                Vec<T>::to_float(raw[k], f);
-#pragma unroll
-                for (int e = 0; e < E; ++e) f[e] *= 0x1p-64f;
-                raw[k] = Vec<T>::from_float(f);
-            }
-        }
+        const RowExact row(m, top);
+        // By every thread: computed in the branch, it holds up the loads ahead (512 x
+        // 8192 on 8 SMs 50.6 us against 42.0).
+        const float scale = row_scale(m, top, row.zero);
+        if (live && rtid == 0) p.out_scale[t] = scale;
         void* out[1] = {p.out};
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
@@ -98,7 +91,7 @@ __global__ void __launch_bounds__(kQuantThreads, quantize_ctas(VPT, Vec<T>::kEle
             if (live && v < nvec) {
                 float f[E];
                 Vec<T>::to_float(raw[k], f);
-                store_q8<E>(out, 1, t * p.H + static_cast<int64_t>(v) * E, f, rd, p.qtype);
+                store_q8<E>(out, 1, t * p.H + static_cast<int64_t>(v) * E, f, row, p.qtype);
             }
         }
     }
