@@ -236,12 +236,13 @@ int tw_split_launch(const void* const* partials, int n_parts,
  * 8-bit values q with one fp32 scale s:
  *   s = max_h |v[h]| / top,  q[h] = round(v[h] / s),  v[h] ~ q[h] * s
  * with top = 127 (TW_INT8) or 448 (TW_E4M3), rounded to nearest even.
- * tw_quantize_rows_q8 rounds v times top / max to fp32 first (correctly but for 2^-20
- * of an ulp, 2^-4 in rows above 2^100): of bf16 rows every q is the formula's, of fp32 rows a quotient within
- * half an ulp of the middle between two values counts as the middle.  The norm's
- * may go to either value within two ulp of the middle.  A row whose largest
- * magnitude is below 2^-117 is a zero row: s = 0, q = 0.  A row that holds a
- * NaN or an infinity: s = NaN, q = 0 (it stands for NaN throughout).  8-bit
+ * tw_quantize_rows_q8 rounds v times top / max to fp32 first (correctly but for
+ * 2^-20 of an ulp, 2^-4 in rows above 2^100): of bf16 rows every q is the
+ * formula's, of fp32 rows a quotient within half an ulp of the middle between
+ * two values counts as the middle.  The norm's quotients may go to either value
+ * within two ulp of the middle.  A row whose largest magnitude is below 2^-117
+ * is a zero row: s = 0, q = 0.  A row that holds a NaN or an infinity: s = NaN,
+ * q = 0 (it stands for NaN throughout).  8-bit
  * tensors are [T, H] with row stride H bytes, 16-byte aligned; scales are fp32
  * [T], 4-byte aligned; only rows and scales of tokens [t0, t1) are written.
  * The other conventions are those at the top. */
@@ -249,11 +250,11 @@ int tw_split_launch(const void* const* partials, int n_parts,
 /* The fused step with 8-bit outputs: out[k][t,h] and out_scale[k][t] hold the
  * quantised y[t,:] = x / rms * weight for every destination k, residual_out[t,:]
  * = x in dtype as ever.  The fp32 row is quantised, not a rounded copy; its
- * largest magnitude is taken as max_h |x * weight| times 1 / rms, so that a row whose
- * product overflows fp32 counts as one that holds an infinity, and one whose
- * max_h |x * weight| is below 2^-117 as a zero row whatever its rms.  out_scale is a HOST
- * array of n_out DEVICE pointers.  Kernel chosen as by TW_PATH_AUTO.  qtype is a
- * tw_qtype; the alias rule covers the scales. */
+ * largest magnitude is taken as max_h |x * weight| times 1 / rms, so that a row
+ * whose product overflows fp32 counts as one that holds an infinity, and one
+ * whose max_h |x * weight| is below 2^-117 as a zero row whatever its rms.
+ * out_scale is a HOST array of n_out DEVICE pointers.  Kernel chosen as by
+ * TW_PATH_AUTO.  qtype is a tw_qtype; the alias rule covers the scales. */
 int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,
                                    const void* residual, const void* weight,
                                    void* const* out, float* const* out_scale,
@@ -273,13 +274,14 @@ int tw_quantize_rows_q8(const void* x, void* out, float* out_scale, int64_t T,
  *   out[t,n] = (sum_k x[t,k] * w[n,k]) * x_scale[t] * w_scale[n]
  * for t in [t0, t1), rounded once to dtype (TW_BF16 or TW_F32).  x [T, K] and
  * w [N, K] are 8-bit of one qtype (int8 values may use all of [-128, 127]),
- * out is [T, N]; all row-major and dense.  Products are exact.  int8 sums of
- * up to 4 tokens a call are 32-bit integers, rounded to fp32 once; all others are
- * held in fp32: exact for int8 while every partial sum stays within 2^24 (any K <=
- * 1024), otherwise off by at most (K / 16 + 32) * 2^-23 * sum_k |x[t,k] w[n,k]| (a
- * rounding or truncation at each of K / 16 steps, which grows with K; with terms of one
- * sign 9 * 2^-24 of the sum was seen at K = 8192 and 250 * 2^-24 at 65536).  The
- * order of the sum depends on the sizes and max_sms, not on the data or the run.  Written to partials[r] of the fused step, out is a
+ * out is [T, N]; all row-major and dense.  Products are exact.  int8 sums of up
+ * to 4 tokens a call are 32-bit integers, rounded to fp32 once; all others are
+ * held in fp32: exact for int8 while every partial sum stays within 2^24 (any
+ * K <= 1024), otherwise off by at most (K / 16 + 32) * 2^-23 * sum_k |x[t,k]
+ * w[n,k]| (a rounding or truncation at each of K / 16 steps: it grows with K;
+ * with terms of one sign 9 * 2^-24 of the sum was seen at K = 8192 and
+ * 250 * 2^-24 at 65536).  The order of the sum depends on the sizes and max_sms,
+ * not on the data or the run.  Written to partials[r] of the fused step, out is a
  * row-parallel layer's partial.
  * Rules: K a multiple of 16, 16 <= K <= TW_MAX_K_Q8; T and N at most
  * 2^31 - 512, N >= 1; x, w and out 16-byte aligned, the scales 4-byte aligned;

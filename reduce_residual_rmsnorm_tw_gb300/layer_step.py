@@ -65,7 +65,14 @@ def two_chunk_layer_step_q8(x, x_scale, w, w_scale, partials, residual, weight, 
     the fused steps write ``out`` in 8 bits with ``out_scale``, the next linear
     layer's input.  The product of chunk B leaves ``budget`` SMs to the fused
     step of chunk A beside it.  On return ``gemm_stream`` is ordered after the
-    whole step."""
+    whole step.
+
+    On one GPU this pays only where the product of a chunk lasts as long as the
+    fused step of the other on ``budget`` SMs: with 8 partials of 16384 x 8192
+    and K = 8192, 1500 us (int8, 32 SMs) against 1514 for the product and the
+    fused step called in turn on one stream, and 994 against 999 in e4m3 (48
+    SMs); with K = 1024 or 2048 tokens the calls in turn are faster (2048 x 8192
+    over K = 8192: 203 us against 221 in int8, 140 against 149 in e4m3)."""
     T = residual.shape[0]
     split = T // 2 if t_split is None else t_split
     sms = torch.cuda.get_device_properties(residual.device).multi_processor_count
