@@ -292,6 +292,102 @@ int tw_gemm_q8(const void* x, const float* x_scale, const void* w,
                int64_t t0, int64_t t1, int max_sms, void* stream, int dtype,
                int qtype);
 
+/* A layer with sandwich norms, gates and scales (an addition of this library;
+ * the pages' layer adds the block's output to the residual as it is).  The
+ * fused step with a norm of the block's output before the residual add:
+ *   s[t,h]            = sum_{r=0}^{n_parts-1} partials[r][t,h]
+ *   u[t,h]            = s[t,h] / sqrt(mean_h s[t,:]^2 + post_eps) * post_weight[h]
+ *   x[t,h]            = residual_scale * residual[t,h]
+ *                       + block_scale * gate[t / gate_tokens, h] * u[t,h]
+ *   residual_out[t,h] = x[t,h]                                 rounded to dtype
+ *   out[k][t,h]       = x[t,h] / sqrt(mean_h x[t,:]^2 + eps) * weight[h]
+ * post_weight NULL: no norm of the block's output, u = s (post_eps is then only
+ * checked).  gate NULL: no gate (a factor of 1; gate_tokens is not looked at).
+ * gate is [ceil(T / gate_tokens), H], dense: gate_tokens = 1 gives every token a
+ * row of its own, the tokens of a sequence give a row per sequence, T or more
+ * one row for all (a learned scale per feature).  All of it is held in fp32 (the
+ * partials summed in rank order) and rounded to dtype where it is stored; a sum
+ * of squares that leaves fp32 makes its norm's result 0, as in the plain step.
+ * Rules as for tw_fused_reduce_add_rmsnorm; post_weight and gate 16-byte aligned and
+ * apart from every output; post_eps finite and >= 0; block_scale and
+ * residual_scale finite; gate_tokens >= 1. */
+int tw_fused_reduce_postnorm_add_rmsnorm(
+    const void* const* partials, int n_parts, const void* post_weight, const void* gate,
+    int64_t gate_tokens, const void* residual, const void* weight, void* const* out, int n_out,
+    void* residual_out, int64_t T, int64_t H, float post_eps, float eps, float block_scale,
+    float residual_scale, int64_t t0, int64_t t1, int max_sms, void* stream, int dtype);
+
+/* The same with 8-bit outputs and a scale per token, quantised as by
+ * tw_fused_reduce_add_rmsnorm_q8. */
+int tw_fused_reduce_postnorm_add_rmsnorm_q8(
+    const void* const* partials, int n_parts, const void* post_weight, const void* gate,
+    int64_t gate_tokens, const void* residual, const void* weight, void* const* out,
+    float* const* out_scale, int n_out, void* residual_out, int64_t T, int64_t H, float post_eps,
+    float eps, float block_scale, float residual_scale, int64_t t0, int64_t t1, int max_sms,
+    void* stream, int dtype, int qtype);
+
+/* Weights in 4 bits with group scales, for decode steps that are bound by
+ * reading them (an addition of this library).  A weight row w[n,:] is held as
+ * 4-bit values q with a bf16 scale for every `group` (32, 64 or 128) consecutive
+ * k, the last group of a row short where K is not a multiple:
+ *   s = bf16(max_group |w| / top),  q[k] = round(w[k] / s),  w[k] ~ q[k] * s
+ * with top = 7 (TW_INT4) or 6 (TW_E2M1), both roundings to nearest even and exact
+ * (of the real quotients, for bf16 and fp32 weights).  A group whose largest
+ * magnitude is below 2^-117 is a zero group: s = 0, q = 0.  A group that holds a
+ * NaN or an infinity: s = NaN, q = 0 (it stands for NaN throughout).
+ *
+ * Packed form (tw_w4_bytes bytes, 16-byte aligned): tiles of 16 channels x 128 k,
+ * tile (n / 16, k / 128) at (n / 16 * ceil(K / 128) + k / 128) * tile_bytes with
+ * tile_bytes = 1024 + 4096 / group.  Channels and k beyond N and K hold q = 0 and
+ * s = 0.  With r = n % 16, c = k % 128:
+ *   the value is in the 32-bit word at byte r / 8 * 512 + (r % 8 * 4 + c / 8 % 4) * 16
+ *   + c / 32 * 4, value i = c % 8 of the word's eight in its low half if i is even
+ *   else its high half, there value v = i / 2 of four:
+ *     TW_INT4: q + 8 in bits 4 v .. 4 v + 3
+ *     TW_E2M1: sign at bit 15, 12, 14, 13, the other three bits at 6..8, 3..5, 9..11,
+ *              0..2 for v = 0, 1, 2, 3
+ *   the scale is the bf16 at byte 1024 + c / group * 32 + (r % 8 * 2 + r / 8) * 2. */
+typedef enum {
+    TW_INT4 = 0, /* integers, quantised to [-7, 7]; -8 may be held too */
+    TW_E2M1 = 1  /* 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
+} tw_wtype;
+
+/* Types of tw_gemm_w4's x. */
+typedef enum {
+    TW_X_BF16 = 0,
+    TW_X_F32 = 1,
+    TW_X_INT8 = 2, /* with a scale per token, as tw_*_q8 leave rows */
+    TW_X_E4M3 = 3
+} tw_xtype;
+
+/* Bytes of [N, K] weights in packed form.  1 <= N <= 2^31 - 512, K a multiple of
+ * 16 with 16 <= K <= TW_MAX_K_Q8 (the rules of every tw_*_w4 call). */
+int tw_w4_bytes(int64_t N, int64_t K, int group, size_t* bytes);
+
+/* w [N, K] (dtype, dense, 16-byte aligned) into packed form. */
+int tw_quantize_w4(const void* w, void* packed, int64_t N, int64_t K, int group, int max_sms,
+                   void* stream, int dtype, int wtype);
+
+/* The weights that packed form stands for, q * s rounded to dtype, as dense
+ * [N, K] rows: for a library product of many tokens. */
+int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int group, int max_sms,
+                     void* stream, int dtype, int wtype);
+
+/* A linear layer on 4-bit weights:
+ *   out[t,n] = (sum_k x[t,k] * w[n,k]) * x_scale[t]
+ * for t in [t0, t1), rounded once to dtype (TW_BF16 or TW_F32).  x is [T, K] of
+ * xtype; x_scale is fp32 [T] for 8-bit x and NULL otherwise; out is [T, N].  A
+ * group's products are exact and add up in fp32; the group's sum times its scale
+ * adds up over the groups in fp32 too (fp32 x is cut into three bf16 terms,
+ * without loss down to 2^-110 in magnitude).  The order of the sum depends on the
+ * sizes and max_sms only.  Made for few tokens: from some 64 tokens on,
+ * tw_dequantize_w4 and a library product are faster.
+ * Rules: T at most 2^31 - 512; x, packed and out 16-byte aligned, x_scale 4-byte
+ * aligned; out overlaps no input. */
+int tw_gemm_w4(const void* x, const float* x_scale, const void* packed, void* out, int64_t T,
+               int64_t N, int64_t K, int group, int64_t t0, int64_t t1, int max_sms,
+               void* stream, int xtype, int dtype, int wtype);
+
 /* The fused step for tensors in page-locked HOST memory (cudaHostAlloc or
  * cudaHostRegister): partials, residual, weight, out and residual_out are host
  * pointers with the layout and rules above.

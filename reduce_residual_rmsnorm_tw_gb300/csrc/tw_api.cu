@@ -68,6 +68,8 @@ struct DeviceState {
     const char* cluster_error[2] = {"", ""};
     // Set-up of the 8-bit operators (cudaError_t as int, see DeviceInfo).
     int norm_q8_error = 0, quantize_error = 0, gemv_error = 0, gemm_error = 0;
+    // Set-up of the step with two norms and of the 4-bit operators, likewise.
+    int postnorm_error = 0, w4_rows_error = 0, w4_gemm_error = 0;
     // Clusters of 1, 2, 4, 8 CTAs that run at once, per kernel instantiation:
     // [0] with every CTA alone on its SM (budgeted launches), [1] with CTAs
     // free to share SMs; then [log2 cluster][dtype][vectors per thread 1, 2,
@@ -136,6 +138,9 @@ int device_state(DeviceState** out) {
         d.quantize_error = optional(quantize_prepare(d.smem_optin));
         d.gemv_error = optional(gemv_prepare(d.smem_optin));
         d.gemm_error = optional(gemm_prepare(d.smem_optin, d.gemm_clusters));
+        d.postnorm_error = optional(postnorm_prepare(d.smem_optin));
+        d.w4_rows_error = optional(w4_rows_prepare(d.smem_optin));
+        d.w4_gemm_error = optional(w4_gemm_prepare(d.smem_optin));
         for (int q8 = 0; q8 < 2; ++q8) {
             const int err = optional(cluster_set_attributes(d.smem_optin, q8 != 0));
             d.cluster_ready[q8] = err == cudaSuccess;
@@ -197,6 +202,11 @@ struct Args {
     int q8 = 0;  // 8-bit outputs of type qtype, with out_scale[k][t] per token
     int qtype = 0;
     float* const* out_scale = nullptr;
+    int post = 0;  // a norm, gate and scales before the residual add
+    const void* post_weight = nullptr;
+    const void* gate = nullptr;
+    int64_t gate_tokens = 1;
+    float post_eps = 0.f, block_scale = 1.f, residual_scale = 1.f;
 };
 
 size_t elem_size(int dtype) { return dtype == TW_BF16 ? 2 : 4; }
@@ -272,12 +282,25 @@ int check_args(const Args& a) {
         }
     }
 
+    if (a.post) {
+        if (!(a.post_eps >= 0.f) || std::isinf(a.post_eps))
+            return fail(TW_ERR_INVALID_ARG, "post_eps must be finite and >= 0");
+        if (!std::isfinite(a.block_scale) || !std::isfinite(a.residual_scale))
+            return fail(TW_ERR_INVALID_ARG, "block_scale and residual_scale must be finite");
+        if (a.gate && a.gate_tokens < 1)
+            return fail(TW_ERR_INVALID_ARG, "gate_tokens %lld < 1", (long long)a.gate_tokens);
+        if (misaligned(a.post_weight) || misaligned(a.gate))
+            return fail(TW_ERR_ALIGNMENT, "post_weight and gate must be 16-byte aligned");
+    }
+
     // Aliasing: outputs (the destinations, residual_out, then the scales of
     // 8-bit destinations) against inputs and against each other.
     const size_t tb = static_cast<size_t>(a.T) * static_cast<size_t>(a.H) * es;
     const size_t wb = static_cast<size_t>(a.H) * es;
     const void* outs[2 * TW_MAX_OUTS + 1];
     size_t out_bytes[2 * TW_MAX_OUTS + 1];
+    // The gate's rows of tokens [0, T): at most T of them.
+    const size_t gb = a.gate && a.T > 0 ? ((a.T - 1) / a.gate_tokens + 1) * wb : 0;
     int n_outputs = 0;
     for (int k = 0; k < a.n_out; ++k) {
         outs[n_outputs] = a.out[k];
@@ -297,6 +320,9 @@ int check_args(const Args& a) {
             if (overlaps(o, ob, a.partials[r], tb))
                 return fail(TW_ERR_ALIAS, "an output overlaps partials[%d]", r);
         if (overlaps(o, ob, a.weight, wb)) return fail(TW_ERR_ALIAS, "an output overlaps weight");
+        if (a.post_weight && overlaps(o, ob, a.post_weight, wb))
+            return fail(TW_ERR_ALIAS, "an output overlaps post_weight");
+        if (overlaps(o, ob, a.gate, gb)) return fail(TW_ERR_ALIAS, "an output overlaps gate");
         if (overlaps(o, ob, a.residual, tb) && !(is_res_out && o == a.residual))
             return fail(TW_ERR_ALIAS, "an output overlaps residual (only residual_out == "
                         "residual, exactly, is allowed)");
@@ -483,6 +509,23 @@ int launch_range(const Args& a, DeviceState& d, int64_t t0, int64_t t1, int path
     return TW_OK;
 }
 
+// The step with a norm, gate and scales before the residual add.
+int fused_postnorm(const Args& a, void* stream) {
+    int rc = check_args(a);
+    if (rc != TW_OK) return rc;
+    if (a.t0 == a.t1) return TW_OK;
+    DeviceState* d = nullptr;
+    if ((rc = device_state(&d)) != TW_OK) return rc;
+    if (d->postnorm_error)
+        return fail(TW_ERR_UNSUPPORTED, "step with two norms unavailable on this device (%s)",
+                    cudaGetErrorName(static_cast<cudaError_t>(d->postnorm_error)));
+    const PostParams p{make_params(a, *d, a.t0, a.t1, nullptr), a.post_weight, a.gate,
+                       a.gate_tokens, a.post_eps, a.block_scale, a.residual_scale};
+    const int err = launch_postnorm(p, a.dtype, a.max_sms, d->sm_count, stream);
+    if (err != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(err), "kernel launch");
+    return TW_OK;
+}
+
 int fused(const Args& a, int path, uint32_t* smid_log, void* stream) {
     int rc = check_args(a);
     if (rc != TW_OK) return rc;
@@ -618,6 +661,8 @@ int device_info(DeviceInfo* out) {
     out->quantize_error = d->quantize_error;
     out->gemv_error = d->gemv_error;
     out->gemm_error = d->gemm_error;
+    out->w4_rows_error = d->w4_rows_error;
+    out->w4_gemm_error = d->w4_gemm_error;
     memcpy(out->gemm_clusters, d->gemm_clusters, sizeof(out->gemm_clusters));
     return TW_OK;
 }
@@ -689,6 +734,44 @@ int tw_fused_reduce_add_rmsnorm_q8(const void* const* partials, int n_parts,
     a.qtype = qtype;
     a.out_scale = out_scale;
     return tw::fused(a, TW_PATH_AUTO, nullptr, stream);
+}
+
+int tw_fused_reduce_postnorm_add_rmsnorm(
+    const void* const* partials, int n_parts, const void* post_weight, const void* gate,
+    int64_t gate_tokens, const void* residual, const void* weight, void* const* out, int n_out,
+    void* residual_out, int64_t T, int64_t H, float post_eps, float eps, float block_scale,
+    float residual_scale, int64_t t0, int64_t t1, int max_sms, void* stream, int dtype) {
+    Args a{partials, n_parts, residual, weight, out, n_out, residual_out,
+           T,        H,       eps,      t0,     t1,  max_sms, dtype};
+    a.post = 1;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.gate_tokens = gate_tokens;
+    a.post_eps = post_eps;
+    a.block_scale = block_scale;
+    a.residual_scale = residual_scale;
+    return tw::fused_postnorm(a, stream);
+}
+
+int tw_fused_reduce_postnorm_add_rmsnorm_q8(
+    const void* const* partials, int n_parts, const void* post_weight, const void* gate,
+    int64_t gate_tokens, const void* residual, const void* weight, void* const* out,
+    float* const* out_scale, int n_out, void* residual_out, int64_t T, int64_t H, float post_eps,
+    float eps, float block_scale, float residual_scale, int64_t t0, int64_t t1, int max_sms,
+    void* stream, int dtype, int qtype) {
+    Args a{partials, n_parts, residual, weight, out, n_out, residual_out,
+           T,        H,       eps,      t0,     t1,  max_sms, dtype};
+    a.post = 1;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.gate_tokens = gate_tokens;
+    a.post_eps = post_eps;
+    a.block_scale = block_scale;
+    a.residual_scale = residual_scale;
+    a.q8 = 1;
+    a.qtype = qtype;
+    a.out_scale = out_scale;
+    return tw::fused_postnorm(a, stream);
 }
 
 int tw_fused_reduce_add_rmsnorm(const void* const* partials, int n_parts, const void* residual,

@@ -90,6 +90,7 @@ struct DeviceInfo {
     // What setting an operator's kernels up answered (cudaError_t as int); where it
     // is not 0 its calls report TW_ERR_UNSUPPORTED and everything else still runs.
     int quantize_error, gemv_error, gemm_error;
+    int w4_rows_error, w4_gemm_error;
     // Clusters of 1, 2, 4, 8 CTAs of the product kernels that run at once:
     // [CTAs per unit - 1][int8][log2 of the cluster].
     int gemm_clusters[2][2][4];
@@ -126,6 +127,41 @@ int launch_gemv(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* strea
 int gemv_prepare(int smem_optin);
 int launch_gemm(const GemmArgs& g, int max_sms, const DeviceInfo& d, void* stream);
 int gemm_prepare(int smem_optin, int (*clusters)[2][4]);
+
+// Weights in 4 bits (tw_w4_rows.cu, tw_w4_gemm.cu; packed form: tw.h).
+constexpr int kW4Channels = 16, kW4Inner = 128;  // of a tile
+__host__ __device__ constexpr int w4_tile_bytes(int group) { return 1024 + 4096 / group; }
+struct W4RowsArgs {
+    const void* from;
+    void* to;
+    int64_t N, K;
+    int group, dtype, wtype;
+};
+int launch_w4_quantize(const W4RowsArgs& a, int max_sms, int sm_count, void* stream);
+int launch_w4_dequantize(const W4RowsArgs& a, int max_sms, int sm_count, void* stream);
+int w4_rows_prepare(int smem_optin);
+struct W4GemmArgs {
+    const void* x;         // [M, K], rows of the token range
+    const float* x_scale;  // [M] (8-bit x)
+    const void* packed;
+    void* out;             // [M, N]
+    int64_t M, N, K;
+    int group, xtype, dtype, wtype;
+};
+int launch_w4_gemm(const W4GemmArgs& a, int max_sms, int sm_count, void* stream);
+int w4_gemm_prepare(int smem_optin);
+
+// The step with a norm before the residual add (tw_postnorm.cu): what it has
+// beside the plain step's Params.
+struct PostParams {
+    Params p;
+    const void* post_weight;  // NULL: no norm of the block's output
+    const void* gate;         // NULL: no gate
+    int64_t gate_tokens;
+    float post_eps, block_scale, residual_scale;
+};
+int launch_postnorm(const PostParams& p, int dtype, int max_sms, int sm_count, void* stream);
+int postnorm_prepare(int smem_optin);
 
 // Record `message` as the calling thread's last error and return `code`.
 int set_last_error(int code, const char* message);

@@ -1,0 +1,342 @@
+// tw_postnorm.cu -- the fused step of a layer with sandwich norms: a norm of
+// the block's output, its gate and scales between the reduce and the residual
+// add.  Per token, in fp32:
+//   s = sum_r partials[r]              ranks in order
+//   u = s / sqrt(mean s^2 + post_eps) * post_weight
+//   x = residual_scale * residual + block_scale * gate * u
+//   residual_out = x,  out[k] = x / sqrt(mean x^2 + eps) * weight
+// Two reductions over the row, the second on what the first gives: the row
+// stays in registers for both.  (One pass over sums of s^2, r^2, r v and v^2
+// would give mean x^2 too, but loses it to cancellation where the block's output
+// and the residual nearly cancel.)  Bound by HBM: n_parts + 1 rows (and a gate's) in,
+// n_out + 1 out.
+#include "tw_tcgen05.cuh"
+
+namespace tw {
+namespace {
+
+constexpr int kThreads = 256;         // per CTA where a row has CTAs to itself
+constexpr int kClusterCta = 128;      // per CTA where a row has a cluster
+
+__device__ __forceinline__ uint32_t cluster_cta_count() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+// The start-up barrier of a cluster in two halves: every CTA must be running
+// before any writes into its shared memory.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// Write a float into CTA `rank`'s shared memory, at `local`'s place in this one's.
+__device__ __forceinline__ void st_peer_f32(float* local, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(map_to_rank(smem_addr(local), rank)),
+                 "f"(v)
+                 : "memory");
+}
+
+// VPT: 16-byte vectors of the row per thread; W: warps per row (of a CTA, where a
+// cluster of CTAs shares the row: CL).
+template <typename T, int VPT, int W, bool CL, bool Q8>
+__global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
+    postnorm_kernel(const __grid_constant__ PostParams pp) {
+    using V = Vec<T>;
+    constexpr int E = V::kElems;
+    constexpr int kWarps = (CL ? kClusterCta : kThreads) / 32;
+    constexpr int kRows = kWarps / W;
+    // Rows of partials whose loads are in flight at once.
+    constexpr int kAhead = VPT >= 8 ? 1 : 8 / VPT;
+    const Params& p = pp.p;
+    // Warp totals: [second reduction][buffer][warp], of sums and of maxima.
+    __shared__ float warp_part[2][2][kWarps];
+    __shared__ float warp_max[Q8 ? 2 : 1][kWarps];
+    // The CTAs' totals, written into every CTA of the cluster.
+    __shared__ float cta_part[CL ? 2 : 1][2][kClusterMaxSize];
+    __shared__ float cta_max[CL && Q8 ? 2 : 1][kClusterMaxSize];
+
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int slot = warp / W;                     // row of the CTA
+    const int rtid = threadIdx.x - slot * W * 32;  // thread of the row
+    uint32_t crank = 0, csize = 1;
+    if constexpr (CL) {
+        crank = cluster_cta_rank();
+        csize = cluster_cta_count();
+    }
+    const int nvec = static_cast<int>(p.row_bytes / 16);
+    const int per_cta = CL ? (nvec + static_cast<int>(csize) - 1) / static_cast<int>(csize) : nvec;
+    const int v_begin = static_cast<int>(crank) * per_cta;
+    const int v_end = v_begin + per_cta < nvec ? v_begin + per_cta : nvec;
+    const int64_t step = CL ? static_cast<int64_t>(gridDim.x / csize)
+                            : static_cast<int64_t>(gridDim.x) * kRows;
+    int64_t t = p.t0 + (CL ? static_cast<int64_t>(blockIdx.x / csize)
+                           : static_cast<int64_t>(blockIdx.x) * kRows + slot);
+    if constexpr (CL) cluster_arrive_relaxed();
+    grid_dependency_wait();
+    grid_launch_dependents();
+    bool peers_started = false;
+    int buf = 0;
+
+    // Sum (and maximum) of the row over its threads; `which`: 0 the block's
+    // norm, 1 the layer's.  Buffers alternate by row, so that a row's totals are
+    // read before any thread can be two rows on.
+    auto reduce = [&](int which, float v, float m, float* most) {
+        v = warp_sum(v);
+        if (Q8 && which) m = warp_max_abs(m);
+        if constexpr (W > 1 || CL) {
+            if (lane == 0) {
+                warp_part[which][buf][warp] = v;
+                if (Q8 && which) warp_max[Q8 ? buf : 0][warp] = m;
+            }
+            if constexpr (CL || W == kWarps)
+                __syncthreads();
+            else
+                named_barrier(1 + slot, W * 32);
+            v = 0.f;
+            m = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                v += warp_part[which][buf][slot * W + w];
+                if (Q8 && which) m = max_abs(m, warp_max[Q8 ? buf : 0][slot * W + w]);
+            }
+        }
+        if constexpr (CL) {
+            if (!peers_started) {
+                cluster_wait();
+                peers_started = true;
+            }
+            // Every CTA gets every total and adds them in rank order.
+            if (threadIdx.x < csize) {
+                st_peer_f32(&cta_part[which][buf][crank], threadIdx.x, v);
+                if (Q8 && which) st_peer_f32(&cta_max[Q8 ? buf : 0][crank], threadIdx.x, m);
+            }
+            cluster_barrier();
+            v = 0.f;
+            m = 0.f;
+            for (uint32_t r = 0; r < csize; ++r) {
+                v += cta_part[which][buf][r];
+                if (Q8 && which) m = max_abs(m, cta_max[Q8 ? buf : 0][r]);
+            }
+        }
+        *most = m;
+        return v;
+    };
+
+    // A group of warps takes its rows on its own; a CTA's groups that share a
+    // barrier (W == kWarps) are one.
+    for (; t < p.t1; t += step, buf ^= 1) {
+        const int64_t row_off = t * p.row_bytes;
+        float s[VPT][E];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e) s[k][e] = 0.f;
+        for (int r0 = 0; r0 < p.n_parts; r0 += kAhead) {
+            uint4 raw[kAhead][VPT];
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                for (int k = 0; k < VPT; ++k) {
+                    const int v = v_begin + rtid + k * W * 32;
+                    if (r0 + a < p.n_parts && v < v_end)
+                        raw[a][k] = ld_global_nc(static_cast<const char*>(p.partials[r0 + a]) +
+                                                 row_off + static_cast<int64_t>(v) * 16);
+                }
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+#pragma unroll
+                for (int k = 0; k < VPT; ++k)
+                    if (r0 + a < p.n_parts && v_begin + rtid + k * W * 32 < v_end)
+                        add_vec(s[k], raw[a][k], static_cast<T*>(nullptr));
+        }
+        // The residual (and the gate) on their way while the sum is reduced.
+        uint4 res[VPT], gate[VPT];
+        const char* gate_row =
+            pp.gate ? static_cast<const char*>(pp.gate) + t / pp.gate_tokens * p.row_bytes
+                    : nullptr;
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = v_begin + rtid + k * W * 32;
+            res[k] = v < v_end ? ld_global(static_cast<const char*>(p.residual) + row_off +
+                                           static_cast<int64_t>(v) * 16)
+                               : make_uint4(0, 0, 0, 0);
+            gate[k] = gate_row && v < v_end ? ld_global(gate_row + static_cast<int64_t>(v) * 16)
+                                            : make_uint4(0, 0, 0, 0);
+        }
+        float c = 1.f, most = 0.f;
+        if (pp.post_weight) {
+            float ss2[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) sum_squares<E>(ss2, s[k]);
+            const float total = reduce(0, ss2[0] + ss2[1], 0.f, &most);
+            c = rsqrtf(total * p.inv_H + pp.post_eps);
+        }
+        float ss2[2] = {0.f, 0.f}, m = 0.f;
+        uint4 wv[VPT];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = v_begin + rtid + k * W * 32;
+            const bool live = v < v_end;
+            float f[E];
+            if (pp.post_weight) {
+                V::to_float(live ? ld_global(static_cast<const char*>(pp.post_weight) + v * 16)
+                                 : make_uint4(0, 0, 0, 0), f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[k][e] = s[k][e] * c * f[e];
+            }
+            if (gate_row) {
+                V::to_float(gate[k], f);
+#pragma unroll
+                for (int e = 0; e < E; ++e) s[k][e] *= f[e];
+            }
+            V::to_float(res[k], f);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                s[k][e] = fmaf(pp.block_scale, s[k][e], pp.residual_scale * f[e]);
+            sum_squares<E>(ss2, s[k]);
+            wv[k] = live ? ld_global(static_cast<const char*>(p.weight) + v * 16)
+                         : make_uint4(0, 0, 0, 0);
+            if constexpr (Q8) m = max_abs_product<T>(m, s[k], wv[k]);
+        }
+        const float total = reduce(1, ss2[0] + ss2[1], m, &most);
+        const float inv = rsqrtf(total * p.inv_H + p.eps);
+        [[maybe_unused]] RowQuant rq;
+        if constexpr (Q8) {
+            rq = RowQuant(most, inv, quant_top(p.qtype));
+            if (crank == 0 && rtid < p.n_out)
+                p.out_scale[rtid][t] = row_scale(rq.y, quant_top(p.qtype), rq.zero);
+        }
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            const int v = v_begin + rtid + k * W * 32;
+            if (v >= v_end) continue;
+            const int64_t off = row_off + static_cast<int64_t>(v) * 16;
+            st_global_cs(static_cast<char*>(p.residual_out) + off, V::from_float(s[k]));
+            float w[E], y[E];
+            V::to_float(wv[k], w);
+            if constexpr (Q8) {
+#pragma unroll
+                for (int e = 0; e < E; e += 2) mul2(y + e, s[k] + e, w + e);
+                store_q8<E>(p.out, p.n_out, t * p.H + static_cast<int64_t>(v) * E, y, rq, p.qtype);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) y[e] = (s[k][e] * inv) * w[e];
+                const uint4 packed = V::from_float(y);
+                for (int o = 0; o < p.n_out; ++o)
+                    st_global_cs(static_cast<char*>(p.out[o]) + off, packed);
+            }
+        }
+    }
+    // A CTA with no token still completes the start-up barrier.
+    if constexpr (CL)
+        if (!peers_started) cluster_wait();
+}
+
+template <typename T, bool Q8>
+void* postnorm_rows_entry(int vpt, int w) {
+    switch (w * 16 + vpt) {
+        case 1 * 16 + 1: return reinterpret_cast<void*>(&postnorm_kernel<T, 1, 1, false, Q8>);
+        case 1 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 1, false, Q8>);
+        case 2 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 2, false, Q8>);
+        case 4 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, false, Q8>);
+        case 8 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 8, false, Q8>);
+        case 8 * 16 + 4: return reinterpret_cast<void*>(&postnorm_kernel<T, 4, 8, false, Q8>);
+        case 8 * 16 + 8: return reinterpret_cast<void*>(&postnorm_kernel<T, 8, 8, false, Q8>);
+        default: return nullptr;
+    }
+}
+
+template <typename T, bool Q8>
+void* postnorm_cluster_entry(int vpt) {
+    switch (vpt) {
+        case 1: return reinterpret_cast<void*>(&postnorm_kernel<T, 1, 4, true, Q8>);
+        case 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, true, Q8>);
+        case 4: return reinterpret_cast<void*>(&postnorm_kernel<T, 4, 4, true, Q8>);
+        default: return nullptr;
+    }
+}
+
+// The instantiation for vpt vectors per thread and w warps per row (0: a cluster).
+void* postnorm_kernel_for(int dtype, int vpt, int w, bool q8) {
+    if (dtype == TW_BF16) {
+        using T = __nv_bfloat16;
+        if (w == 0) return q8 ? postnorm_cluster_entry<T, true>(vpt)
+                              : postnorm_cluster_entry<T, false>(vpt);
+        return q8 ? postnorm_rows_entry<T, true>(vpt, w) : postnorm_rows_entry<T, false>(vpt, w);
+    }
+    if (w == 0) return q8 ? postnorm_cluster_entry<float, true>(vpt)
+                          : postnorm_cluster_entry<float, false>(vpt);
+    return q8 ? postnorm_rows_entry<float, true>(vpt, w)
+              : postnorm_rows_entry<float, false>(vpt, w);
+}
+
+// Warps per row and vectors per thread for rows of nvec vectors.
+void rows_shape(int64_t nvec, int* vpt, int* w) {
+    *w = 1;
+    *vpt = nvec <= 32 ? 1 : 2;
+    while (*w < 8 && nvec > static_cast<int64_t>(*w) * 32 * *vpt) *w *= 2;
+    while (nvec > static_cast<int64_t>(*w) * 32 * *vpt) *vpt *= 2;
+}
+
+// Tokens up to which a range goes to clusters (one per token).
+constexpr int64_t kClusterTokens = 64;
+
+}  // namespace
+
+int postnorm_prepare(int smem_optin) {
+    if (smem_optin < kExclusiveSmemBytes + 2048) return static_cast<int>(cudaErrorInvalidValue);
+    for (int dt = 0; dt < 2; ++dt)
+        for (int w = 0; w <= 8; w = w ? 2 * w : 1)
+            for (int vpt = 1; vpt <= 8; vpt *= 2)
+                for (bool q8 : {false, true}) {
+                    void* fn = postnorm_kernel_for(dt, vpt, w, q8);
+                    if (!fn) continue;
+                    cudaError_t e = cudaFuncSetAttribute(
+                        fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
+                    if (e != cudaSuccess) return static_cast<int>(e);
+                }
+    return 0;
+}
+
+int launch_postnorm(const PostParams& pp, int dtype, int max_sms, int sm_count, void* stream) {
+    const Params& p = pp.p;
+    const int64_t tokens = p.t1 - p.t0, nvec = p.row_bytes / 16;
+    const int64_t sms = max_sms < sm_count ? max_sms : sm_count;
+    // Under a budget each CTA is alone on its SM.
+    const bool whole = max_sms >= sm_count;
+    const size_t smem = whole ? 0 : kExclusiveSmemBytes;
+    int cluster = 1;
+    while (cluster * 2 <= 8 && cluster * 2 <= sms) cluster *= 2;
+    const int vc = cluster_vectors_per_thread(p.row_bytes, cluster);
+    if (tokens <= kClusterTokens && vc != 0 && (whole || tokens * cluster <= sms)) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(cluster * tokens));
+        cfg.blockDim = dim3(kClusterCta);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = static_cast<cudaStream_t>(stream);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = whole ? 2 : 1;
+        void* args[] = {const_cast<PostParams*>(&pp)};
+        return static_cast<int>(
+            cudaLaunchKernelExC(&cfg, postnorm_kernel_for(dtype, vc, 0, p.q8 != 0), args));
+    }
+    int vpt = 0, w = 0;
+    rows_shape(nvec, &vpt, &w);
+    const int64_t rows = kThreads / 32 / w;
+    const int64_t ctas = (tokens + rows - 1) / rows;
+    const int64_t most = !whole ? sms : w == 8 ? int64_t{1} << 30 : int64_t{8} * sms;
+    return launch_with_pdl(postnorm_kernel_for(dtype, vpt, w, p.q8 != 0), pp,
+                           static_cast<int>(ctas < most ? ctas : most), kThreads, smem, whole,
+                           stream);
+}
+
+}  // namespace tw

@@ -22,6 +22,8 @@ STATUS_NAMES = {0: "TW_OK", -1: "TW_ERR_INVALID_ARG", -2: "TW_ERR_ALIGNMENT",
 _DTYPES = {torch.bfloat16: TW_BF16, torch.float32: TW_F32}
 TW_INT8, TW_E4M3 = 0, 1
 _QTYPES = {torch.int8: TW_INT8, torch.float8_e4m3fn: TW_E4M3}
+WTYPES = {"int4": 0, "e2m1": 1}
+_XTYPES = {torch.bfloat16: 0, torch.float32: 1, torch.int8: 2, torch.float8_e4m3fn: 3}
 # The current stream's handle without a Stream object around it (a decode step's
 # kernel is over in the time that takes).  The call is private to torch: where it
 # is missing, the public one serves.
@@ -78,6 +80,25 @@ def load():
     lib.tw_gemm_q8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, ctypes.c_int, vp,
                                ctypes.c_int, ctypes.c_int]
     lib.tw_gemm_q8.restype = ctypes.c_int
+    floats = [ctypes.c_float] * 4
+    lib.tw_fused_reduce_postnorm_add_rmsnorm.argtypes = [
+        pp, ctypes.c_int, vp, vp, i64, vp, vp, pp, ctypes.c_int, vp, i64, i64, *floats, i64, i64,
+        ctypes.c_int, vp, ctypes.c_int]
+    lib.tw_fused_reduce_postnorm_add_rmsnorm.restype = ctypes.c_int
+    lib.tw_fused_reduce_postnorm_add_rmsnorm_q8.argtypes = [
+        pp, ctypes.c_int, vp, vp, i64, vp, vp, pp, pp, ctypes.c_int, vp, i64, i64, *floats, i64,
+        i64, ctypes.c_int, vp, ctypes.c_int, ctypes.c_int]
+    lib.tw_fused_reduce_postnorm_add_rmsnorm_q8.restype = ctypes.c_int
+    lib.tw_w4_bytes.argtypes = [i64, i64, ctypes.c_int, ctypes.POINTER(ctypes.c_size_t)]
+    lib.tw_w4_bytes.restype = ctypes.c_int
+    for name in ("tw_quantize_w4", "tw_dequantize_w4"):
+        fn = getattr(lib, name)
+        fn.argtypes = [vp, vp, i64, i64, ctypes.c_int, ctypes.c_int, vp, ctypes.c_int,
+                       ctypes.c_int]
+        fn.restype = ctypes.c_int
+    lib.tw_gemm_w4.argtypes = [vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, i64, i64,
+                               ctypes.c_int, vp, ctypes.c_int, ctypes.c_int, ctypes.c_int]
+    lib.tw_gemm_w4.restype = ctypes.c_int
     lib.tw_split_launch.argtypes = [pp, ctypes.c_int, vp, vp, pp, ctypes.c_int,
                                     vp, i64, i64, ctypes.c_float, i64,
                                     ctypes.c_int, vp, vp, ctypes.c_int]
@@ -361,6 +382,196 @@ def tw_gemm_q8(x, x_scale, w, w_scale, out, t0=0, t1=None, max_sms=None, stream=
         x.data_ptr(), x_scale.data_ptr(), w.data_ptr(), w_scale.data_ptr(), out.data_ptr(), T, N,
         K, t0, T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
         _stream_handle(stream), _DTYPES[out.dtype], qt))
+
+
+def _optional(name, t, shape, dtype, dev):
+    """The pointer of a tensor that may be left out."""
+    if t is None:
+        return None
+    _dense(name, t, shape, dtype)
+    if t.get_device() != dev:
+        raise ValueError("every tensor must be on the current CUDA device")
+    return t.data_ptr()
+
+
+def _postnorm(entry, partials, residual, weight, out, out_scale, residual_out, eps, post_weight,
+              post_eps, gate, gate_tokens, block_scale, residual_scale, t0, t1, max_sms, stream):
+    if residual.dim() != 2:
+        raise ValueError("residual must be [T, H]")
+    shape, dtype = residual.shape, residual.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"dtype {dtype} not supported (bfloat16 or float32)")
+    T, H = shape
+    n, n_out = len(partials), len(out)
+    if not n or not n_out:
+        raise ValueError("need at least one partial and one destination")
+    dev = torch.cuda.current_device() if residual.is_cuda else -1
+    p_arr = _pointers("partials", partials, shape, dtype, dev)
+    scales, tail = (), (_DTYPES[dtype],)
+    if out_scale is None:
+        o_arr = _pointers("out", out, shape, dtype, dev)
+    else:
+        if len(out_scale) != n_out:
+            raise ValueError("need a scale tensor for each destination")
+        tail += (_quantised(out[0]),)
+        o_arr = _pointers("out", out, shape, out[0].dtype, dev)
+        scales = (_pointers("out_scale", out_scale, (T,), torch.float32, dev),)
+    _dense("residual", residual, shape, dtype)
+    _dense("residual_out", residual_out, shape, dtype)
+    _dense("weight", weight, (H,), dtype)
+    post = _optional("post_weight", post_weight, (H,), dtype, dev)
+    if gate is not None and gate_tokens < 1:
+        raise ValueError("gate_tokens must be at least 1")
+    g = None if gate is None else _optional("gate", gate, (-(-T // gate_tokens), H), dtype, dev)
+    _on_current_device(residual, weight, residual_out)
+    if T == 0:
+        return
+    _check(entry(p_arr, n, post, g, gate_tokens, residual.data_ptr(), weight.data_ptr(), o_arr,
+                 *scales, n_out, residual_out.data_ptr(), T, H,
+                 eps if post_eps is None else post_eps, eps, block_scale, residual_scale, t0,
+                 T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
+                 _stream_handle(stream), *tail))
+
+
+def tw_fused_reduce_postnorm_add_rmsnorm(partials, residual, weight, out, residual_out, eps,
+                                         post_weight=None, post_eps=None, gate=None,
+                                         gate_tokens=1, block_scale=1.0, residual_scale=1.0,
+                                         t0=0, t1=None, max_sms=None, stream=None):
+    """The fused step with a norm of the block's output (``post_weight`` [H],
+    ``post_eps``: default ``eps``), its gate and scales before the residual add:
+    x = residual_scale * residual + block_scale * gate * RMSNorm(sum partials).
+    Without ``post_weight`` the sum is not normalised.  ``gate`` is
+    [ceil(T / gate_tokens), H]: a row for every ``gate_tokens`` tokens."""
+    _postnorm(load().tw_fused_reduce_postnorm_add_rmsnorm, partials, residual, weight, out, None,
+              residual_out, eps, post_weight, post_eps, gate, gate_tokens, block_scale,
+              residual_scale, t0, t1, max_sms, stream)
+
+
+def tw_fused_reduce_postnorm_add_rmsnorm_q8(partials, residual, weight, out, out_scale,
+                                            residual_out, eps, post_weight=None, post_eps=None,
+                                            gate=None, gate_tokens=1, block_scale=1.0,
+                                            residual_scale=1.0, t0=0, t1=None, max_sms=None,
+                                            stream=None):
+    """The same with ``out`` in 8 bits (int8 or float8_e4m3fn) and one scale per
+    token in ``out_scale``, as in tw_fused_reduce_add_rmsnorm_q8."""
+    _postnorm(load().tw_fused_reduce_postnorm_add_rmsnorm_q8, partials, residual, weight, out,
+              list(out_scale), residual_out, eps, post_weight, post_eps, gate, gate_tokens,
+              block_scale, residual_scale, t0, t1, max_sms, stream)
+
+
+class W4Weight:
+    """Weights [n, k] in 4 bits ("int4" or "e2m1") with a bf16 scale for every
+    ``group`` consecutive k of a channel, in the packed form of ``include/tw.h``:
+    ``packed`` (uint8) holds them.  tw_quantize_w4 fills one in, from_values takes
+    a checkpoint's values and scales."""
+
+    def __init__(self, n, k, group=128, kind="int4", device=None):
+        if kind not in WTYPES:
+            raise ValueError(f"kind {kind} is not one of {sorted(WTYPES)}")
+        size = ctypes.c_size_t()
+        _check(load().tw_w4_bytes(n, k, group, ctypes.byref(size)))
+        self.n, self.k, self.group, self.kind = n, k, group, kind
+        self.wtype = WTYPES[kind]
+        self.packed = torch.empty(size.value, dtype=torch.uint8,
+                                  device="cuda" if device is None else device)
+
+    @classmethod
+    def from_values(cls, values, scale, group=128, kind="int4"):
+        """Lay out ``values`` [n, k] (of the kind's values: -8 .. 7, or 0, 0.5, 1, 1.5, 2,
+        3, 4, 6 and their negatives) with ``scale`` [n, ceil(k / group)] (bf16 numbers), on
+        the tensors' device.  Done with torch operations, once, when a model is loaded."""
+        n, k = values.shape
+        self = cls(n, k, group, kind, values.device)
+        if scale.shape != (n, -(-k // group)):
+            raise ValueError(f"scale must be [{n}, {-(-k // group)}]")
+        held = scale.to(torch.bfloat16)
+        if not torch.equal(held.float().nan_to_num(-1.0), scale.float().nan_to_num(-1.0)):
+            raise ValueError("scale must hold bf16 numbers")
+        stripes, tiles = -(-n // 16), -(-k // 128)
+        v = torch.zeros(stripes * 16, tiles * 128, dtype=torch.float32, device=values.device)
+        v[:n, :k] = values
+        if kind == "int4":
+            code = v.round().clamp(-8, 7)
+            exact, code = code, code.to(torch.int32) + 8
+            fields = [(15, 4 * i, 0) for i in range(4)]
+        else:
+            grid = torch.tensor([0, 1, 2, 3, 4, 4, 5, 5, 6, 6, 6, 6, 7], device=v.device)
+            level = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=v.device)
+            magnitude = grid[(v.abs() * 2).clamp(0, 12).nan_to_num().to(torch.int64)]
+            exact = torch.copysign(level[magnitude], v)
+            code = magnitude.to(torch.int32) + torch.signbit(v).to(torch.int32) * 8
+            # Where the three low bits and the sign of a word's values go.
+            fields = [(7, 6, 15), (7, 3, 12), (7, 9, 14), (7, 0, 13)]
+        if not torch.equal(exact, v):
+            raise ValueError(f"values hold numbers that {kind} does not")
+        # [stripe, half, row, tile, k / 32, k / 8 % 4, k / 2 % 4, k % 2]
+        code = code.view(stripes, 2, 8, tiles, 4, 4, 4, 2)
+        word = torch.zeros(code.shape[:6], dtype=torch.int32, device=v.device)
+        for i, (mask, at, sign) in enumerate(fields):
+            for h in range(2):
+                c = code[..., i, h]
+                word |= (c & mask) << (at + 16 * h)
+                if kind == "e2m1":
+                    word |= (c >> 3) << (sign + 16 * h)
+        word = word.permute(0, 3, 1, 2, 5, 4).contiguous().view(torch.uint8)
+        s = torch.zeros(stripes * 16, tiles * 128 // group, dtype=torch.bfloat16,
+                        device=v.device)
+        s[:n, :scale.shape[1]] = held
+        s = s.view(stripes, 2, 8, tiles, 128 // group).permute(0, 3, 4, 2, 1).contiguous()
+        self.packed.copy_(torch.cat([word.reshape(stripes, tiles, 1024),
+                                     s.view(torch.uint8).reshape(stripes, tiles, -1)],
+                                    dim=2).reshape(-1))
+        return self
+
+
+def tw_quantize_w4(w, into, max_sms=None, stream=None):
+    """Quantise ``w`` ([n, k] bfloat16 or float32) into ``into``, a W4Weight."""
+    if w.dtype not in _DTYPES:
+        raise ValueError(f"dtype {w.dtype} not supported (bfloat16 or float32)")
+    _dense("w", w, (into.n, into.k), w.dtype)
+    _on_current_device(w, into.packed)
+    _check(load().tw_quantize_w4(
+        w.data_ptr(), into.packed.data_ptr(), into.n, into.k, into.group,
+        _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[w.dtype],
+        into.wtype))
+
+
+def tw_dequantize_w4(w, out, max_sms=None, stream=None):
+    """The weights that ``w`` (a W4Weight) stands for, into ``out`` ([n, k]
+    bfloat16 or float32)."""
+    if out.dtype not in _DTYPES:
+        raise ValueError(f"dtype {out.dtype} not supported (bfloat16 or float32)")
+    _dense("out", out, (w.n, w.k), out.dtype)
+    _on_current_device(out, w.packed)
+    _check(load().tw_dequantize_w4(
+        w.packed.data_ptr(), out.data_ptr(), w.n, w.k, w.group,
+        _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[out.dtype],
+        w.wtype))
+
+
+def tw_gemm_w4(x, w, out, x_scale=None, t0=0, t1=None, max_sms=None, stream=None):
+    """out[t, n] = sum_k x[t, k] * w[n, k] on rows [t0, t1): ``x`` [T, k] bfloat16
+    or float32, or int8 or float8_e4m3fn with ``x_scale`` [T]; ``w`` a W4Weight;
+    ``out`` [T, n] bfloat16 or float32."""
+    if x.dim() != 2 or x.shape[1] != w.k:
+        raise ValueError(f"x must be [T, {w.k}]")
+    T = x.shape[0]
+    xt = _XTYPES.get(x.dtype)
+    if xt is None or out.dtype not in _DTYPES:
+        raise ValueError(f"dtypes {x.dtype}, {out.dtype} not supported")
+    if (x_scale is None) != (xt < 2):
+        raise ValueError("x_scale goes with 8-bit x, and only with it")
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    _dense("out", out, (T, w.n), out.dtype)
+    _on_current_device(x, w.packed, out)
+    scale = _optional("x_scale", x_scale, (T,), torch.float32, x.get_device())
+    if T == 0:
+        return
+    _check(load().tw_gemm_w4(
+        x.data_ptr(), scale, w.packed.data_ptr(), out.data_ptr(), T, w.n, w.k, w.group, t0,
+        T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
+        _stream_handle(stream), xt, _DTYPES[out.dtype], w.wtype))
 
 
 def tw_split_launch(partials, residual, weight, out, residual_out, eps,
