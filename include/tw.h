@@ -346,7 +346,7 @@ int tw_fused_reduce_postnorm_add_rmsnorm_q8(
  *     TW_INT4: q + 8 in bits 4 v .. 4 v + 3
  *     TW_E2M1: sign at bit 15, 12, 14, 13, the other three bits at 6..8, 3..5, 9..11,
  *              0..2 for v = 0, 1, 2, 3
- *   the scale is the bf16 at byte 1024 + c / group * 32 + (r % 8 * 2 + r / 8) * 2. */
+ *   the scale is the bf16 at byte 1024 + r % 8 * (512 / group) + c / group * 4 + r / 8 * 2. */
 typedef enum {
     TW_INT4 = 0, /* integers, quantised to [-7, 7]; -8 may be held too */
     TW_E2M1 = 1  /* 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives */
@@ -379,7 +379,7 @@ int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int grou
  * xtype; x_scale is fp32 [T] for 8-bit x and NULL otherwise; out is [T, N].  A
  * group's products are exact and add up in fp32; the group's sum times its scale
  * adds up over the groups in fp32 too (fp32 x is cut into three bf16 terms,
- * without loss down to 2^-110 in magnitude).  The order of the sum depends on the
+ * without loss down to 2^-96 in magnitude).  The order of the sum depends on the
  * sizes and max_sms only.  Made for few tokens: from some 64 tokens on,
  * tw_dequantize_w4 and a library product are faster.
  * Rules: T at most 2^31 - 512; x, packed and out 16-byte aligned, x_scale 4-byte

@@ -76,6 +76,7 @@ struct DeviceState {
     // 4][partials held 2, 4, 8, 16][8-bit outputs].
     int max_clusters[2][4][2][3][4][2] = {};
     int gemm_clusters[2][2][4] = {};  // see DeviceInfo
+    int w4_clusters[4] = {};          // see DeviceInfo
     unsigned int* status = nullptr;
     cudaEvent_t fork = nullptr;
     cudaEvent_t join = nullptr;
@@ -140,7 +141,7 @@ int device_state(DeviceState** out) {
         d.gemm_error = optional(gemm_prepare(d.smem_optin, d.gemm_clusters));
         d.postnorm_error = optional(postnorm_prepare(d.smem_optin));
         d.w4_rows_error = optional(w4_rows_prepare(d.smem_optin));
-        d.w4_gemm_error = optional(w4_gemm_prepare(d.smem_optin));
+        d.w4_gemm_error = optional(w4_gemm_prepare(d.smem_optin, d.w4_clusters));
         for (int q8 = 0; q8 < 2; ++q8) {
             const int err = optional(cluster_set_attributes(d.smem_optin, q8 != 0));
             d.cluster_ready[q8] = err == cudaSuccess;
@@ -663,6 +664,8 @@ int device_info(DeviceInfo* out) {
     out->gemm_error = d->gemm_error;
     out->w4_rows_error = d->w4_rows_error;
     out->w4_gemm_error = d->w4_gemm_error;
+    out->smem_optin = d->smem_optin;
+    memcpy(out->w4_clusters, d->w4_clusters, sizeof(out->w4_clusters));
     memcpy(out->gemm_clusters, d->gemm_clusters, sizeof(out->gemm_clusters));
     return TW_OK;
 }

@@ -91,6 +91,8 @@ struct DeviceInfo {
     // is not 0 its calls report TW_ERR_UNSUPPORTED and everything else still runs.
     int quantize_error, gemv_error, gemm_error;
     int w4_rows_error, w4_gemm_error;
+    int smem_optin;
+    int w4_clusters[4];  // of 1, 2, 4, 8 CTAs of the 4-bit product that run at once
     // Clusters of 1, 2, 4, 8 CTAs of the product kernels that run at once:
     // [CTAs per unit - 1][int8][log2 of the cluster].
     int gemm_clusters[2][2][4];
@@ -148,8 +150,8 @@ struct W4GemmArgs {
     int64_t M, N, K;
     int group, xtype, dtype, wtype;
 };
-int launch_w4_gemm(const W4GemmArgs& a, int max_sms, int sm_count, void* stream);
-int w4_gemm_prepare(int smem_optin);
+int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* stream);
+int w4_gemm_prepare(int smem_optin, int* clusters);
 
 // The step with a norm before the residual add (tw_postnorm.cu): what it has
 // beside the plain step's Params.

@@ -162,6 +162,6 @@ extern "C" int tw_gemm_w4(const void* x, const float* x_scale, const void* packe
                            xtype,
                            dtype,
                            wtype};
-    return tw::launch_status(tw::launch_w4_gemm(a, max_sms, d.sm_count, stream),
+    return tw::launch_status(tw::launch_w4_gemm(a, max_sms, d, stream),
                              "gemm_w4 launch");
 }

@@ -139,7 +139,7 @@ __device__ __forceinline__ int word_at(int row, int kk) {
     return row / 8 * 512 + (row % 8 * 4 + kk % 4) * 16 + kk / 4 * 4;
 }
 __device__ __forceinline__ int scale_at(int row, int kk, int group) {
-    return 1024 + kk * 8 / group * 32 + (row % 8 * 2 + row / 8) * 2;
+    return 1024 + row % 8 * (512 / group) + kk * 8 / group * 4 + row / 8 * 2;
 }
 
 // kDepth: steps (of two channels) whose loads are in flight at once.

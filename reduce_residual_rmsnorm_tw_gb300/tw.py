@@ -517,7 +517,7 @@ class W4Weight:
         s = torch.zeros(stripes * 16, tiles * 128 // group, dtype=torch.bfloat16,
                         device=v.device)
         s[:n, :scale.shape[1]] = held
-        s = s.view(stripes, 2, 8, tiles, 128 // group).permute(0, 3, 4, 2, 1).contiguous()
+        s = s.view(stripes, 2, 8, tiles, 128 // group).permute(0, 3, 2, 4, 1).contiguous()
         self.packed.copy_(torch.cat([word.reshape(stripes, tiles, 1024),
                                      s.view(torch.uint8).reshape(stripes, tiles, -1)],
                                     dim=2).reshape(-1))

@@ -124,7 +124,7 @@ def test_fp32_x_keeps_all_its_bits():
     g = torch.Generator().manual_seed(4)
     bits = torch.randint(0x00800000, 0x7f800000, (50, k), generator=g, dtype=torch.int32)
     x = bits.view(torch.float32) * torch.sign(torch.randn(50, k, generator=g))
-    x = torch.where(x.abs() < 2.0 ** -110, torch.ones_like(x), x)
+    x = torch.where(x.abs() < 2.0 ** -96, torch.ones_like(x), x)
     x = torch.where(x.abs() > 2.0 ** 125, torch.ones_like(x), x)
     out = torch.empty(50, 16, device="cuda")
     tw.tw_gemm_w4(x.cuda(), w4, out)

@@ -70,7 +70,7 @@ def unpack(w4):
         sign = half >> np.array([15, 12, 14, 13], dtype=np.uint64)[v] & np.uint64(1)
         code = half >> np.array([6, 3, 9, 0], dtype=np.uint64)[v] & np.uint64(7)
         values = np.where(sign == 1, -1.0, 1.0) * LEVELS["e2m1"][code.astype(int)]
-    sat = 1024 + c // group * 32 + (r % 8 * 2 + r // 8) * 2
+    sat = 1024 + r % 8 * (512 // group) + c // group * 4 + r // 8 * 2
     bits = raw[st, ti, sat].astype(np.uint32) | raw[st, ti, sat + 1].astype(np.uint32) << 8
     scale = (bits << 16).astype(np.uint32).view(np.float32).astype(np.float64)
     # One scale per group.
@@ -91,8 +91,8 @@ def product_bound(x, w, out, group, dtype, fp32_x):
     are exact; its sum is a chain of group / 16 matrix steps, each off by a rounding
     or truncation of the sum so far and by the alignment of its 16 terms (8 more of
     them in all); groups, warps and the three terms of fp32 x are joined by fp32
-    additions; a scale multiplies; the result is rounded to dtype."""
+    additions (sixteen warps, eight CTAs); a scale multiplies; the result is rounded to dtype."""
     size = np.abs(x) @ np.abs(w).T * (1.01 if fp32_x else 1.0)
     tiles = -(-w.shape[1] // 128)
-    adds = tiles * (128 // group) + 8 * (3 if fp32_x else 1) + 2
+    adds = tiles * (128 // group) + 24 * (3 if fp32_x else 1) + 2
     return half_step(dtype) * np.abs(out) + ((group / 16 + 8) * 2 + adds) * U * size
