@@ -76,7 +76,7 @@ struct DeviceState {
     // 4][partials held 2, 4, 8, 16][8-bit outputs].
     int max_clusters[2][4][2][3][4][2] = {};
     int gemm_clusters[2][2][4] = {};  // see DeviceInfo
-    int w4_clusters[4] = {};          // see DeviceInfo
+    int w4_clusters[2][4] = {};       // see DeviceInfo
     unsigned int* status = nullptr;
     cudaEvent_t fork = nullptr;
     cudaEvent_t join = nullptr;

@@ -92,7 +92,8 @@ struct DeviceInfo {
     int quantize_error, gemv_error, gemm_error;
     int w4_rows_error, w4_gemm_error;
     int smem_optin;
-    int w4_clusters[4];  // of 1, 2, 4, 8 CTAs of the 4-bit product that run at once
+    // Clusters of 1, 2, 4, 8 CTAs of the 4-bit product that run at once, [CTAs per SM - 1].
+    int w4_clusters[2][4];
     // Clusters of 1, 2, 4, 8 CTAs of the product kernels that run at once:
     // [CTAs per unit - 1][int8][log2 of the cluster].
     int gemm_clusters[2][2][4];
@@ -151,7 +152,7 @@ struct W4GemmArgs {
     int group, xtype, dtype, wtype;
 };
 int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* stream);
-int w4_gemm_prepare(int smem_optin, int* clusters);
+int w4_gemm_prepare(int smem_optin, int (*clusters)[4]);
 
 // The step with a norm before the residual add (tw_postnorm.cu): what it has
 // beside the plain step's Params.

@@ -8,15 +8,18 @@
 // terms of eight bits each, which count as three tokens.
 //
 // A tile of W lies in HBM as the lanes read it (tw.h): lane (g, q) takes 16 bytes
-// of row g and 16 of row g + 8 straight into registers, kDepth tiles ahead; word j
-// holds k = 32 j + 8 q .. + 7, so that a word's two MMAs stay within 32 k and a
-// group of 32 can be scaled on its own.
+// of row g and 16 of row g + 8; word j holds k = 32 j + 8 q .. + 7, so that a word's
+// two MMAs stay within 32 k and a group of 32 can be scaled on its own.  A stripe of
+// 16 channels is contiguous, so a tile is one bulk copy into the warp's own ring in
+// shared memory, a few tiles ahead, with no barrier but the copy's.
 //
-// One CTA of 16 warps per SM.  It holds x of its K in shared memory and takes an even
-// share of the 16-channel stripes, `at_once` of them (times R) at a time: as many
-// warps share a stripe, each a contiguous piece of its K, and their sums are joined
-// through shared memory in warp order.  Where x does not fit, a cluster of CTAs
-// splits K, and joins through distributed shared memory in rank order.
+// Two CTAs of eight warps share an SM, so that one streams while the other starts,
+// joins or stores.  A CTA holds x of its K in shared memory and takes an even share
+// of the stripes, `at_once` of them at a time: as many warps share a stripe, each a
+// contiguous piece of its K, and their sums are joined through shared memory in warp
+// order.  A cluster of CTAs may split K as well (where x would not fit, or its copies
+// into every SM would outweigh W), and joins through distributed shared memory in
+// rank order.
 #include <cuda_fp16.h>
 
 #include "tw_tcgen05.cuh"
@@ -24,8 +27,11 @@
 namespace tw {
 namespace {
 
-constexpr int kWarps = 16;
+constexpr int kChunk = 2;                    // tiles of a bulk copy
+constexpr int kMinSlots = 2, kMaxSlots = 4;  // of a warp's ring
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxSplit = 8;
 constexpr int kXPad = 32;  // bf16: rows of x 64 bytes off each other in the banks
 constexpr int kXAhead = 4;
 constexpr int kColumnsMax = 32;  // tokens at a time (fp32 x: three for one)
@@ -42,13 +48,24 @@ __device__ __forceinline__ void sts128(uint32_t addr, const uint4& v) {
                  "r"(v.z), "r"(v.w)
                  : "memory");
 }
+// `bytes` of global memory to shared memory, counted on `bar` (multiples of 16).
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+            "r"(dst),
+        "l"(src), "r"(bytes), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // A word's eight values as four pairs of bf16, (k, k + 1) for k = 0, 2, 4, 6: the
-// values themselves (e2m1) or times 2^-7 (int4).  bf16 numbers below 2^-125 are their
-// last eight bits times 2^-133, so that two nibbles in eight need no shift.
+// values themselves (e2m1) or times 2^-7 (int4; the factor comes back in at the
+// end, so results below 2^-119 in magnitude may lose bits).  bf16 numbers below
+// 2^-125 are their last eight bits times 2^-133, so that two nibbles in eight need no
+// shift.
 constexpr float kInt4Factor = 128.f;
 template <bool INT4>
 __device__ __forceinline__ void widen(uint32_t w, uint32_t (&h)[4]) {
@@ -80,6 +97,14 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
         "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
@@ -153,290 +178,326 @@ __device__ __forceinline__ void x_terms(const XEight& x, int xtype, uint4 (&term
     }
 }
 
-struct W4Plan {
-    W4GemmArgs a;
-    int tokens;   // at a time
-    int at_once;  // stripe groups (of R stripes) of a CTA at a time, a power of two
-    int split;    // CTAs of a cluster, which split K
-};
-
-// A tile's words for one lane, and its scales (rows g and g + 8 of each group).
-template <int R, int G>
-struct Tile {
-    uint4 w[R][2];
-    uint32_t s[R][128 / G];
-};
-template <int G>
-__device__ __forceinline__ void load_scales(uint32_t (&s)[128 / G], const char* p) {
-    if constexpr (G == 128)
-        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(s[0]) : "l"(p));
-    else if constexpr (G == 64)
-        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                     : "=r"(s[0]), "=r"(s[1])
-                     : "l"(p));
-    else
-        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3])
-                     : "l"(p));
+// Floats between the columns of a warp's sums.
+constexpr int kRowStride = kW4Channels + 1;
+// Tiles that a warp warms L2 with before the launch before this one has ended.
+constexpr int kWarm = 16;
+// Tiles of x that a CTA holds at a time.
+__host__ __device__ constexpr int x_tiles(int tiles, int split, int slices) {
+    return ((tiles + split - 1) / split + slices - 1) / slices;
 }
 
-// A warp's way through its CTA's stripe groups: rounds of at_once groups (fewer in
-// the last), in each a contiguous piece of a group's tiles.
+struct W4Plan {
+    W4GemmArgs a;
+    int tokens;       // at a time
+    int log_at_once;  // stripes of a CTA at a time
+    int log_split;    // CTAs of a cluster, which split K
+    int slots;        // of a warp's ring
+    int slices;       // of a CTA's K, whose x is in shared memory one after the other
+    unsigned int* status;
+};
+
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int j) {
+    return j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
+}
+// The scales of rows g and g + 8 for a tile's groups.
+template <int G>
+__device__ __forceinline__ void lds_scales(uint32_t (&s)[128 / G], uint32_t addr) {
+    if constexpr (G == 128)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(s[0]) : "r"(addr));
+    else if constexpr (G == 64)
+        asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(s[0]), "=r"(s[1]) : "r"(addr));
+    else
+        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3])
+                     : "r"(addr));
+}
+
+// A warp's way through its CTA's stripes: rounds of up to 2^log_at_once stripes (fewer
+// in the last), each round in slices of K, in each a contiguous piece of a stripe's
+// tiles.
 struct Way {
-    int at, end;      // the round's first group and the CTA's last
-    int groups;       // of the round
-    int group, tile;  // this warp's group and first tile
-    int tiles;        // this warp's tiles
-    __device__ __forceinline__ void round(int at_once, int warp, int lo, int hi) {
-        const int rest = end - at;
-        groups = at_once;
-        while (groups / 2 >= rest && groups > 1) groups /= 2;
-        const int shares = kWarps / groups;  // warps of a group
-        const int share = warp % shares;
-        group = at + warp / shares;
-        tile = lo + (hi - lo) * share / shares;
-        tiles = group < end ? lo + (hi - lo) * (share + 1) / shares - tile : 0;
+    int at, end;    // the round's first stripe and the CTA's last
+    int log_n;      // stripes of the round
+    int stripe;     // this warp's
+    __device__ __forceinline__ void round(int log_at_once, int warp) {
+        log_n = log_at_once;
+        while (log_n > 0 && (1 << (log_n - 1)) >= end - at) --log_n;
+        stripe = at + (warp << log_n) / kWarps;
+    }
+    // This warp's first tile and tiles of [lo, hi).
+    __device__ __forceinline__ void piece(int warp, int lo, int hi, int* first, int* n) const {
+        const int shares = kWarps >> log_n, share = warp & (shares - 1);
+        *first = lo + (hi - lo) * share / shares;
+        *n = stripe < end ? lo + (hi - lo) * (share + 1) / shares - *first : 0;
     }
 };
 
-// INT4: the weights' type; NT: blocks of eight tokens (fp32 x: three per token);
-// R: stripes per warp; G: the group; kDepth: tiles in flight per warp.
-template <bool INT4, int NT, int R, int G, int kDepth>
-__global__ void __launch_bounds__(kThreads, 1)
+// INT4: the weights' type; NT: blocks of eight columns of x (fp32: three per token);
+// G: the group.
+template <bool INT4, int NT, int G>
+__global__ void __launch_bounds__(kThreads, 2)
     w4_gemm_kernel(const __grid_constant__ W4Plan plan) {
     constexpr int kTile = w4_tile_bytes(G);
-    constexpr int kColumns = NT * 8, kRowStride = 16 * R + 1;
+    constexpr int kSlot = kChunk * kTile;
+    constexpr int kColumns = NT * 8;
     const W4GemmArgs& a = plan.a;
     extern __shared__ __align__(128) unsigned char smem[];
     float* part = reinterpret_cast<float*>(smem);  // [warp][column][kRowStride]
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
+    const int lane = threadIdx.x % 32;
     const int row = lane / 4, quad = lane % 4;
     const int parts = a.xtype == TW_X_F32 ? 3 : 1;
     const int K = static_cast<int>(a.K);
     const int tiles_k = (K + kW4Inner - 1) / kW4Inner;
-    const int stripes = static_cast<int>((a.N + 15) / 16);
-    const int groups = (stripes + R - 1) / R;
-    // This CTA's share of K (of the cluster) and of the groups.
-    const int split = plan.split;
+    const int stripes = static_cast<int>((a.N + kW4Channels - 1) / kW4Channels);
+    // This CTA's share of K (of the cluster), cut into slices, and of the stripes.
+    const int split = 1 << plan.log_split, slices = plan.slices;
     const int rank = split > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
     const int lo = tiles_k * rank / split, hi = tiles_k * (rank + 1) / split;
+    auto slice_at = [&](int s) { return lo + (hi - lo) * s / slices; };
     const int64_t sets = gridDim.x / split, set = blockIdx.x / split;
-    const int first = static_cast<int>(groups * set / sets);
-    const int end = static_cast<int>(groups * (set + 1) / sets);
-    const int x_tiles = (tiles_k + split - 1) / split;  // at most, of any rank
-    const int x_stride = (x_tiles * kW4Inner + kXPad) * 2;
-    // Sums that the cluster's CTAs write here: [buffer][rank][output / split].
+    const int first = static_cast<int>(stripes * set / sets);
+    const int end = static_cast<int>(stripes * (set + 1) / sets);
+    const int x_stride = (x_tiles(tiles_k, split, slices) * kW4Inner + kXPad) * 2;
+    // Sums that the cluster's CTAs write here: [buffer][rank][column][channel of this
+    // rank's]; the rings; their barriers; x.
     float* joined = part + kWarps * kColumns * kRowStride;
-    const int outputs = plan.at_once * 16 * R * plan.tokens;
-    const int per_rank = (outputs + split - 1) / split;
-    const uint32_t xs =
-        smem_addr(joined) + (split > 1 ? (2 * split * per_rank * 4 + 15) / 16 * 16 : 0);
+    const int own = (kW4Channels << plan.log_at_once) / split;
+    const uint32_t rings = smem_addr(joined) + (split > 1 ? 2 * split * kColumns * own * 4 : 0);
+    const uint32_t ring = rings + warp * plan.slots * kSlot;
+    const uint32_t bars = rings + kWarps * plan.slots * kSlot;
+    const uint32_t bar = bars + warp * kMaxSlots * 8;
+    const uint32_t xs = bars + kWarps * kMaxSlots * 8;
 
+    if (lane == 0) {
+        for (int i = 0; i < plan.slots; ++i) mbar_init(bar + i * 8, 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
     const char* packed = static_cast<const char*>(a.packed);
-    Way ld{first, end, 0, 0, 0, 0};
-    ld.round(plan.at_once, warp, lo, hi);
-    // The first round's W on its way into L2 while the launch before this one ends (a
-    // hint that reads nothing: what that launch writes is seen all the same).
-    if (lane == 0 && ld.tiles > 0)
-        for (int r = 0; r < R; ++r)
-            if (ld.group * R + r < stripes)
-                bulk_prefetch_l2(packed + (static_cast<int64_t>(ld.group * R + r) * tiles_k +
-                                           ld.tile) * kTile,
-                                 static_cast<uint32_t>((ld.tiles < 16 ? ld.tiles : 16) * kTile));
+    Way ld{first, end, 0, 0};
+    int ld_slice = 0, ld_first = 0, left = 0;
+    const char* from = packed;
+    auto begin = [&]() {
+        ld.piece(warp, slice_at(ld_slice), slice_at(ld_slice + 1), &ld_first, &left);
+        from = packed + (static_cast<int64_t>(ld.stripe) * tiles_k + ld_first) * kTile;
+    };
+    ld.round(plan.log_at_once, warp);
+    begin();
+    // The first W on its way into L2 while the launch before this one ends (a hint that
+    // reads nothing: what that launch writes is seen all the same).
+    if (lane == 0 && left > 0)
+        bulk_prefetch_l2(from, static_cast<uint32_t>((left < kWarm ? left : kWarm) * kTile));
     if (split > 1) cluster_barrier();  // every CTA runs before any writes into it
     grid_dependency_wait();
     grid_launch_dependents();
 
+    const uint32_t one = elect_one();
+    uint32_t slot_ld = 0, slot = 0, phase = 0;
     int buf = 0;
     for (int64_t m0 = 0; m0 < a.M; m0 += plan.tokens) {
         const int tokens = static_cast<int>(a.M - m0 < plan.tokens ? a.M - m0 : plan.tokens);
         const int cols = tokens * parts;
-        // The next tile to load: its place in the round, whose tiles count up to a
-        // multiple of kDepth so that registers are named at compile time.
-        int ld_i = 0;
-        ld = Way{first, end, 0, 0, 0, 0};
-        ld.round(plan.at_once, warp, lo, hi);
-        Tile<R, G> ahead[kDepth];
-        auto load = [&](Tile<R, G>& t) {
-            // (A warp may be without tiles for whole rounds.)
-            while (ld_i == (ld.tiles + kDepth - 1) / kDepth * kDepth && ld.at < end) {
-                ld_i = 0;
-                ld.at += ld.groups;
-                if (ld.at < end)
-                    ld.round(plan.at_once, warp, lo, hi);
-                else
-                    ld.tiles = 0;
+        auto load = [&]() {
+            while (left == 0) {  // a warp may be without tiles for whole rounds
+                if (ld.at >= end) return;
+                if (++ld_slice >= slices) {
+                    ld_slice = 0;
+                    ld.at += 1 << ld.log_n;
+                    if (ld.at >= end) return;
+                    ld.round(plan.log_at_once, warp);
+                }
+                begin();
             }
-            if (ld_i < ld.tiles) {
+            const int n = left < kChunk ? left : kChunk;
+            if (one) {
+                mbar_arrive_expect_tx(bar + slot_ld * 8, n * kTile);
+                bulk_copy(ring + slot_ld * kSlot, from, n * kTile, bar + slot_ld * 8);
+            }
+            from += kSlot;
+            left -= n;
+            if (++slot_ld == static_cast<uint32_t>(plan.slots)) slot_ld = 0;
+        };
+        ld = Way{first, end, 0, 0};
+        ld.round(plan.log_at_once, warp);
+        ld_slice = 0;
+        begin();
+        for (int d = 0; d < plan.slots; ++d) load();
+
+        // x of a slice of this CTA's K, zero up to the end of its last tile; kXAhead
+        // loads of a thread in flight.
+        auto stage_x = [&](int slice) {
+            const int x_size = a.xtype == TW_X_BF16 ? 2 : a.xtype == TW_X_F32 ? 4 : 1;
+            const int k0 = slice_at(slice) * kW4Inner;
+            const uint32_t row_pieces =
+                static_cast<uint32_t>(slice_at(slice + 1) - slice_at(slice)) * (kW4Inner / 8);
+            const uint32_t pieces = row_pieces * tokens;
+            for (uint32_t e0 = threadIdx.x; e0 < pieces; e0 += kThreads * kXAhead) {
+                XEight x[kXAhead] = {};
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    // A stripe beyond the last: the last once more, not stored.
-                    const int stripe = R == 1 || ld.group * R + r < stripes ? ld.group * R + r
-                                                                           : stripes - 1;
-                    const char* from =
-                        packed + (static_cast<int64_t>(stripe) * tiles_k + ld.tile + ld_i) * kTile;
-                    t.w[r][0] = ld_global_nc(from + lane * 16);
-                    t.w[r][1] = ld_global_nc(from + 512 + lane * 16);
-                    load_scales<G>(t.s[r], from + 1024 + row * (512 / G));
+                for (int i = 0; i < kXAhead; ++i) {
+                    const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
+                    const int64_t k = k0 + static_cast<int64_t>(e % row_pieces) * 8;
+                    if (e < pieces && k < K)
+                        x[i].load(static_cast<const char*>(a.x) + ((m0 + t) * a.K + k) * x_size,
+                                  a.xtype);
+                }
+#pragma unroll
+                for (int i = 0; i < kXAhead; ++i) {
+                    const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
+                    if (e >= pieces) break;
+                    uint4 terms[3];
+                    x_terms(x[i], a.xtype, terms);
+                    for (int p = 0; p < parts; ++p)
+                        sts128(xs + (t * parts + p) * x_stride + e % row_pieces * 16, terms[p]);
                 }
             }
-            ++ld_i;
+            __syncthreads();
         };
+        if (slices == 1) stage_x(0);
+        // Where the lane's rows of x begin.  Columns beyond the last repeat the first:
+        // one read for all of them, and nothing of theirs is stored.
+        uint32_t x_row[NT];
 #pragma unroll
-        for (int d = 0; d < kDepth; ++d) load(ahead[d]);
+        for (int b = 0; b < NT; ++b)
+            x_row[b] = xs + (b * 8 + row < cols ? b * 8 + row : 0) * x_stride + quad * 16;
 
-        // x of this CTA's K, zero up to the end of its last tile; kXAhead loads of a
-        // thread in flight.
-        const int x_size = a.xtype == TW_X_BF16 ? 2 : a.xtype == TW_X_F32 ? 4 : 1;
-        const uint32_t row_pieces = static_cast<uint32_t>(hi - lo) * (kW4Inner / 8);
-        const uint32_t pieces = row_pieces * tokens;
-        for (uint32_t e0 = threadIdx.x; e0 < pieces; e0 += kThreads * kXAhead) {
-            XEight x[kXAhead] = {};
+        Way at{first, end, 0, 0};
+        for (; at.at < end; at.at += 1 << at.log_n) {
+            at.round(plan.log_at_once, warp);
+            float total[NT][4] = {};
+            for (int slice = 0; slice < slices; ++slice) {
+                if (slices > 1) {
+                    __syncthreads();  // the x before has been read
+                    stage_x(slice);
+                }
+                int tile = 0, tiles = 0;
+                at.piece(warp, slice_at(slice), slice_at(slice + 1), &tile, &tiles);
+                uint32_t x_at = (tile - slice_at(slice)) * (kW4Inner * 2);
+                for (int i = 0; i < tiles; i += kChunk) {
+                    // (A copy that does not arrive: the device status says so.)
+                    if (!mbar_wait_slice(bar + slot * 8, phase, nullptr))
+                        atomicOr(plan.status, 1u);
+                    const uint32_t t = ring + slot * kSlot + lane * 16;
+                    const uint32_t ts = ring + slot * kSlot + 1024 + row * (512 / G);
 #pragma unroll
-            for (int i = 0; i < kXAhead; ++i) {
-                const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
-                const int64_t k = lo * kW4Inner + static_cast<int64_t>(e % row_pieces) * 8;
-                if (e < pieces && k < K)
-                    x[i].load(static_cast<const char*>(a.x) + ((m0 + t) * a.K + k) * x_size,
-                              a.xtype);
-            }
-#pragma unroll
-            for (int i = 0; i < kXAhead; ++i) {
-                const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
-                if (e >= pieces) break;
-                uint4 terms[3];
-                x_terms(x[i], a.xtype, terms);
-                for (int p = 0; p < parts; ++p)
-                    sts128(xs + (p * tokens + t) * x_stride + e % row_pieces * 16, terms[p]);
-            }
-        }
-        __syncthreads();
-
-        Way at{first, end, 0, 0, 0, 0};
-        for (; at.at < end; at.at += at.groups) {
-            at.round(plan.at_once, warp, lo, hi);
-            float total[R][NT][4] = {};
-            for (int i0 = 0; i0 < at.tiles; i0 += kDepth) {
-#pragma unroll
-                for (int d = 0; d < kDepth; ++d) {
-                    if (i0 + d < at.tiles) {
-                        const Tile<R, G>& t = ahead[d];
-                        const uint32_t x_at =
-                            xs + (at.tile + i0 + d - lo) * (kW4Inner * 2) + quad * 16;
-                        float sum[R][NT][4] = {};
+                    for (int c = 0; c < kChunk; ++c, x_at += kW4Inner * 2) {
+                        if (c > 0 && i + c >= tiles) break;
+                        const uint4 w[2] = {lds128(t + c * kTile), lds128(t + c * kTile + 512)};
+                        uint32_t s[128 / G];
+                        lds_scales<G>(s, ts + c * kTile);
+                        // Two chains of MMAs a group, so that one hides the other's latency.
+                        float sum[2][NT][4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             uint4 xv[NT];
 #pragma unroll
-                            for (int b = 0; b < NT; ++b)
-                                xv[b] = b * 8 + row < cols
-                                            ? lds128(x_at + (b * 8 + row) * x_stride + j * 64)
-                                            : make_uint4(0, 0, 0, 0);
+                            for (int b = 0; b < NT; ++b) xv[b] = lds128(x_row[b] + x_at + j * 64);
+                            uint32_t u[4], v[4];
+                            widen<INT4>(word_of(w[0], j), u);
+                            widen<INT4>(word_of(w[1], j), v);
 #pragma unroll
-                            for (int r = 0; r < R; ++r) {
-                                uint32_t u[4], v[4];
-                                widen<INT4>(j == 0   ? t.w[r][0].x
-                                            : j == 1 ? t.w[r][0].y
-                                            : j == 2 ? t.w[r][0].z
-                                                     : t.w[r][0].w, u);
-                                widen<INT4>(j == 0   ? t.w[r][1].x
-                                            : j == 1 ? t.w[r][1].y
-                                            : j == 2 ? t.w[r][1].z
-                                                     : t.w[r][1].w, v);
-#pragma unroll
-                                for (int b = 0; b < NT; ++b) {
-                                    mma(sum[r][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
-                                    mma(sum[r][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
+                            for (int b = 0; b < NT; ++b) {
+                                if (j * 32 % G == 0) {
+                                    mma_first(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
+                                    mma_first(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
+                                } else {
+                                    mma(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
+                                    mma(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
                                 }
-                                if ((j + 1) * 32 % G == 0) {
-                                    // The group is whole.
-                                    const uint32_t s = t.s[r][j * 32 / G];
-                                    const float s0 = __uint_as_float(s << 16);
-                                    const float s1 = __uint_as_float(s & 0xffff0000u);
+                            }
+                            if ((j + 1) * 32 % G == 0) {
+                                // The group is whole.
+                                const float s0 = __uint_as_float(s[j * 32 / G] << 16);
+                                const float s1 = __uint_as_float(s[j * 32 / G] & 0xffff0000u);
 #pragma unroll
-                                    for (int b = 0; b < NT; ++b)
+                                for (int b = 0; b < NT; ++b)
 #pragma unroll
-                                        for (int e = 0; e < 4; ++e) {
-                                            if (INT4) sum[r][b][e] *= kInt4Factor;
-                                            total[r][b][e] = fmaf(sum[r][b][e], e < 2 ? s0 : s1,
-                                                                  total[r][b][e]);
-                                            sum[r][b][e] = 0.f;
-                                        }
-                                }
+                                    for (int e = 0; e < 4; ++e)
+                                        total[b][e] = fmaf(sum[0][b][e] + sum[1][b][e],
+                                                           e < 2 ? s0 : s1, total[b][e]);
                             }
                         }
                     }
-                    load(ahead[d]);
+                    if (++slot == static_cast<uint32_t>(plan.slots)) {
+                        slot = 0;
+                        phase ^= 1u;
+                    }
+                    __syncwarp();  // every lane has read the slot
+                    load();
                 }
             }
             // The warps' sums, joined in warp order.
 #pragma unroll
-            for (int r = 0; r < R; ++r)
+            for (int b = 0; b < NT; ++b)
 #pragma unroll
-                for (int b = 0; b < NT; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        part[(warp * kColumns + b * 8 + quad * 2 + e % 2) * kRowStride + r * 16 +
-                             row + e / 2 * 8] = total[r][b][e];
+                for (int e = 0; e < 4; ++e)
+                    part[(warp * kColumns + b * 8 + quad * 2 + e % 2) * kRowStride + row +
+                         e / 2 * 8] = total[b][e];
             __syncthreads();
-            const int shares = kWarps / at.groups;
-            const int channels = at.groups * 16 * R;
-            const int64_t n0 = static_cast<int64_t>(at.at) * 16 * R;
-            auto store = [&](int t, int c, float sum) {
-                if (n0 + c >= a.N || at.at + c / (16 * R) >= end) return;
+            const int shares = kWarps >> at.log_n, log_channels = 4 + at.log_n;
+            const int64_t n0 = static_cast<int64_t>(at.at) * kW4Channels;
+            // Of column c, channel i of the round.
+            auto sum_of = [&](int c, int i) {
+                const float* from = part + ((i / 16 * shares) * kColumns + c) * kRowStride + i % 16;
+                float sum = 0.f;
+                for (int w = 0; w < shares; ++w) sum += from[w * kColumns * kRowStride];
+                return sum;
+            };
+            auto store = [&](int t, int i, float sum) {
+                if (n0 + i >= a.N || at.at + i / kW4Channels >= end) return;
+                if (INT4) sum *= kInt4Factor;
                 if (a.x_scale) sum *= a.x_scale[m0 + t];
-                const int64_t to = (m0 + t) * a.N + n0 + c;
+                const int64_t to = (m0 + t) * a.N + n0 + i;
                 if (a.dtype == TW_BF16)
                     static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(sum);
                 else
                     static_cast<float*>(a.out)[to] = sum;
             };
-            for (int e = threadIdx.x; e < tokens * channels; e += kThreads) {
-                const int t = e / channels, c = e % channels;
-                const float* from = part +
-                                    (c / (16 * R) * shares * kColumns + t) * kRowStride +
-                                    c % (16 * R);
-                float sum = 0.f;
-                // fp32 x: the smaller terms first.
-                for (int p = parts - 1; p >= 0; --p)
-                    for (int w = 0; w < shares; ++w)
-                        sum += from[(w * kColumns + p * tokens) * kRowStride];
-                if (split == 1)
-                    store(t, c, sum);
-                else
-                    st_cluster_f32(map_to_rank(smem_addr(joined + (buf * split + rank) * per_rank +
-                                                         e / split),
-                                               static_cast<uint32_t>(e % split)),
-                                   sum);
-            }
-            if (split > 1) {
-                // Output e is rank e % split's.  A buffer is written again two rounds
-                // later, behind the barrier that its readers reach when done.
-                cluster_barrier();
-                for (int e = threadIdx.x * split + rank; e < tokens * channels;
-                     e += kThreads * split) {
+            if (split == 1) {
+                for (int e = threadIdx.x; e < tokens << log_channels; e += kThreads) {
+                    const int t = e >> log_channels, i = e & ((1 << log_channels) - 1);
                     float sum = 0.f;
-                    for (int r = 0; r < split; ++r)
-                        sum += joined[(buf * split + r) * per_rank + e / split];
-                    store(e / channels, e % channels, sum);
+                    // fp32 x: the smaller terms first.
+                    for (int p = parts - 1; p >= 0; --p) sum += sum_of(t * parts + p, i);
+                    store(t, i, sum);
+                }
+                __syncthreads();  // the sums are read
+            } else {
+                // Rank q finishes channels [q, q + 1) * channels / split of the round.  A
+                // buffer is written again two rounds later, behind the barrier that its
+                // readers reach when done.
+                const int log_own = log_channels - plan.log_split;
+                float* sums = joined + buf * split * kColumns * own;
+                for (int e = threadIdx.x; e < cols << log_channels; e += kThreads) {
+                    const int c = e >> log_channels, i = e & ((1 << log_channels) - 1);
+                    float* to = sums + (rank * kColumns + c) * own + (i & ((1 << log_own) - 1));
+                    st_cluster_f32(map_to_rank(smem_addr(to), static_cast<uint32_t>(i >> log_own)),
+                                   sum_of(c, i));
+                }
+                cluster_barrier();
+                for (int e = threadIdx.x; e < tokens << log_own; e += kThreads) {
+                    const int t = e >> log_own, i = e & ((1 << log_own) - 1);
+                    float sum = 0.f;
+                    for (int p = parts - 1; p >= 0; --p)
+                        for (int r = 0; r < split; ++r)
+                            sum += sums[(r * kColumns + t * parts + p) * own + i];
+                    store(t, (rank << log_own) + i, sum);
                 }
                 buf ^= 1;
             }
-            __syncthreads();  // the sums are read
         }
+        __syncthreads();  // x is read
     }
 }
 
-// R and depth by the tokens' blocks: x is read from shared memory once per R stripes.
 template <bool INT4, int G>
 void* entry(int nt) {
-    switch (nt) {
-        case 1: return reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 1, 1, G, 4>);
-        case 2: return reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 2, 2, G, 2>);
-        default: return reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 4, 1, G, 2>);
-    }
+    return nt == 1   ? reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 1, G>)
+           : nt == 2 ? reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 2, G>)
+                     : reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 4, G>);
 }
-constexpr int stripes_per_warp(int nt) { return nt == 2 ? 2 : 1; }
 void* kernel_for(int wtype, int nt, int group) {
     if (wtype == TW_INT4)
         return group == 32 ? entry<true, 32>(nt) : group == 64 ? entry<true, 64>(nt)
@@ -445,18 +506,19 @@ void* kernel_for(int wtype, int nt, int group) {
                                                             : entry<false, 128>(nt);
 }
 
-// Shared memory for `columns` columns of x in `nt` blocks, K over `split` CTAs and
-// at_once groups at a time of `tokens` tokens.
-int64_t smem_bytes(int nt, int columns, int tokens, int64_t K, int split, int at_once) {
-    const int r = stripes_per_warp(nt);
-    const int64_t part = static_cast<int64_t>(kWarps) * nt * 8 * (16 * r + 1) * 4;
-    const int64_t per_rank = (static_cast<int64_t>(at_once) * 16 * r * tokens + split - 1) / split;
-    const int64_t joined = split > 1 ? (2 * split * per_rank * 4 + 15) / 16 * 16 : 0;
-    const int64_t tiles_k = (K + kW4Inner - 1) / kW4Inner;
-    return part + joined + columns * ((tiles_k + split - 1) / split * kW4Inner + kXPad) * 2;
+// Shared memory of a CTA for `columns` columns of x in `nt` blocks.
+int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
+    const int64_t part = static_cast<int64_t>(kWarps) * nt * 8 * kRowStride * 4;
+    const int64_t joined =
+        p.log_split > 0 ? int64_t{2} * nt * 8 * (kW4Channels << p.log_at_once) * 4 : 0;
+    const int64_t rings = kWarps * (p.slots * kChunk * w4_tile_bytes(group) + kMaxSlots * 8);
+    const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
+    return part + joined + rings +
+           static_cast<int64_t>(columns) *
+               (x_tiles(tiles, 1 << p.log_split, p.slices) * kW4Inner + kXPad) * 2;
 }
-// Groups at a time of a CTA that shares them with a cluster (its sums take room).
-constexpr int kSplitAtOnce = 4;
+// What a CTA may use where two share an SM.
+int64_t half_smem(int smem_optin) { return (smem_optin - 1024) / 2; }
 
 cudaLaunchConfig_t config(int grid, int split, size_t smem, bool pdl, void* stream,
                           cudaLaunchAttribute (&attr)[2]) {
@@ -478,7 +540,7 @@ cudaLaunchConfig_t config(int grid, int split, size_t smem, bool pdl, void* stre
 
 }  // namespace
 
-int w4_gemm_prepare(int smem_optin, int* clusters) {
+int w4_gemm_prepare(int smem_optin, int (*clusters)[4]) {
     for (int wtype : {TW_INT4, TW_E2M1})
         for (int nt = 1; nt <= 4; nt *= 2)
             for (int group = 32; group <= 128; group *= 2) {
@@ -487,15 +549,17 @@ int w4_gemm_prepare(int smem_optin, int* clusters) {
                                          cudaFuncAttributeMaxDynamicSharedMemorySize, smem_optin);
                 if (e != cudaSuccess) return static_cast<int>(e);
             }
-    // Clusters of 1, 2, 4, 8 CTAs that run at once (a CTA takes an SM's registers, so
-    // the instantiations do not differ).
-    for (int i = 0; i < 4; ++i) {
-        cudaLaunchAttribute attr[2];
-        const cudaLaunchConfig_t cfg = config(1 << i, 1 << i, smem_optin, false, nullptr, attr);
-        cudaError_t e =
-            cudaOccupancyMaxActiveClusters(clusters + i, kernel_for(TW_INT4, 1, 128), &cfg);
-        if (e != cudaSuccess) return static_cast<int>(e);
-    }
+    // Clusters of 1, 2, 4, 8 CTAs that run at once, with a CTA and with two on an SM.
+    for (int ctas = 1; ctas <= 2; ++ctas)
+        for (int i = 0; i < 4; ++i) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg =
+                config(1 << i, 1 << i, static_cast<size_t>(ctas == 1 ? smem_optin : half_smem(smem_optin)),
+                       false, nullptr, attr);
+            cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[ctas - 1][i],
+                                                           kernel_for(TW_INT4, 1, 128), &cfg);
+            if (e != cudaSuccess) return static_cast<int>(e);
+        }
     return 0;
 }
 
@@ -503,46 +567,56 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
     const bool whole = max_sms >= d.sm_count;
     const int parts = a.xtype == TW_X_F32 ? 3 : 1;
-    // The most tokens at a time whose x fits, K over the fewest CTAs.
-    W4Plan plan{a, 0, 1, 1};
+    const int64_t stripes = (a.N + kW4Channels - 1) / kW4Channels;
+    const int64_t tiles = (a.K + kW4Inner - 1) / kW4Inner;
+    W4Plan plan{a, 0, 0, 0, 0, 1, d.status};
+    int64_t smem = 0, sets = 0;
     int nt = 0;
-    int64_t smem = 0;
-    for (int64_t tokens = a.M < kColumnsMax / parts ? a.M : kColumnsMax / parts;
-         tokens > 0 && nt == 0; --tokens) {
+    // The most tokens at a time whose x fits, K over the fewest CTAs, two of them on an
+    // SM if they fit so (under a budget each is alone there).  One token that does not
+    // fit the SMs of a budget: in slices, staged again for each round.
+    auto choose = [&](int64_t tokens, int slices) {
         const int columns = static_cast<int>(tokens) * parts;
         const int blocks = columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
-        for (int split = 1, i = 0; split <= 8 && split <= sms; split *= 2, ++i) {
-            if (d.w4_clusters[i] < 1) break;
-            const int64_t need = smem_bytes(blocks, columns, static_cast<int>(tokens), a.K, split,
-                                            kSplitAtOnce);
-            if (need > d.smem_optin) continue;
-            plan.tokens = static_cast<int>(tokens);
-            plan.split = split;
-            nt = blocks;
-            smem = need;
-            break;
-        }
-    }
-    if (nt == 0) return static_cast<int>(cudaErrorInvalidConfiguration);
-    int log2_split = 0;
-    while ((1 << log2_split) < plan.split) ++log2_split;
-    const int r = stripes_per_warp(nt);
-    const int64_t groups = (a.N + 16 * r - 1) / (16 * r);
-    int64_t sets = sms / plan.split;
-    if (plan.split > 1 && sets > d.w4_clusters[log2_split]) sets = d.w4_clusters[log2_split];
-    if (sets > groups) sets = groups;
-    // Groups at a time: what a CTA has, at most one per warp; a group's warps have
-    // two tiles each where there are that many.
-    const int64_t share = (groups + sets - 1) / sets;
-    const int64_t tiles = ((a.K + kW4Inner - 1) / kW4Inner + plan.split - 1) / plan.split;
-    const int most = plan.split > 1 ? kSplitAtOnce : kWarps;
-    while (plan.at_once < most && plan.at_once < share &&
-           (plan.at_once < 4 || 2 * kWarps / plan.at_once > tiles))
-        plan.at_once *= 2;
-    if (!whole && smem < kExclusiveSmemBytes) smem = kExclusiveSmemBytes;
+        for (int ctas = whole ? 2 : 1; ctas > 0; --ctas)
+            for (int i = 0; i < 4 && (1 << i) <= tiles; ++i) {
+                int64_t at_once = sms * ctas >> i;
+                const int64_t clusters = d.w4_clusters[ctas - 1][i];
+                if (i > 0 && at_once > clusters) at_once = clusters;
+                if (at_once < 1) break;
+                sets = at_once < stripes ? at_once : stripes;
+                // Stripes at a time: a warp for each if there are that many, but some
+                // warps for one while they have two tiles each.
+                const int64_t share = (stripes + sets - 1) / sets;
+                plan.log_split = i;
+                plan.log_at_once = 0;
+                while ((1 << plan.log_at_once) < kWarps && (1 << plan.log_at_once) < share &&
+                       (i > 0 || plan.log_at_once < 1 ||
+                        2 * kWarps >> plan.log_at_once > tiles >> i))
+                    ++plan.log_at_once;
+                plan.slices = slices;
+                const int64_t room = ctas == 1 ? d.smem_optin : half_smem(d.smem_optin);
+                for (plan.slots = kMaxSlots; plan.slots >= kMinSlots; --plan.slots) {
+                    smem = smem_bytes(blocks, columns, a.K, a.group, plan);
+                    if (smem > room) continue;
+                    if (ctas == 1 && smem < kExclusiveSmemBytes) smem = kExclusiveSmemBytes;
+                    plan.tokens = static_cast<int>(tokens);
+                    nt = blocks;
+                    return true;
+                }
+            }
+        return false;
+    };
+    bool found = false;
+    for (int64_t tokens = a.M < kColumnsMax / parts ? a.M : kColumnsMax / parts;
+         tokens > 0 && !found; --tokens)
+        found = choose(tokens, 1);
+    for (int slices = 2; !found && slices <= tiles; slices *= 2) found = choose(1, slices);
+    if (!found) return static_cast<int>(cudaErrorInvalidConfiguration);
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config(static_cast<int>(sets * plan.split), plan.split,
-                                          static_cast<size_t>(smem), whole, stream, attr);
+    const cudaLaunchConfig_t cfg = config(static_cast<int>(sets << plan.log_split),
+                                          1 << plan.log_split, static_cast<size_t>(smem), whole,
+                                          stream, attr);
     void* args[] = {&plan};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, kernel_for(a.wtype, nt, a.group), args));
 }

@@ -79,6 +79,12 @@ def test_budgets(t, n, k, max_sms):
     run(t, n, k, 64, "e2m1", "bf16", "f32", max_sms=max_sms)
 
 
+@pytest.mark.parametrize("xtype", ["bf16", "f32"])
+@pytest.mark.parametrize("max_sms,k", [(1, 16384), (2, 32768), (3, 65536), (1, 65536)])
+def test_long_rows_on_few_sms(max_sms, k, xtype):
+    run(2, 150, k, 32, "int4", xtype, "f32", max_sms=max_sms)
+
+
 def test_rows_outside_the_range_are_left_alone():
     w4, w64 = make(70, 256, 32, "int4")
     x, _, x64 = make_x(13, 256, "f32")
