@@ -27,11 +27,14 @@
 namespace tw {
 namespace {
 
-constexpr int kChunk = 2;                    // tiles of a bulk copy
-constexpr int kMinSlots = 2, kMaxSlots = 4;  // of a warp's ring
+// Tiles of a bulk copy, and copies that a warp's ring holds: few and long where one
+// block of columns leaves the room (8 x 8192 x 8192 15.1 -> 13.2 us, 1 10.8 -> 10.5;
+// with more columns short ones, so that three or four of them fit beside x).
+__host__ __device__ constexpr int chunk_of(int nt) { return nt == 1 ? 4 : 2; }
+__host__ __device__ constexpr int max_slots(int nt) { return nt == 1 ? 2 : 4; }
+constexpr int kMinSlots = 2, kMaxSlots = 4;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kMaxSplit = 8;
 constexpr int kXPad = 32;  // bf16: rows of x 64 bytes off each other in the banks
 constexpr int kXAhead = 4;
 constexpr int kColumnsMax = 32;  // tokens at a time (fp32 x: three for one)
@@ -239,7 +242,7 @@ template <bool INT4, int NT, int G>
 __global__ void __launch_bounds__(kThreads, 2)
     w4_gemm_kernel(const __grid_constant__ W4Plan plan) {
     constexpr int kTile = w4_tile_bytes(G);
-    constexpr int kSlot = kChunk * kTile;
+    constexpr int kChunk = chunk_of(NT), kSlot = kChunk * kTile;
     constexpr int kColumns = NT * 8;
     const W4GemmArgs& a = plan.a;
     extern __shared__ __align__(128) unsigned char smem[];
@@ -332,25 +335,32 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int k0 = slice_at(slice) * kW4Inner;
             const uint32_t row_pieces =
                 static_cast<uint32_t>(slice_at(slice + 1) - slice_at(slice)) * (kW4Inner / 8);
-            const uint32_t pieces = row_pieces * tokens;
-            for (uint32_t e0 = threadIdx.x; e0 < pieces; e0 += kThreads * kXAhead) {
+            // The thread's next piece: the at-th of token t.
+            uint32_t t = 0, at = threadIdx.x;
+            const auto count = static_cast<uint32_t>(tokens);
+            while (t < count) {
                 XEight x[kXAhead] = {};
+                uint32_t to[kXAhead];
+                bool in[kXAhead];
 #pragma unroll
-                for (int i = 0; i < kXAhead; ++i) {
-                    const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
-                    const int64_t k = k0 + static_cast<int64_t>(e % row_pieces) * 8;
-                    if (e < pieces && k < K)
+                for (int i = 0; i < kXAhead; ++i, at += kThreads) {
+                    while (at >= row_pieces && t < count) {
+                        at -= row_pieces;
+                        ++t;
+                    }
+                    in[i] = t < count;
+                    to[i] = xs + t * parts * x_stride + at * 16;
+                    const int64_t k = k0 + static_cast<int64_t>(at) * 8;
+                    if (in[i] && k < K)
                         x[i].load(static_cast<const char*>(a.x) + ((m0 + t) * a.K + k) * x_size,
                                   a.xtype);
                 }
 #pragma unroll
                 for (int i = 0; i < kXAhead; ++i) {
-                    const uint32_t e = e0 + i * kThreads, t = e / row_pieces;
-                    if (e >= pieces) break;
+                    if (!in[i]) break;
                     uint4 terms[3];
                     x_terms(x[i], a.xtype, terms);
-                    for (int p = 0; p < parts; ++p)
-                        sts128(xs + (t * parts + p) * x_stride + e % row_pieces * 16, terms[p]);
+                    for (int p = 0; p < parts; ++p) sts128(to[i] + p * x_stride, terms[p]);
                 }
             }
             __syncthreads();
@@ -511,7 +521,7 @@ int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
     const int64_t part = static_cast<int64_t>(kWarps) * nt * 8 * kRowStride * 4;
     const int64_t joined =
         p.log_split > 0 ? int64_t{2} * nt * 8 * (kW4Channels << p.log_at_once) * 4 : 0;
-    const int64_t rings = kWarps * (p.slots * kChunk * w4_tile_bytes(group) + kMaxSlots * 8);
+    const int64_t rings = kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8);
     const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
     return part + joined + rings +
            static_cast<int64_t>(columns) *
@@ -596,7 +606,7 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
                     ++plan.log_at_once;
                 plan.slices = slices;
                 const int64_t room = ctas == 1 ? d.smem_optin : half_smem(d.smem_optin);
-                for (plan.slots = kMaxSlots; plan.slots >= kMinSlots; --plan.slots) {
+                for (plan.slots = max_slots(blocks); plan.slots >= kMinSlots; --plan.slots) {
                     smem = smem_bytes(blocks, columns, a.K, a.group, plan);
                     if (smem > room) continue;
                     if (ctas == 1 && smem < kExclusiveSmemBytes) smem = kExclusiveSmemBytes;
