@@ -76,6 +76,7 @@ struct DeviceState {
     // 4][partials held 2, 4, 8, 16][8-bit outputs].
     int max_clusters[2][4][2][3][4][2] = {};
     int gemm_clusters[2][2][4] = {};  // see DeviceInfo
+    PostDevice postnorm = {};
     int w4_clusters[2][4] = {};       // see DeviceInfo
     unsigned int* status = nullptr;
     cudaEvent_t fork = nullptr;
@@ -139,7 +140,10 @@ int device_state(DeviceState** out) {
         d.quantize_error = optional(quantize_prepare(d.smem_optin));
         d.gemv_error = optional(gemv_prepare(d.smem_optin));
         d.gemm_error = optional(gemm_prepare(d.smem_optin, d.gemm_clusters));
-        d.postnorm_error = optional(postnorm_prepare(d.smem_optin));
+        d.postnorm.sm_count = d.sm_count;
+        d.postnorm.smem_optin = d.smem_optin;
+        d.postnorm_error = optional(postnorm_prepare(d.smem_optin, d.postnorm.clusters));
+        if (!d.postnorm_error) d.postnorm_error = optional(postnorm_rows_prepare(d.smem_optin));
         d.w4_rows_error = optional(w4_rows_prepare(d.smem_optin));
         d.w4_gemm_error = optional(w4_gemm_prepare(d.smem_optin, d.w4_clusters));
         for (int q8 = 0; q8 < 2; ++q8) {
@@ -520,9 +524,10 @@ int fused_postnorm(const Args& a, void* stream) {
     if (d->postnorm_error)
         return fail(TW_ERR_UNSUPPORTED, "step with two norms unavailable on this device (%s)",
                     cudaGetErrorName(static_cast<cudaError_t>(d->postnorm_error)));
-    const PostParams p{make_params(a, *d, a.t0, a.t1, nullptr), a.post_weight, a.gate,
-                       a.gate_tokens, a.post_eps, a.block_scale, a.residual_scale};
-    const int err = launch_postnorm(p, a.dtype, a.max_sms, d->sm_count, stream);
+    PostParams p{make_params(a, *d, a.t0, a.t1, nullptr), a.post_weight, a.gate,
+                 a.gate_tokens, a.post_eps, a.block_scale, a.residual_scale};
+    p.p.prefetch = a.max_sms >= d->sm_count ? 1 : 0;
+    const int err = launch_postnorm(p, a.dtype, a.max_sms, d->postnorm, stream);
     if (err != cudaSuccess) return cuda_fail(static_cast<cudaError_t>(err), "kernel launch");
     return TW_OK;
 }

@@ -163,8 +163,18 @@ struct PostParams {
     int64_t gate_tokens;
     float post_eps, block_scale, residual_scale;
 };
-int launch_postnorm(const PostParams& p, int dtype, int max_sms, int sm_count, void* stream);
-int postnorm_prepare(int smem_optin);
+struct PostDevice {
+    int sm_count, smem_optin;
+    // Clusters of 8 CTAs that run at once: [dtype][log2 vectors per thread][8-bit outputs].
+    int clusters[2][3][2];
+};
+int launch_postnorm(const PostParams& p, int dtype, int max_sms, const PostDevice& d,
+                    void* stream);
+int postnorm_prepare(int smem_optin, int (*clusters)[3][2]);
+// Its form for many tokens with long rows (tw_postnorm_rows.cu).
+int launch_postnorm_rows(const PostParams& p, int dtype, int sms, bool whole, int smem_optin,
+                         void* stream);
+int postnorm_rows_prepare(int smem_optin);
 
 // Record `message` as the calling thread's last error and return `code`.
 int set_last_error(int code, const char* message);

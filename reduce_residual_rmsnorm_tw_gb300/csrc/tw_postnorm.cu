@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
     constexpr int kRows = kWarps / W;
     // Rows of partials whose loads are in flight at once.
     constexpr int kAhead = VPT >= 8 ? 1 : 8 / VPT;
+    constexpr bool kEarly = VPT <= 2;
     const Params& p = pp.p;
     // Warp totals: [second reduction][buffer][warp], of sums and of maxima.
     __shared__ float warp_part[2][2][kWarps];
@@ -73,6 +74,15 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
                             : static_cast<int64_t>(gridDim.x) * kRows;
     int64_t t = p.t0 + (CL ? static_cast<int64_t>(blockIdx.x / csize)
                            : static_cast<int64_t>(blockIdx.x) * kRows + slot);
+    // The first token on its way into L2 while the launch before this one ends (a hint
+    // that reads nothing: what that launch writes is seen all the same).
+    if (p.prefetch && rtid == 0 && t < p.t1 && v_begin < v_end) {
+        const int64_t off = t * p.row_bytes + static_cast<int64_t>(v_begin) * 16;
+        const auto bytes = static_cast<uint32_t>((v_end - v_begin) * 16);
+        for (int r = 0; r < p.n_parts; ++r)
+            bulk_prefetch_l2(static_cast<const char*>(p.partials[r]) + off, bytes);
+        bulk_prefetch_l2(static_cast<const char*>(p.residual) + off, bytes);
+    }
     if constexpr (CL) cluster_arrive_relaxed();
     grid_dependency_wait();
     grid_launch_dependents();
@@ -128,6 +138,27 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
     // barrier (W == kWarps) are one.
     for (; t < p.t1; t += step, buf ^= 1) {
         const int64_t row_off = t * p.row_bytes;
+        // What the sum does not need is on its way beside it, the weights too where
+        // there are registers for them.
+        uint4 res[VPT], gate[VPT], pw[VPT], wv[VPT];
+        const char* gate_row =
+            pp.gate ? static_cast<const char*>(pp.gate) + t / pp.gate_tokens * p.row_bytes
+                    : nullptr;
+        auto load = [&](const void* row, int k) {
+            const int v = v_begin + rtid + k * W * 32;
+            return row && v < v_end ? ld_global(static_cast<const char*>(row) +
+                                                static_cast<int64_t>(v) * 16)
+                                    : make_uint4(0, 0, 0, 0);
+        };
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+            res[k] = load(static_cast<const char*>(p.residual) + row_off, k);
+            gate[k] = load(gate_row, k);
+            if constexpr (kEarly) {
+                pw[k] = load(pp.post_weight, k);
+                wv[k] = load(p.weight, k);
+            }
+        }
         float s[VPT][E];
 #pragma unroll
         for (int k = 0; k < VPT; ++k)
@@ -151,20 +182,6 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
                     if (r0 + a < p.n_parts && v_begin + rtid + k * W * 32 < v_end)
                         add_vec(s[k], raw[a][k], static_cast<T*>(nullptr));
         }
-        // The residual (and the gate) on their way while the sum is reduced.
-        uint4 res[VPT], gate[VPT];
-        const char* gate_row =
-            pp.gate ? static_cast<const char*>(pp.gate) + t / pp.gate_tokens * p.row_bytes
-                    : nullptr;
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            const int v = v_begin + rtid + k * W * 32;
-            res[k] = v < v_end ? ld_global(static_cast<const char*>(p.residual) + row_off +
-                                           static_cast<int64_t>(v) * 16)
-                               : make_uint4(0, 0, 0, 0);
-            gate[k] = gate_row && v < v_end ? ld_global(gate_row + static_cast<int64_t>(v) * 16)
-                                            : make_uint4(0, 0, 0, 0);
-        }
         float c = 1.f, most = 0.f;
         if (pp.post_weight) {
             float ss2[2] = {0.f, 0.f};
@@ -174,15 +191,11 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
             c = rsqrtf(total * p.inv_H + pp.post_eps);
         }
         float ss2[2] = {0.f, 0.f}, m = 0.f;
-        uint4 wv[VPT];
 #pragma unroll
         for (int k = 0; k < VPT; ++k) {
-            const int v = v_begin + rtid + k * W * 32;
-            const bool live = v < v_end;
             float f[E];
             if (pp.post_weight) {
-                V::to_float(live ? ld_global(static_cast<const char*>(pp.post_weight) + v * 16)
-                                 : make_uint4(0, 0, 0, 0), f);
+                V::to_float(kEarly ? pw[k] : load(pp.post_weight, k), f);
 #pragma unroll
                 for (int e = 0; e < E; ++e) s[k][e] = s[k][e] * c * f[e];
             }
@@ -196,8 +209,7 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
             for (int e = 0; e < E; ++e)
                 s[k][e] = fmaf(pp.block_scale, s[k][e], pp.residual_scale * f[e]);
             sum_squares<E>(ss2, s[k]);
-            wv[k] = live ? ld_global(static_cast<const char*>(p.weight) + v * 16)
-                         : make_uint4(0, 0, 0, 0);
+            if constexpr (!kEarly) wv[k] = load(p.weight, k);
             if constexpr (Q8) m = max_abs_product<T>(m, s[k], wv[k]);
         }
         const float total = reduce(1, ss2[0] + ss2[1], m, &most);
@@ -242,8 +254,6 @@ void* postnorm_rows_entry(int vpt, int w) {
         case 2 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 2, false, Q8>);
         case 4 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, false, Q8>);
         case 8 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 8, false, Q8>);
-        case 8 * 16 + 4: return reinterpret_cast<void*>(&postnorm_kernel<T, 4, 8, false, Q8>);
-        case 8 * 16 + 8: return reinterpret_cast<void*>(&postnorm_kernel<T, 8, 8, false, Q8>);
         default: return nullptr;
     }
 }
@@ -272,20 +282,45 @@ void* postnorm_kernel_for(int dtype, int vpt, int w, bool q8) {
               : postnorm_rows_entry<float, false>(vpt, w);
 }
 
-// Warps per row and vectors per thread for rows of nvec vectors.
+// Warps per row and vectors per thread for rows of nvec <= 512 vectors.
 void rows_shape(int64_t nvec, int* vpt, int* w) {
     *w = 1;
     *vpt = nvec <= 32 ? 1 : 2;
     while (*w < 8 && nvec > static_cast<int64_t>(*w) * 32 * *vpt) *w *= 2;
-    while (nvec > static_cast<int64_t>(*w) * 32 * *vpt) *vpt *= 2;
 }
 
-// Tokens up to which a range goes to clusters (one per token).
-constexpr int64_t kClusterTokens = 64;
+// Which kernel (us, 8 partials bf16: cluster / this file's rows / ring):
+//   rows to 8 KB   up to kRowsTokens tokens per SM this file's, a CTA or less per row,
+//                  two vectors a thread (64 x 4096 4.3 / 4.1 / 4.9, 200 x 4096 8.7 / 5.3
+//                  / 6.4, 2 x 400 x 4096 - / 6.3 / 6.0); rows below 4 KB always (2 x 4096
+//                  x 1024 - / 11.7 / 12.9)
+//   longer rows    a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
+//                  / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
+//   everything else the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9)
+constexpr int64_t kShortRowBytes = 4096, kRowsRowBytes = 8192;
+constexpr int64_t kRowsTokens = 2;
+
+cudaLaunchConfig_t cluster_config(int cluster, int64_t tokens, size_t smem, bool pdl, void* stream,
+                                  cudaLaunchAttribute (&attr)[2]) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(cluster * tokens));
+    cfg.blockDim = dim3(kClusterCta);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 2 : 1;
+    return cfg;
+}
 
 }  // namespace
 
-int postnorm_prepare(int smem_optin) {
+int postnorm_prepare(int smem_optin, int (*clusters)[3][2]) {
     if (smem_optin < kExclusiveSmemBytes + 2048) return static_cast<int>(cudaErrorInvalidValue);
     for (int dt = 0; dt < 2; ++dt)
         for (int w = 0; w <= 8; w = w ? 2 * w : 1)
@@ -297,43 +332,53 @@ int postnorm_prepare(int smem_optin) {
                         fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
                     if (e != cudaSuccess) return static_cast<int>(e);
                 }
+    // Clusters of 8 CTAs that run at once, by vectors per thread (1, 2, 4).
+    for (int v = 0; v < 3; ++v) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = cluster_config(8, 1, 0, false, nullptr, attr);
+        for (int dt = 0; dt < 2; ++dt)
+            for (bool q8 : {false, true}) {
+                int n = 0;
+                cudaError_t e = cudaOccupancyMaxActiveClusters(
+                    &n, postnorm_kernel_for(dt, 1 << v, 0, q8), &cfg);
+                if (e != cudaSuccess) return static_cast<int>(e);
+                clusters[dt][v][q8] = n;
+            }
+    }
     return 0;
 }
 
-int launch_postnorm(const PostParams& pp, int dtype, int max_sms, int sm_count, void* stream) {
+int launch_postnorm(const PostParams& pp, int dtype, int max_sms, const PostDevice& d,
+                    void* stream) {
     const Params& p = pp.p;
     const int64_t tokens = p.t1 - p.t0, nvec = p.row_bytes / 16;
-    const int64_t sms = max_sms < sm_count ? max_sms : sm_count;
+    const int64_t sms = max_sms < d.sm_count ? max_sms : d.sm_count;
     // Under a budget each CTA is alone on its SM.
-    const bool whole = max_sms >= sm_count;
+    const bool whole = max_sms >= d.sm_count;
     const size_t smem = whole ? 0 : kExclusiveSmemBytes;
-    int cluster = 1;
-    while (cluster * 2 <= 8 && cluster * 2 <= sms) cluster *= 2;
-    const int vc = cluster_vectors_per_thread(p.row_bytes, cluster);
-    if (tokens <= kClusterTokens && vc != 0 && (whole || tokens * cluster <= sms)) {
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(cluster * tokens));
-        cfg.blockDim = dim3(kClusterCta);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = static_cast<cudaStream_t>(stream);
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
-        attr[0].val.clusterDim.y = 1;
-        attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = whole ? 2 : 1;
-        void* args[] = {const_cast<PostParams*>(&pp)};
-        return static_cast<int>(
-            cudaLaunchKernelExC(&cfg, postnorm_kernel_for(dtype, vc, 0, p.q8 != 0), args));
+    if (p.row_bytes > kRowsRowBytes) {
+        int cluster = 1;
+        while (cluster * 2 <= 8 && cluster * 2 <= sms) cluster *= 2;
+        const int vc = cluster_vectors_per_thread(p.row_bytes, cluster);
+        const int64_t at_once =
+            whole ? vc ? d.clusters[dtype][vc == 4 ? 2 : vc - 1][p.q8] : 0 : sms / cluster;
+        if (vc != 0 && tokens <= at_once) {
+            cudaLaunchAttribute attr[2];
+            const cudaLaunchConfig_t cfg =
+                cluster_config(cluster, tokens, smem, whole, stream, attr);
+            void* args[] = {const_cast<PostParams*>(&pp)};
+            return static_cast<int>(
+                cudaLaunchKernelExC(&cfg, postnorm_kernel_for(dtype, vc, 0, p.q8 != 0), args));
+        }
     }
+    if (p.row_bytes >= kShortRowBytes &&
+        (p.row_bytes > kRowsRowBytes || tokens > kRowsTokens * sms))
+        return launch_postnorm_rows(pp, dtype, static_cast<int>(sms), whole, d.smem_optin, stream);
     int vpt = 0, w = 0;
     rows_shape(nvec, &vpt, &w);
     const int64_t rows = kThreads / 32 / w;
     const int64_t ctas = (tokens + rows - 1) / rows;
-    const int64_t most = !whole ? sms : w == 8 ? int64_t{1} << 30 : int64_t{8} * sms;
+    const int64_t most = whole ? (int64_t{1} << 31) - 1 : sms;
     return launch_with_pdl(postnorm_kernel_for(dtype, vpt, w, p.q8 != 0), pp,
                            static_cast<int>(ctas < most ? ctas : most), kThreads, smem, whole,
                            stream);
