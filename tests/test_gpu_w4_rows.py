@@ -100,6 +100,24 @@ def test_budgets_give_the_same(max_sms):
     check(torch.randn(130, 1424, generator=g), 64, "int4", max_sms=max_sms)
 
 
+@pytest.mark.parametrize("kind", ["int4", "e2m1"])
+def test_tensors_aligned_to_16_bytes_only(kind):
+    n, k = 20, 400
+    g = torch.Generator().manual_seed(11)
+    flat = torch.randn(n * k + 4, generator=g).cuda()
+    w = flat[4:].view(n, k)
+    assert w.data_ptr() % 32 == 16
+    w4, ref4 = tw.W4Weight(n, k, 64, kind), tw.W4Weight(n, k, 64, kind)
+    tw.tw_quantize_w4(w, w4)
+    tw.tw_quantize_w4(w.clone(), ref4)
+    assert torch.equal(w4.packed, ref4.packed)
+    out = torch.empty(n * k + 8, device="cuda")[4:-4].view(n, k)
+    tw.tw_dequantize_w4(w4, out)
+    want = torch.empty(n, k, device="cuda")
+    tw.tw_dequantize_w4(w4, want)
+    assert torch.equal(out, want)
+
+
 def test_past_2_31_elements():
     n, k = 40000, 65536  # 2.6e9 weights
     w4 = tw.W4Weight(n, k, 128, "e2m1")
