@@ -14,7 +14,8 @@ The GEMM of the bf16 steps is a plain library GEMM (``torch.matmul``, cuBLAS):
 the compute the pages overlap with, not part of the fused path.  Every step of
 the fused path runs in libtw.so.  The 8-bit step
 (:func:`two_chunk_layer_step_q8`) runs its product there too, and hands the
-normalised rows on in 8 bits.
+normalised rows on in 8 bits.  :func:`sandwich_layer_step_w4` is a layer with
+norms before and after its block and weights in 4 bits, for decode.
 """
 import torch
 
@@ -88,3 +89,39 @@ def two_chunk_layer_step_q8(x, x_scale, w, w_scale, partials, residual, weight, 
     fused_stream.wait_event(done_b)
     tw.tw_fused_reduce_add_rmsnorm_q8(*args, split, T, stream=fused_stream)
     gemm_stream.wait_stream(fused_stream)
+
+
+# From this many tokens on, reading 4-bit weights back and a library product are faster
+# than the product on 4 bits (8192 x 8192: see sandwich_layer_step_w4).
+W4_LIBRARY_TOKENS = 48
+
+
+def sandwich_layer_step_w4(x, w, partials, residual, weight, out, residual_out, eps,
+                           x_scale=None, out_scale=None, workspace=None, stream=None, **block):
+    """A row-parallel linear layer on 4-bit weights and the norms around the residual
+    add behind it, on one stream (default: the current one).
+
+    ``x`` [T, K] and ``w`` (a tw.W4Weight of H channels) give partial 0 = x @ w^T ([T, H];
+    the other partials stand for the other ranks' outputs); then
+    tw_fused_reduce_postnorm_add_rmsnorm with ``block`` (post_weight, post_eps, gate,
+    gate_tokens, block_scale, residual_scale), or its form with 8-bit outputs where
+    ``out_scale`` is given.  ``x`` may be in 8 bits with ``x_scale``, as that form leaves
+    rows.
+
+    ``workspace``, a [H, K] bfloat16 tensor, is for many tokens: from W4_LIBRARY_TOKENS
+    on a bfloat16 ``x`` (with bfloat16 partials) is multiplied by the weights read back
+    into it, a plain library GEMM."""
+    stream = torch.cuda.current_stream() if stream is None else stream
+    if (workspace is not None and x.shape[0] >= W4_LIBRARY_TOKENS
+            and x.dtype == partials[0].dtype == torch.bfloat16):
+        tw.tw_dequantize_w4(w, workspace, stream=stream)
+        with torch.cuda.stream(stream):
+            torch.matmul(x, workspace.t(), out=partials[0])
+    else:
+        tw.tw_gemm_w4(x, w, partials[0], x_scale=x_scale, stream=stream)
+    if out_scale is None:
+        tw.tw_fused_reduce_postnorm_add_rmsnorm(partials, residual, weight, out, residual_out,
+                                                eps, stream=stream, **block)
+    else:
+        tw.tw_fused_reduce_postnorm_add_rmsnorm_q8(partials, residual, weight, out, out_scale,
+                                                   residual_out, eps, stream=stream, **block)
