@@ -13,13 +13,12 @@
 // 16 channels is contiguous, so a tile is one bulk copy into the warp's own ring in
 // shared memory, a few tiles ahead, with no barrier but the copy's.
 //
-// Two CTAs of eight warps share an SM, so that one streams while the other starts,
-// joins or stores.  A CTA holds x of its K in shared memory and takes an even share
-// of the stripes, `at_once` of them at a time: as many warps share a stripe, each a
-// contiguous piece of its K, and their sums are joined through shared memory in warp
-// order.  A cluster of CTAs may split K as well (where x would not fit, or its copies
-// into every SM would outweigh W), and joins through distributed shared memory in
-// rank order.
+// Two CTAs of eight warps share an SM, so that one streams while the other starts or
+// joins.  A CTA holds x of its K in shared memory and takes an even share of the
+// stripes; a cluster of CTAs may split K (where x would not fit, or its copies into
+// every SM would outweigh W).  A warp's piece of work is a share of a stripe's K; the
+// warps take pieces in turn and never wait for each other, but leave their sums where
+// the stripe's CTA of the cluster adds them up, in their order, when all are done.
 #include <cuda_fp16.h>
 
 #include "tw_tcgen05.cuh"
@@ -36,7 +35,7 @@ constexpr int kMinSlots = 2, kMaxSlots = 4;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kXPad = 32;  // bf16: rows of x 64 bytes off each other in the banks
-constexpr int kXAhead = 4;
+constexpr int kXAhead = 8;  // 16-byte pieces of x of a thread in flight
 constexpr int kColumnsMax = 32;  // tokens at a time (fp32 x: three for one)
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -115,74 +114,61 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Eight values of x as they lie in memory: 16 bytes of bf16, 32 of fp32, 8 of
-// 8-bit values.
-struct XEight {
-    uint4 v[2];
-    __device__ __forceinline__ void load(const char* from, int xtype) {
-        if (xtype >= TW_X_INT8) {
-            const uint2 b = *reinterpret_cast<const uint2*>(from);
-            v[0].x = b.x;
-            v[0].y = b.y;
-            return;
-        }
-        v[0] = ld_global(from);
-        if (xtype == TW_X_F32) v[1] = ld_global(from + 16);
-    }
-};
+// int8 x is held times 2^-7: a byte in a bf16's last bits is v 2^-133 (as in widen).
+constexpr float kInt8Factor = 128.f;
 
-// They as bf16 in terms[0] (8-bit and bf16) or as three terms that add up to them
-// (fp32: the leading eight bits, cut off, then the next eight, then the rest; an
-// infinity or a NaN as its own first term).
-__device__ __forceinline__ void x_terms(const XEight& x, int xtype, uint4 (&terms)[3]) {
+__device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+// Sixteen bytes of x (8 bf16, 4 fp32 or 16 8-bit values, the first k of them) as bf16
+// to row + 2 k and, fp32, as three terms that add up to them to three rows `stride`
+// apart: the leading eight bits, cut off, then the next eight, then the rest; an
+// infinity or a NaN as its own first term.
+__device__ __forceinline__ void store_x(const uint4& x, int xtype, uint32_t to, int stride) {
+    const uint32_t word[4] = {x.x, x.y, x.z, x.w};
     if (xtype == TW_X_BF16) {
-        terms[0] = x.v[0];
+        sts128(to, x);
     } else if (xtype == TW_X_F32) {
-        float f[8];
-        Vec<float>::to_float(x.v[0], f);
-        Vec<float>::to_float(x.v[1], f + 4);
-        uint32_t w[3][4];
+        float t[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float t[3][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float v = f[2 * i + h];
-                const bool finite = fabsf(v) <= 3.402823466e38f;
-                t[0][h] = finite ? __uint_as_float(__float_as_uint(v) & 0xffff0000u) : v;
-                const float rest = finite ? v - t[0][h] : 0.f;
-                t[1][h] = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
-                t[2][h] = rest - t[1][h];
-            }
-#pragma unroll
-            for (int p = 0; p < 3; ++p) w[p][i] = pack_bf16(t[p][0], t[p][1]);
+            const float v = __uint_as_float(word[i]);
+            const bool finite = fabsf(v) <= 3.402823466e38f;
+            t[0][i] = finite ? __uint_as_float(word[i] & 0xffff0000u) : v;
+            const float rest = finite ? v - t[0][i] : 0.f;
+            t[1][i] = __uint_as_float(__float_as_uint(rest) & 0xffff0000u);
+            t[2][i] = rest - t[1][i];
         }
 #pragma unroll
-        for (int p = 0; p < 3; ++p) terms[p] = make_uint4(w[p][0], w[p][1], w[p][2], w[p][3]);
+        for (int p = 0; p < 3; ++p)
+            sts64(to + p * stride, pack_bf16(t[p][0], t[p][1]), pack_bf16(t[p][2], t[p][3]));
     } else {
-        uint32_t w[4];
+        uint32_t h[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t two = (i < 2 ? x.v[0].x : x.v[0].y) >> (i % 2 * 16) & 0xffffu;
+        for (int i = 0; i < 8; ++i) {
             if (xtype == TW_X_INT8) {
-                w[i] = pack_bf16(static_cast<float>(static_cast<int8_t>(two & 0xffu)),
-                                 static_cast<float>(static_cast<int8_t>(two >> 8)));
+                const uint32_t u = __byte_perm(word[i / 2] ^ 0x80808080u, 0,
+                                               i % 2 ? 0x4342 : 0x4140);  // v + 128
+                asm("fma.rn.bf16x2 %0, %1, %2, %3;"
+                    : "=r"(h[i])
+                    : "r"(u), "r"(0x7e807e80u), "r"(0xbf80bf80u));  // 2^126, -1
             } else {
-                uint32_t h;
+                uint32_t f;
                 asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\t"
                     "cvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
-                    : "=r"(h)
-                    : "r"(two));
-                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-                w[i] = pack_bf16(f.x, f.y);
+                    : "=r"(f)
+                    : "r"(word[i / 2] >> (i % 2 * 16)));
+                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                h[i] = pack_bf16(v.x, v.y);
             }
         }
-        terms[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        sts128(to, make_uint4(h[0], h[1], h[2], h[3]));
+        sts128(to + 16, make_uint4(h[4], h[5], h[6], h[7]));
     }
 }
 
-// Floats between the columns of a warp's sums.
-constexpr int kRowStride = kW4Channels + 1;
+// Floats between the columns of a piece's sums (a fragment's stores meet no bank twice).
+constexpr int kRowStride = kW4Channels + 4;
 // Tiles that a warp warms L2 with before the launch before this one has ended.
 constexpr int kWarm = 16;
 // Tiles of x that a CTA holds at a time.
@@ -193,10 +179,11 @@ __host__ __device__ constexpr int x_tiles(int tiles, int split, int slices) {
 struct W4Plan {
     W4GemmArgs a;
     int tokens;       // at a time
-    int log_at_once;  // stripes of a CTA at a time
-    int log_split;    // CTAs of a cluster, which split K
+    int split;        // CTAs of a cluster, which split K
     int slots;        // of a warp's ring
     int slices;       // of a CTA's K, whose x is in shared memory one after the other
+    int shares;       // pieces of a stripe's K in a slice
+    int pass;         // stripes whose sums are held at a time
     unsigned int* status;
 };
 
@@ -216,24 +203,12 @@ __device__ __forceinline__ void lds_scales(uint32_t (&s)[128 / G], uint32_t addr
                      : "r"(addr));
 }
 
-// A warp's way through its CTA's stripes: rounds of up to 2^log_at_once stripes (fewer
-// in the last), each round in slices of K, in each a contiguous piece of a stripe's
-// tiles.
+// A warp's way through its CTA's pieces: passes of up to `pass` stripes, in each the
+// slices of K one after the other, in each the pieces warp, warp + kWarps, ...
 struct Way {
-    int at, end;    // the round's first stripe and the CTA's last
-    int log_n;      // stripes of the round
-    int stripe;     // this warp's
-    __device__ __forceinline__ void round(int log_at_once, int warp) {
-        log_n = log_at_once;
-        while (log_n > 0 && (1 << (log_n - 1)) >= end - at) --log_n;
-        stripe = at + (warp << log_n) / kWarps;
-    }
-    // This warp's first tile and tiles of [lo, hi).
-    __device__ __forceinline__ void piece(int warp, int lo, int hi, int* first, int* n) const {
-        const int shares = kWarps >> log_n, share = warp & (shares - 1);
-        *first = lo + (hi - lo) * share / shares;
-        *n = stripe < end ? lo + (hi - lo) * (share + 1) / shares - *first : 0;
-    }
+    int at, end;    // the pass's first stripe and the CTA's last
+    int slice, item;
+    int stripe, first, tiles;  // the piece: its stripe, first tile and tiles
 };
 
 // INT4: the weights' type; NT: blocks of eight columns of x (fp32: three per token);
@@ -243,10 +218,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     w4_gemm_kernel(const __grid_constant__ W4Plan plan) {
     constexpr int kTile = w4_tile_bytes(G);
     constexpr int kChunk = chunk_of(NT), kSlot = kChunk * kTile;
-    constexpr int kColumns = NT * 8;
     const W4GemmArgs& a = plan.a;
     extern __shared__ __align__(128) unsigned char smem[];
-    float* part = reinterpret_cast<float*>(smem);  // [warp][column][kRowStride]
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x / 32), 0);
     const int lane = threadIdx.x % 32;
     const int row = lane / 4, quad = lane % 4;
@@ -255,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tiles_k = (K + kW4Inner - 1) / kW4Inner;
     const int stripes = static_cast<int>((a.N + kW4Channels - 1) / kW4Channels);
     // This CTA's share of K (of the cluster), cut into slices, and of the stripes.
-    const int split = 1 << plan.log_split, slices = plan.slices;
+    const int split = plan.split, slices = plan.slices, shares = plan.shares;
     const int rank = split > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
     const int lo = tiles_k * rank / split, hi = tiles_k * (rank + 1) / split;
     auto slice_at = [&](int s) { return lo + (hi - lo) * s / slices; };
@@ -263,11 +236,13 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int first = static_cast<int>(stripes * set / sets);
     const int end = static_cast<int>(stripes * (set + 1) / sets);
     const int x_stride = (x_tiles(tiles_k, split, slices) * kW4Inner + kXPad) * 2;
-    // Sums that the cluster's CTAs write here: [buffer][rank][column][channel of this
-    // rank's]; the rings; their barriers; x.
-    float* joined = part + kWarps * kColumns * kRowStride;
-    const int own = (kW4Channels << plan.log_at_once) / split;
-    const uint32_t rings = smem_addr(joined) + (split > 1 ? 2 * split * kColumns * own * 4 : 0);
+    // Stripe i of a pass belongs to rank i % split, which holds its pieces' sums:
+    // [piece][i / split][column][kRowStride].  Then the rings, their barriers, x.
+    const int columns = plan.tokens * parts;
+    const int owned = (plan.pass + split - 1) / split;
+    float* sums = reinterpret_cast<float*>(smem);
+    const uint32_t rings =
+        smem_addr(smem) + split * slices * shares * owned * columns * kRowStride * 4;
     const uint32_t ring = rings + warp * plan.slots * kSlot;
     const uint32_t bars = rings + kWarps * plan.slots * kSlot;
     const uint32_t bar = bars + warp * kMaxSlots * 8;
@@ -278,40 +253,57 @@ __global__ void __launch_bounds__(kThreads, 2)
         mbar_init_fence();
     }
     __syncwarp();
-    const char* packed = static_cast<const char*>(a.packed);
-    Way ld{first, end, 0, 0};
-    int ld_slice = 0, ld_first = 0, left = 0;
-    const char* from = packed;
-    auto begin = [&]() {
-        ld.piece(warp, slice_at(ld_slice), slice_at(ld_slice + 1), &ld_first, &left);
-        from = packed + (static_cast<int64_t>(ld.stripe) * tiles_k + ld_first) * kTile;
+    auto items_of = [&](const Way& w) {
+        return (end - w.at < plan.pass ? end - w.at : plan.pass) * shares;
     };
-    ld.round(plan.log_at_once, warp);
-    begin();
+    auto piece = [&](Way& w) {
+        const int share = w.item % shares;
+        const int from = slice_at(w.slice), to = slice_at(w.slice + 1);
+        w.stripe = w.at + w.item / shares;
+        w.first = from + (to - from) * share / shares;
+        w.tiles = from + (to - from) * (share + 1) / shares - w.first;
+    };
+    const char* packed = static_cast<const char*>(a.packed);
+    auto place = [&](const Way& w) {
+        return packed + (static_cast<int64_t>(w.stripe) * tiles_k + w.first) * kTile;
+    };
+    Way ld{first, end, 0, warp, 0, 0, 0};
     // The first W on its way into L2 while the launch before this one ends (a hint that
     // reads nothing: what that launch writes is seen all the same).
-    if (lane == 0 && left > 0)
-        bulk_prefetch_l2(from, static_cast<uint32_t>((left < kWarm ? left : kWarm) * kTile));
+    if (ld.item < items_of(ld)) {
+        piece(ld);
+        if (lane == 0 && ld.tiles > 0)
+            bulk_prefetch_l2(place(ld), static_cast<uint32_t>(
+                                            (ld.tiles < kWarm ? ld.tiles : kWarm) * kTile));
+    }
     if (split > 1) cluster_barrier();  // every CTA runs before any writes into it
     grid_dependency_wait();
     grid_launch_dependents();
 
     const uint32_t one = elect_one();
     uint32_t slot_ld = 0, slot = 0, phase = 0;
-    int buf = 0;
     for (int64_t m0 = 0; m0 < a.M; m0 += plan.tokens) {
         const int tokens = static_cast<int>(a.M - m0 < plan.tokens ? a.M - m0 : plan.tokens);
         const int cols = tokens * parts;
+        // The next chunk to load.
+        const char* from = packed;
+        int left = 0;
+        ld = Way{first, end, 0, warp - kWarps, 0, 0, 0};
         auto load = [&]() {
-            while (left == 0) {  // a warp may be without tiles for whole rounds
+            while (left == 0) {  // on to the warp's next piece (which may be without tiles)
                 if (ld.at >= end) return;
-                if (++ld_slice >= slices) {
-                    ld_slice = 0;
-                    ld.at += 1 << ld.log_n;
-                    if (ld.at >= end) return;
-                    ld.round(plan.log_at_once, warp);
+                ld.item += kWarps;
+                if (ld.item >= items_of(ld)) {
+                    ld.item = warp - kWarps;
+                    if (++ld.slice == slices) {
+                        ld.slice = 0;
+                        ld.at += plan.pass;
+                    }
+                    continue;
                 }
-                begin();
+                piece(ld);
+                left = ld.tiles;
+                from = place(ld);
             }
             const int n = left < kChunk ? left : kChunk;
             if (one) {
@@ -322,46 +314,39 @@ __global__ void __launch_bounds__(kThreads, 2)
             left -= n;
             if (++slot_ld == static_cast<uint32_t>(plan.slots)) slot_ld = 0;
         };
-        ld = Way{first, end, 0, 0};
-        ld.round(plan.log_at_once, warp);
-        ld_slice = 0;
-        begin();
         for (int d = 0; d < plan.slots; ++d) load();
 
         // x of a slice of this CTA's K, zero up to the end of its last tile; kXAhead
         // loads of a thread in flight.
         auto stage_x = [&](int slice) {
-            const int x_size = a.xtype == TW_X_BF16 ? 2 : a.xtype == TW_X_F32 ? 4 : 1;
+            const int log_size = a.xtype == TW_X_BF16 ? 1 : a.xtype == TW_X_F32 ? 2 : 0;
+            const int per_piece = 16 >> log_size;  // values
             const int k0 = slice_at(slice) * kW4Inner;
             const uint32_t row_pieces =
-                static_cast<uint32_t>(slice_at(slice + 1) - slice_at(slice)) * (kW4Inner / 8);
+                static_cast<uint32_t>((slice_at(slice + 1) - slice_at(slice)) * kW4Inner) /
+                per_piece;
             // The thread's next piece: the at-th of token t.
             uint32_t t = 0, at = threadIdx.x;
             const auto count = static_cast<uint32_t>(tokens);
             while (t < count) {
-                XEight x[kXAhead] = {};
+                uint4 x[kXAhead];
                 uint32_t to[kXAhead];
-                bool in[kXAhead];
 #pragma unroll
                 for (int i = 0; i < kXAhead; ++i, at += kThreads) {
                     while (at >= row_pieces && t < count) {
                         at -= row_pieces;
                         ++t;
                     }
-                    in[i] = t < count;
-                    to[i] = xs + t * parts * x_stride + at * 16;
-                    const int64_t k = k0 + static_cast<int64_t>(at) * 8;
-                    if (in[i] && k < K)
-                        x[i].load(static_cast<const char*>(a.x) + ((m0 + t) * a.K + k) * x_size,
-                                  a.xtype);
+                    x[i] = make_uint4(0, 0, 0, 0);
+                    to[i] = t < count ? xs + t * parts * x_stride + at * per_piece * 2 : 0;
+                    const int64_t k = k0 + static_cast<int64_t>(at) * per_piece;
+                    if (t < count && k < K)
+                        x[i] = ld_global(static_cast<const char*>(a.x) +
+                                         (((m0 + t) * a.K + k) << log_size));
                 }
 #pragma unroll
-                for (int i = 0; i < kXAhead; ++i) {
-                    if (!in[i]) break;
-                    uint4 terms[3];
-                    x_terms(x[i], a.xtype, terms);
-                    for (int p = 0; p < parts; ++p) sts128(to[i] + p * x_stride, terms[p]);
-                }
+                for (int i = 0; i < kXAhead; ++i)
+                    if (to[i] != 0) store_x(x[i], a.xtype, to[i], x_stride);
             }
             __syncthreads();
         };
@@ -373,132 +358,130 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int b = 0; b < NT; ++b)
             x_row[b] = xs + (b * 8 + row < cols ? b * 8 + row : 0) * x_stride + quad * 16;
 
-        Way at{first, end, 0, 0};
-        for (; at.at < end; at.at += 1 << at.log_n) {
-            at.round(plan.log_at_once, warp);
-            float total[NT][4] = {};
-            for (int slice = 0; slice < slices; ++slice) {
+        Way at{first, end, 0, 0, 0, 0, 0};
+        for (; at.at < end; at.at += plan.pass) {
+            const int items = items_of(at);
+            for (at.slice = 0; at.slice < slices; ++at.slice) {
                 if (slices > 1) {
                     __syncthreads();  // the x before has been read
-                    stage_x(slice);
+                    stage_x(at.slice);
                 }
-                int tile = 0, tiles = 0;
-                at.piece(warp, slice_at(slice), slice_at(slice + 1), &tile, &tiles);
-                uint32_t x_at = (tile - slice_at(slice)) * (kW4Inner * 2);
-                for (int i = 0; i < tiles; i += kChunk) {
-                    // (A copy that does not arrive: the device status says so.)
-                    if (!mbar_wait_slice(bar + slot * 8, phase, nullptr))
-                        atomicOr(plan.status, 1u);
-                    const uint32_t t = ring + slot * kSlot + lane * 16;
-                    const uint32_t ts = ring + slot * kSlot + 1024 + row * (512 / G);
+                for (at.item = warp; at.item < items; at.item += kWarps) {
+                    piece(at);
+                    const int tiles = at.tiles;
+                    float total[NT][4] = {};
+                    uint32_t x_at = (at.first - slice_at(at.slice)) * (kW4Inner * 2);
+                    for (int i = 0; i < tiles; i += kChunk) {
+                        // (A copy that does not arrive: the device status says so.)
+                        if (!mbar_wait_slice(bar + slot * 8, phase, nullptr))
+                            atomicOr(plan.status, 1u);
+                        const uint32_t t = ring + slot * kSlot + lane * 16;
+                        const uint32_t ts = ring + slot * kSlot + 1024 + row * (512 / G);
 #pragma unroll
-                    for (int c = 0; c < kChunk; ++c, x_at += kW4Inner * 2) {
-                        if (c > 0 && i + c >= tiles) break;
-                        const uint4 w[2] = {lds128(t + c * kTile), lds128(t + c * kTile + 512)};
-                        uint32_t s[128 / G];
-                        lds_scales<G>(s, ts + c * kTile);
-                        // Two chains of MMAs a group, so that one hides the other's latency.
-                        float sum[2][NT][4];
+                        for (int c = 0; c < kChunk; ++c, x_at += kW4Inner * 2) {
+                            if (c > 0 && i + c >= tiles) break;
+                            const uint4 w[2] = {lds128(t + c * kTile), lds128(t + c * kTile + 512)};
+                            uint32_t s[128 / G];
+                            lds_scales<G>(s, ts + c * kTile);
+                            // Two chains of MMAs a group, so that one hides the other's latency.
+                            float sum[2][NT][4];
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint4 xv[NT];
-#pragma unroll
-                            for (int b = 0; b < NT; ++b) xv[b] = lds128(x_row[b] + x_at + j * 64);
-                            uint32_t u[4], v[4];
-                            widen<INT4>(word_of(w[0], j), u);
-                            widen<INT4>(word_of(w[1], j), v);
-#pragma unroll
-                            for (int b = 0; b < NT; ++b) {
-                                if (j * 32 % G == 0) {
-                                    mma_first(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
-                                    mma_first(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
-                                } else {
-                                    mma(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
-                                    mma(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
-                                }
-                            }
-                            if ((j + 1) * 32 % G == 0) {
-                                // The group is whole.
-                                const float s0 = __uint_as_float(s[j * 32 / G] << 16);
-                                const float s1 = __uint_as_float(s[j * 32 / G] & 0xffff0000u);
+                            for (int j = 0; j < 4; ++j) {
+                                uint4 xv[NT];
 #pragma unroll
                                 for (int b = 0; b < NT; ++b)
+                                    xv[b] = lds128(x_row[b] + x_at + j * 64);
+                                uint32_t u[4], v[4];
+                                widen<INT4>(word_of(w[0], j), u);
+                                widen<INT4>(word_of(w[1], j), v);
 #pragma unroll
-                                    for (int e = 0; e < 4; ++e)
-                                        total[b][e] = fmaf(sum[0][b][e] + sum[1][b][e],
-                                                           e < 2 ? s0 : s1, total[b][e]);
+                                for (int b = 0; b < NT; ++b) {
+                                    if (j * 32 % G == 0) {
+                                        mma_first(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x,
+                                                  xv[b].y);
+                                        mma_first(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z,
+                                                  xv[b].w);
+                                    } else {
+                                        mma(sum[0][b], u[0], v[0], u[1], v[1], xv[b].x, xv[b].y);
+                                        mma(sum[1][b], u[2], v[2], u[3], v[3], xv[b].z, xv[b].w);
+                                    }
+                                }
+                                if ((j + 1) * 32 % G == 0) {
+                                    // The group is whole.
+                                    const float s0 = __uint_as_float(s[j * 32 / G] << 16);
+                                    const float s1 = __uint_as_float(s[j * 32 / G] & 0xffff0000u);
+#pragma unroll
+                                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                                        for (int e = 0; e < 4; ++e)
+                                            total[b][e] = fmaf(sum[0][b][e] + sum[1][b][e],
+                                                               e < 2 ? s0 : s1, total[b][e]);
+                                }
                             }
                         }
+                        if (++slot == static_cast<uint32_t>(plan.slots)) {
+                            slot = 0;
+                            phase ^= 1u;
+                        }
+                        __syncwarp();  // every lane has read the slot
+                        load();
                     }
-                    if (++slot == static_cast<uint32_t>(plan.slots)) {
-                        slot = 0;
-                        phase ^= 1u;
-                    }
-                    __syncwarp();  // every lane has read the slot
-                    load();
+                    // The piece's sums, to where its stripe's rank adds them up.
+                    const int i = at.stripe - at.at;
+                    const int which = (rank * slices + at.slice) * shares + at.item % shares;
+                    float* place_of = sums + static_cast<int64_t>(which * owned + i / split) *
+                                                 columns * kRowStride + row;
+                    uint32_t to = smem_addr(place_of);
+                    if (split > 1) to = map_to_rank(to, static_cast<uint32_t>(i % split));
+#pragma unroll
+                    for (int b = 0; b < NT; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int c = b * 8 + quad * 2 + e % 2;
+                            if (c < cols)
+                                st_cluster_f32(to + (c * kRowStride + e / 2 * 8) * 4, total[b][e]);
+                        }
                 }
             }
-            // The warps' sums, joined in warp order.
-#pragma unroll
-            for (int b = 0; b < NT; ++b)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    part[(warp * kColumns + b * 8 + quad * 2 + e % 2) * kRowStride + row +
-                         e / 2 * 8] = total[b][e];
-            __syncthreads();
-            const int shares = kWarps >> at.log_n, log_channels = 4 + at.log_n;
-            const int64_t n0 = static_cast<int64_t>(at.at) * kW4Channels;
-            // Of column c, channel i of the round.
-            auto sum_of = [&](int c, int i) {
-                const float* from = part + ((i / 16 * shares) * kColumns + c) * kRowStride + i % 16;
+            __syncwarp();
+            if (split > 1)
+                cluster_barrier();
+            else
+                __syncthreads();
+            // Every piece of the pass is there: this rank's stripes, added up in order.
+            const int pieces = split * slices * shares;
+            const int mine = (items / shares - rank + split - 1) / split;  // stripes
+            const float factor = (INT4 ? kInt4Factor : 1.f) * (a.xtype == TW_X_INT8 ? kInt8Factor : 1.f);
+            for (int e = threadIdx.x; e < mine * tokens * kW4Channels; e += kThreads) {
+                const int ch = e % kW4Channels, rest = e / kW4Channels;
+                const int t = rest % tokens, i = rest / tokens;
+                const int64_t n =
+                    static_cast<int64_t>(at.at + i * split + rank) * kW4Channels + ch;
+                if (n >= a.N) continue;
                 float sum = 0.f;
-                for (int w = 0; w < shares; ++w) sum += from[w * kColumns * kRowStride];
-                return sum;
-            };
-            auto store = [&](int t, int i, float sum) {
-                if (n0 + i >= a.N || at.at + i / kW4Channels >= end) return;
-                if (INT4) sum *= kInt4Factor;
+                // fp32 x: the smaller terms first.
+                for (int p = parts - 1; p >= 0; --p) {
+                    const float* of = sums + (i * columns + t * parts + p) * kRowStride + ch;
+                    for (int q = 0; q < pieces; ++q)
+                        sum += of[static_cast<int64_t>(q) * owned * columns * kRowStride];
+                }
+                sum *= factor;
                 if (a.x_scale) sum *= a.x_scale[m0 + t];
-                const int64_t to = (m0 + t) * a.N + n0 + i;
+                const int64_t to = (m0 + t) * a.N + n;
                 if (a.dtype == TW_BF16)
                     static_cast<__nv_bfloat16*>(a.out)[to] = __float2bfloat16_rn(sum);
                 else
                     static_cast<float*>(a.out)[to] = sum;
-            };
-            if (split == 1) {
-                for (int e = threadIdx.x; e < tokens << log_channels; e += kThreads) {
-                    const int t = e >> log_channels, i = e & ((1 << log_channels) - 1);
-                    float sum = 0.f;
-                    // fp32 x: the smaller terms first.
-                    for (int p = parts - 1; p >= 0; --p) sum += sum_of(t * parts + p, i);
-                    store(t, i, sum);
-                }
-                __syncthreads();  // the sums are read
-            } else {
-                // Rank q finishes channels [q, q + 1) * channels / split of the round.  A
-                // buffer is written again two rounds later, behind the barrier that its
-                // readers reach when done.
-                const int log_own = log_channels - plan.log_split;
-                float* sums = joined + buf * split * kColumns * own;
-                for (int e = threadIdx.x; e < cols << log_channels; e += kThreads) {
-                    const int c = e >> log_channels, i = e & ((1 << log_channels) - 1);
-                    float* to = sums + (rank * kColumns + c) * own + (i & ((1 << log_own) - 1));
-                    st_cluster_f32(map_to_rank(smem_addr(to), static_cast<uint32_t>(i >> log_own)),
-                                   sum_of(c, i));
-                }
-                cluster_barrier();
-                for (int e = threadIdx.x; e < tokens << log_own; e += kThreads) {
-                    const int t = e >> log_own, i = e & ((1 << log_own) - 1);
-                    float sum = 0.f;
-                    for (int p = parts - 1; p >= 0; --p)
-                        for (int r = 0; r < split; ++r)
-                            sum += sums[(r * kColumns + t * parts + p) * own + i];
-                    store(t, (rank << log_own) + i, sum);
-                }
-                buf ^= 1;
+            }
+            // The sums are read before another pass (and x before other tokens') comes.
+            __syncwarp();
+            if (at.at + plan.pass < end || m0 + plan.tokens < a.M) {
+                if (split > 1)
+                    cluster_barrier();
+                else
+                    __syncthreads();
             }
         }
-        __syncthreads();  // x is read
     }
 }
 
@@ -518,14 +501,13 @@ void* kernel_for(int wtype, int nt, int group) {
 
 // Shared memory of a CTA for `columns` columns of x in `nt` blocks.
 int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
-    const int64_t part = static_cast<int64_t>(kWarps) * nt * 8 * kRowStride * 4;
-    const int64_t joined =
-        p.log_split > 0 ? int64_t{2} * nt * 8 * (kW4Channels << p.log_at_once) * 4 : 0;
-    const int64_t rings = kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8);
+    const int64_t sums = static_cast<int64_t>(p.split) * p.slices * p.shares *
+                         ((p.pass + p.split - 1) / p.split) * columns * kRowStride * 4;
+    const int64_t rings =
+        kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8);
     const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
-    return part + joined + rings +
-           static_cast<int64_t>(columns) *
-               (x_tiles(tiles, 1 << p.log_split, p.slices) * kW4Inner + kXPad) * 2;
+    return sums + rings + static_cast<int64_t>(columns) *
+                              (x_tiles(tiles, p.split, p.slices) * kW4Inner + kXPad) * 2;
 }
 // What a CTA may use where two share an SM.
 int64_t half_smem(int smem_optin) { return (smem_optin - 1024) / 2; }
@@ -579,43 +561,64 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     const int parts = a.xtype == TW_X_F32 ? 3 : 1;
     const int64_t stripes = (a.N + kW4Channels - 1) / kW4Channels;
     const int64_t tiles = (a.K + kW4Inner - 1) / kW4Inner;
-    W4Plan plan{a, 0, 0, 0, 0, 1, d.status};
-    int64_t smem = 0, sets = 0;
+    // Every cut that fits, by the time it takes: a warp's pieces and their tiles, staging
+    // x, a cluster's start and its barrier, each pass's barrier.  The nanoseconds are
+    // fitted to sweeps over splits and sizes (they rank the cuts; as times they are
+    // rough).  The most tokens at a time that fit; one token that does not fit the SMs
+    // of a budget goes in slices, staged again for each pass.
+    constexpr int64_t kTile2 = 440, kTile1 = 300;  // a tile of a warp, two or one CTA on an SM
+    constexpr int64_t kPiece = 250, kStage = 120, kPass = 600, kCluster = 1800;
+    W4Plan best{}, plan{a, 0, 0, 0, 1, 0, 0, d.status};
+    int64_t best_cost = -1, best_smem = 0, best_sets = 0;
     int nt = 0;
-    // The most tokens at a time whose x fits, K over the fewest CTAs, two of them on an
-    // SM if they fit so (under a budget each is alone there).  One token that does not
-    // fit the SMs of a budget: in slices, staged again for each round.
     auto choose = [&](int64_t tokens, int slices) {
         const int columns = static_cast<int>(tokens) * parts;
         const int blocks = columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
+        plan.tokens = static_cast<int>(tokens);
+        plan.slices = slices;
         for (int ctas = whole ? 2 : 1; ctas > 0; --ctas)
             for (int i = 0; i < 4 && (1 << i) <= tiles; ++i) {
-                int64_t at_once = sms * ctas >> i;
+                int64_t sets = sms * ctas >> i;
                 const int64_t clusters = d.w4_clusters[ctas - 1][i];
-                if (i > 0 && at_once > clusters) at_once = clusters;
-                if (at_once < 1) break;
-                sets = at_once < stripes ? at_once : stripes;
-                // Stripes at a time: a warp for each if there are that many, but some
-                // warps for one while they have two tiles each.
-                const int64_t share = (stripes + sets - 1) / sets;
-                plan.log_split = i;
-                plan.log_at_once = 0;
-                while ((1 << plan.log_at_once) < kWarps && (1 << plan.log_at_once) < share &&
-                       (i > 0 || plan.log_at_once < 1 ||
-                        2 * kWarps >> plan.log_at_once > tiles >> i))
-                    ++plan.log_at_once;
-                plan.slices = slices;
+                if (i > 0 && sets > clusters) sets = clusters;
+                if (sets < 1) break;
+                if (sets > stripes) sets = stripes;
+                const int64_t own = (stripes + sets - 1) / sets;  // stripes of a set
                 const int64_t room = ctas == 1 ? d.smem_optin : half_smem(d.smem_optin);
-                for (plan.slots = max_slots(blocks); plan.slots >= kMinSlots; --plan.slots) {
-                    smem = smem_bytes(blocks, columns, a.K, a.group, plan);
-                    if (smem > room) continue;
-                    if (ctas == 1 && smem < kExclusiveSmemBytes) smem = kExclusiveSmemBytes;
-                    plan.tokens = static_cast<int>(tokens);
+                const int64_t inner = x_tiles(static_cast<int>(tiles), 1 << i, slices);
+                plan.split = 1 << i;
+                for (plan.shares = 1; plan.shares <= kWarps && plan.shares <= inner;
+                     plan.shares *= 2) {
+                    // As many stripes a pass as their sums find room, few slots if need be.
+                    plan.pass = static_cast<int>(own < 1024 ? own : 1024);
+                    int64_t smem = 0;
+                    for (;;) {
+                        for (plan.slots = max_slots(blocks); plan.slots >= kMinSlots; --plan.slots)
+                            if ((smem = smem_bytes(blocks, columns, a.K, a.group, plan)) <= room)
+                                break;
+                        if (plan.slots >= kMinSlots || plan.pass == 1) break;
+                        plan.pass = (plan.pass + 1) / 2;
+                    }
+                    if (plan.slots < kMinSlots) continue;
+                    const int64_t passes = (own + plan.pass - 1) / plan.pass;
+                    const int64_t rounds =
+                        ((own < plan.pass ? own : plan.pass) * plan.shares + kWarps - 1) / kWarps;
+                    const int64_t each = (inner + plan.shares - 1) / plan.shares;
+                    const int64_t stage = columns * inner * (kW4Inner / 8) / kThreads * kStage;
+                    const int64_t cost =
+                        passes * (slices * rounds * (each * (ctas == 2 ? kTile2 : kTile1) * (2 + blocks) / 3 + kPiece) +
+                                  kPass + (i > 0 ? kPass : 0)) +
+                        (slices == 1 ? stage : stage * slices * passes) + (i > 0 ? kCluster : 0);
+                    if (best_cost >= 0 && cost >= best_cost) continue;
+                    best_cost = cost;
+                    best = plan;
+                    best_smem = smem;
+                    if (ctas == 1 && smem < kExclusiveSmemBytes) best_smem = kExclusiveSmemBytes;
+                    best_sets = sets;
                     nt = blocks;
-                    return true;
                 }
             }
-        return false;
+        return best_cost >= 0;
     };
     bool found = false;
     for (int64_t tokens = a.M < kColumnsMax / parts ? a.M : kColumnsMax / parts;
@@ -624,10 +627,10 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     for (int slices = 2; !found && slices <= tiles; slices *= 2) found = choose(1, slices);
     if (!found) return static_cast<int>(cudaErrorInvalidConfiguration);
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config(static_cast<int>(sets << plan.log_split),
-                                          1 << plan.log_split, static_cast<size_t>(smem), whole,
-                                          stream, attr);
-    void* args[] = {&plan};
+    const cudaLaunchConfig_t cfg =
+        config(static_cast<int>(best_sets * best.split), best.split,
+               static_cast<size_t>(best_smem), whole, stream, attr);
+    void* args[] = {&best};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, kernel_for(a.wtype, nt, a.group), args));
 }
 
