@@ -179,10 +179,10 @@ __host__ __device__ constexpr int x_tiles(int tiles, int split, int slices) {
 struct W4Plan {
     W4GemmArgs a;
     int tokens;       // at a time
-    int split;        // CTAs of a cluster, which split K
+    int log_split;    // CTAs of a cluster, which split K
     int slots;        // of a warp's ring
     int slices;       // of a CTA's K, whose x is in shared memory one after the other
-    int shares;       // pieces of a stripe's K in a slice
+    int log_shares;   // pieces of a stripe's K in a slice
     int pass;         // stripes whose sums are held at a time
     unsigned int* status;
 };
@@ -228,21 +228,22 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tiles_k = (K + kW4Inner - 1) / kW4Inner;
     const int stripes = static_cast<int>((a.N + kW4Channels - 1) / kW4Channels);
     // This CTA's share of K (of the cluster), cut into slices, and of the stripes.
-    const int split = plan.split, slices = plan.slices, shares = plan.shares;
+    const int log_split = plan.log_split, split = 1 << log_split;
+    const int log_shares = plan.log_shares, shares = 1 << log_shares, slices = plan.slices;
     const int rank = split > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
-    const int lo = tiles_k * rank / split, hi = tiles_k * (rank + 1) / split;
-    auto slice_at = [&](int s) { return lo + (hi - lo) * s / slices; };
-    const int64_t sets = gridDim.x / split, set = blockIdx.x / split;
+    const int lo = tiles_k * rank >> log_split, hi = tiles_k * (rank + 1) >> log_split;
+    auto slice_at = [&](int s) { return slices == 1 ? (s ? hi : lo) : lo + (hi - lo) * s / slices; };
+    const int64_t sets = gridDim.x >> log_split, set = blockIdx.x >> log_split;
     const int first = static_cast<int>(stripes * set / sets);
     const int end = static_cast<int>(stripes * (set + 1) / sets);
     const int x_stride = (x_tiles(tiles_k, split, slices) * kW4Inner + kXPad) * 2;
     // Stripe i of a pass belongs to rank i % split, which holds its pieces' sums:
     // [piece][i / split][column][kRowStride].  Then the rings, their barriers, x.
     const int columns = plan.tokens * parts;
-    const int owned = (plan.pass + split - 1) / split;
+    const int owned = (plan.pass + split - 1) >> log_split;
     float* sums = reinterpret_cast<float*>(smem);
     const uint32_t rings =
-        smem_addr(smem) + split * slices * shares * owned * columns * kRowStride * 4;
+        smem_addr(smem) + ((split * slices) << log_shares) * owned * columns * kRowStride * 4;
     const uint32_t ring = rings + warp * plan.slots * kSlot;
     const uint32_t bars = rings + kWarps * plan.slots * kSlot;
     const uint32_t bar = bars + warp * kMaxSlots * 8;
@@ -254,14 +255,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     __syncwarp();
     auto items_of = [&](const Way& w) {
-        return (end - w.at < plan.pass ? end - w.at : plan.pass) * shares;
+        return (end - w.at < plan.pass ? end - w.at : plan.pass) << log_shares;
     };
     auto piece = [&](Way& w) {
-        const int share = w.item % shares;
+        const int share = w.item & (shares - 1);
         const int from = slice_at(w.slice), to = slice_at(w.slice + 1);
-        w.stripe = w.at + w.item / shares;
-        w.first = from + (to - from) * share / shares;
-        w.tiles = from + (to - from) * (share + 1) / shares - w.first;
+        w.stripe = w.at + (w.item >> log_shares);
+        w.first = from + ((to - from) * share >> log_shares);
+        w.tiles = from + ((to - from) * (share + 1) >> log_shares) - w.first;
     };
     const char* packed = static_cast<const char*>(a.packed);
     auto place = [&](const Way& w) {
@@ -428,18 +429,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                     }
                     // The piece's sums, to where its stripe's rank adds them up.
                     const int i = at.stripe - at.at;
-                    const int which = (rank * slices + at.slice) * shares + at.item % shares;
-                    float* place_of = sums + static_cast<int64_t>(which * owned + i / split) *
-                                                 columns * kRowStride + row;
-                    uint32_t to = smem_addr(place_of);
-                    if (split > 1) to = map_to_rank(to, static_cast<uint32_t>(i % split));
+                    const int which = ((rank * slices + at.slice) << log_shares) +
+                                      (at.item & (shares - 1));
+                    uint32_t to =
+                        smem_addr(smem) +
+                        ((which * owned + (i >> log_split)) * columns * kRowStride + row) * 4;
+                    if (split > 1) to = map_to_rank(to, static_cast<uint32_t>(i & (split - 1)));
 #pragma unroll
                     for (int b = 0; b < NT; ++b)
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int c = b * 8 + quad * 2 + e % 2;
-                            if (c < cols)
-                                st_cluster_f32(to + (c * kRowStride + e / 2 * 8) * 4, total[b][e]);
+                            const uint32_t place_of = to + (c * kRowStride + e / 2 * 8) * 4;
+                            if (c < cols && split > 1)
+                                st_cluster_f32(place_of, total[b][e]);
+                            else if (c < cols)
+                                asm volatile("st.shared.f32 [%0], %1;" ::"r"(place_of),
+                                             "f"(total[b][e])
+                                             : "memory");
                         }
                 }
             }
@@ -449,21 +456,21 @@ __global__ void __launch_bounds__(kThreads, 2)
             else
                 __syncthreads();
             // Every piece of the pass is there: this rank's stripes, added up in order.
-            const int pieces = split * slices * shares;
-            const int mine = (items / shares - rank + split - 1) / split;  // stripes
+            const int pieces = (split * slices) << log_shares;
+            const int mine = ((items >> log_shares) - rank + split - 1) >> log_split;  // stripes
+            const int apart = owned * columns * kRowStride;
             const float factor = (INT4 ? kInt4Factor : 1.f) * (a.xtype == TW_X_INT8 ? kInt8Factor : 1.f);
             for (int e = threadIdx.x; e < mine * tokens * kW4Channels; e += kThreads) {
                 const int ch = e % kW4Channels, rest = e / kW4Channels;
-                const int t = rest % tokens, i = rest / tokens;
+                const int i = tokens == 1 ? rest : rest / tokens, t = rest - i * tokens;
                 const int64_t n =
-                    static_cast<int64_t>(at.at + i * split + rank) * kW4Channels + ch;
+                    static_cast<int64_t>(at.at + (i << log_split) + rank) * kW4Channels + ch;
                 if (n >= a.N) continue;
                 float sum = 0.f;
                 // fp32 x: the smaller terms first.
                 for (int p = parts - 1; p >= 0; --p) {
                     const float* of = sums + (i * columns + t * parts + p) * kRowStride + ch;
-                    for (int q = 0; q < pieces; ++q)
-                        sum += of[static_cast<int64_t>(q) * owned * columns * kRowStride];
+                    for (int q = 0; q < pieces; ++q, of += apart) sum += *of;
                 }
                 sum *= factor;
                 if (a.x_scale) sum *= a.x_scale[m0 + t];
@@ -501,13 +508,14 @@ void* kernel_for(int wtype, int nt, int group) {
 
 // Shared memory of a CTA for `columns` columns of x in `nt` blocks.
 int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
-    const int64_t sums = static_cast<int64_t>(p.split) * p.slices * p.shares *
-                         ((p.pass + p.split - 1) / p.split) * columns * kRowStride * 4;
+    const int split = 1 << p.log_split;
+    const int64_t sums = (static_cast<int64_t>(split) * p.slices << p.log_shares) *
+                         ((p.pass + split - 1) / split) * columns * kRowStride * 4;
     const int64_t rings =
         kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8);
     const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
     return sums + rings + static_cast<int64_t>(columns) *
-                              (x_tiles(tiles, p.split, p.slices) * kW4Inner + kXPad) * 2;
+                              (x_tiles(tiles, split, p.slices) * kW4Inner + kXPad) * 2;
 }
 // What a CTA may use where two share an SM.
 int64_t half_smem(int smem_optin) { return (smem_optin - 1024) / 2; }
@@ -561,13 +569,14 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     const int parts = a.xtype == TW_X_F32 ? 3 : 1;
     const int64_t stripes = (a.N + kW4Channels - 1) / kW4Channels;
     const int64_t tiles = (a.K + kW4Inner - 1) / kW4Inner;
-    // Every cut that fits, by the time it takes: a warp's pieces and their tiles, staging
-    // x, a cluster's start and its barrier, each pass's barrier.  The nanoseconds are
-    // fitted to sweeps over splits and sizes (they rank the cuts; as times they are
-    // rough).  The most tokens at a time that fit; one token that does not fit the SMs
-    // of a budget goes in slices, staged again for each pass.
-    constexpr int64_t kTile2 = 440, kTile1 = 300;  // a tile of a warp, two or one CTA on an SM
-    constexpr int64_t kPiece = 250, kStage = 120, kPass = 600, kCluster = 1800;
+    // Every cut that fits, by the time it takes in ns: a warp's tiles (more of them with
+    // two CTAs on an SM than with one) and pieces, each pass's barrier, of a cluster or not,
+    // staging x; eight CTAs in a cluster seldom find room.  Fitted to 356 cuts of 26 sizes
+    // (1 to 32 tokens, 300 to 32768 channels, K 256 to 8192): the cut taken is 3 % slower
+    // than the best on average, 19 % at most.  The most tokens at a time that fit; one
+    // token that does not fit the SMs of a budget goes in slices, staged for each pass.
+    constexpr int64_t kPiece = 770, kPass = 1200, kClusterPass = 1300, kStage = 160;
+    constexpr int64_t kSecondCta = 390, kClusterOf8 = 2500;
     W4Plan best{}, plan{a, 0, 0, 0, 1, 0, 0, d.status};
     int64_t best_cost = -1, best_smem = 0, best_sets = 0;
     int nt = 0;
@@ -586,9 +595,10 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
                 const int64_t own = (stripes + sets - 1) / sets;  // stripes of a set
                 const int64_t room = ctas == 1 ? d.smem_optin : half_smem(d.smem_optin);
                 const int64_t inner = x_tiles(static_cast<int>(tiles), 1 << i, slices);
-                plan.split = 1 << i;
-                for (plan.shares = 1; plan.shares <= kWarps && plan.shares <= inner;
-                     plan.shares *= 2) {
+                plan.log_split = i;
+                for (plan.log_shares = 0;
+                     plan.log_shares < 4 && (1 << plan.log_shares) <= inner; ++plan.log_shares) {
+                    const int64_t shares = 1 << plan.log_shares;
                     // As many stripes a pass as their sums find room, few slots if need be.
                     plan.pass = static_cast<int>(own < 1024 ? own : 1024);
                     int64_t smem = 0;
@@ -602,13 +612,15 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
                     if (plan.slots < kMinSlots) continue;
                     const int64_t passes = (own + plan.pass - 1) / plan.pass;
                     const int64_t rounds =
-                        ((own < plan.pass ? own : plan.pass) * plan.shares + kWarps - 1) / kWarps;
-                    const int64_t each = (inner + plan.shares - 1) / plan.shares;
-                    const int64_t stage = columns * inner * (kW4Inner / 8) / kThreads * kStage;
+                        ((own < plan.pass ? own : plan.pass) * shares + kWarps - 1) / kWarps;
+                    const int64_t each = (inner + shares - 1) / shares;
+                    const int64_t tile = ctas == 2 ? 232 + 152 * (blocks - 1) : 156 + 98 * (blocks - 1);
+                    const int64_t stage = columns * inner * kStage / 16;
                     const int64_t cost =
-                        passes * (slices * rounds * (each * (ctas == 2 ? kTile2 : kTile1) * (2 + blocks) / 3 + kPiece) +
-                                  kPass + (i > 0 ? kPass : 0)) +
-                        (slices == 1 ? stage : stage * slices * passes) + (i > 0 ? kCluster : 0);
+                        passes * (slices * rounds * (each * tile + kPiece) + kPass +
+                                  (i > 0 ? kClusterPass : 0)) +
+                        (slices == 1 ? stage : stage * slices * passes) +
+                        (ctas == 2 ? kSecondCta : 0) + (i == 3 ? kClusterOf8 : 0);
                     if (best_cost >= 0 && cost >= best_cost) continue;
                     best_cost = cost;
                     best = plan;
@@ -628,7 +640,7 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     if (!found) return static_cast<int>(cudaErrorInvalidConfiguration);
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg =
-        config(static_cast<int>(best_sets * best.split), best.split,
+        config(static_cast<int>(best_sets << best.log_split), 1 << best.log_split,
                static_cast<size_t>(best_smem), whole, stream, attr);
     void* args[] = {&best};
     return static_cast<int>(cudaLaunchKernelExC(&cfg, kernel_for(a.wtype, nt, a.group), args));
