@@ -35,7 +35,6 @@ constexpr int kMinSlots = 2, kMaxSlots = 4;
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kXPad = 32;  // bf16: rows of x 64 bytes off each other in the banks
-constexpr int kXAhead = 8;  // 16-byte pieces of x of a thread in flight
 constexpr int kColumnsMax = 32;  // tokens at a time (fp32 x: three for one)
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
@@ -120,15 +119,13 @@ constexpr float kInt8Factor = 128.f;
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
-// Sixteen bytes of x (8 bf16, 4 fp32 or 16 8-bit values, the first k of them) as bf16
-// to row + 2 k and, fp32, as three terms that add up to them to three rows `stride`
+// Sixteen bytes of x (4 fp32 or 16 8-bit values) as bf16 to `to` and, fp32, as three terms that add up to them to three rows `stride`
 // apart: the leading eight bits, cut off, then the next eight, then the rest; an
 // infinity or a NaN as its own first term.
-__device__ __forceinline__ void store_x(const uint4& x, int xtype, uint32_t to, int stride) {
+template <int XTYPE>
+__device__ __forceinline__ void store_x(const uint4& x, uint32_t to, int stride) {
     const uint32_t word[4] = {x.x, x.y, x.z, x.w};
-    if (xtype == TW_X_BF16) {
-        sts128(to, x);
-    } else if (xtype == TW_X_F32) {
+    if constexpr (XTYPE == TW_X_F32) {
         float t[3][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -146,7 +143,7 @@ __device__ __forceinline__ void store_x(const uint4& x, int xtype, uint32_t to, 
         uint32_t h[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (xtype == TW_X_INT8) {
+            if constexpr (XTYPE == TW_X_INT8) {
                 const uint32_t u = __byte_perm(word[i / 2] ^ 0x80808080u, 0,
                                                i % 2 ? 0x4342 : 0x4140);  // v + 128
                 asm("fma.rn.bf16x2 %0, %1, %2, %3;"
@@ -164,6 +161,35 @@ __device__ __forceinline__ void store_x(const uint4& x, int xtype, uint32_t to, 
         }
         sts128(to, make_uint4(h[0], h[1], h[2], h[3]));
         sts128(to + 16, make_uint4(h[4], h[5], h[6], h[7]));
+    }
+}
+
+// Where row t of `tokens` rows of x lands, `bytes` each, before it becomes `token` bytes of
+// bf16 at t * token: packed towards the end of those and one row more, so that no
+// row's bf16 comes to lie on a later row, or on itself, before it has been read.
+__device__ __forceinline__ int landing(int t, int tokens, int token, int bytes) {
+    return tokens * token - (tokens - 1 - t) * bytes;
+}
+// The rows that landed there as bf16: `inner` values of a row, zero from `own` on.  (One
+// piece of a thread at a time; with eight, longer code: 1 x 256 x 32768 fp32 4.3 -> 5.0 us.)
+template <int XTYPE>
+__device__ __forceinline__ void widen_x(uint32_t xs, int x_stride, int tokens, int inner,
+                                        int own) {
+    constexpr int kValues = XTYPE == TW_X_F32 ? 4 : 16;  // of a piece
+    const int token = x_stride * (XTYPE == TW_X_F32 ? 3 : 1);
+    const int pieces = inner / kValues, from_x = own / kValues;
+    int t = 0, at = threadIdx.x;  // the thread's piece: the at-th of token t
+#pragma unroll 1
+    for (int n = 0; n < tokens * pieces; n += kThreads, at += kThreads) {
+        while (at >= pieces && t < tokens) {
+            at -= pieces;
+            ++t;
+        }
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t < tokens && at < from_x)
+            x = lds128(xs + landing(t, tokens, token, pieces * 16) + at * 16);
+        __syncthreads();  // all of these are read
+        if (t < tokens) store_x<XTYPE>(x, xs + t * token + at * kValues * 2, x_stride);
     }
 }
 
@@ -247,13 +273,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t ring = rings + warp * plan.slots * kSlot;
     const uint32_t bars = rings + kWarps * plan.slots * kSlot;
     const uint32_t bar = bars + warp * kMaxSlots * 8;
-    const uint32_t xs = bars + kWarps * kMaxSlots * 8;
+    const uint32_t x_bar = bars + kWarps * kMaxSlots * 8;
+    const uint32_t xs = x_bar + 16;
 
     if (lane == 0) {
         for (int i = 0; i < plan.slots; ++i) mbar_init(bar + i * 8, 1);
+        if (warp == 0) mbar_init(x_bar, 1);
         mbar_init_fence();
     }
-    __syncwarp();
+    __syncthreads();
     auto items_of = [&](const Way& w) {
         return (end - w.at < plan.pass ? end - w.at : plan.pass) << log_shares;
     };
@@ -282,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid_launch_dependents();
 
     const uint32_t one = elect_one();
-    uint32_t slot_ld = 0, slot = 0, phase = 0;
+    uint32_t slot_ld = 0, slot = 0, phase = 0, x_phase = 0;
     for (int64_t m0 = 0; m0 < a.M; m0 += plan.tokens) {
         const int tokens = static_cast<int>(a.M - m0 < plan.tokens ? a.M - m0 : plan.tokens);
         const int cols = tokens * parts;
@@ -317,38 +345,41 @@ __global__ void __launch_bounds__(kThreads, 2)
         };
         for (int d = 0; d < plan.slots; ++d) load();
 
-        // x of a slice of this CTA's K, zero up to the end of its last tile; kXAhead
-        // loads of a thread in flight.
+        // x of a slice of this CTA's K, zero up to the end of its last tile: a bulk copy a
+        // row (16 x 8192 x 8192 17.2 -> 14.7 us against loads through registers).  Other
+        // types become bf16 from there.
         auto stage_x = [&](int slice) {
             const int log_size = a.xtype == TW_X_BF16 ? 1 : a.xtype == TW_X_F32 ? 2 : 0;
-            const int per_piece = 16 >> log_size;  // values
-            const int k0 = slice_at(slice) * kW4Inner;
-            const uint32_t row_pieces =
-                static_cast<uint32_t>((slice_at(slice + 1) - slice_at(slice)) * kW4Inner) /
-                per_piece;
-            // The thread's next piece: the at-th of token t.
-            uint32_t t = 0, at = threadIdx.x;
-            const auto count = static_cast<uint32_t>(tokens);
-            while (t < count) {
-                uint4 x[kXAhead];
-                uint32_t to[kXAhead];
-#pragma unroll
-                for (int i = 0; i < kXAhead; ++i, at += kThreads) {
-                    while (at >= row_pieces && t < count) {
-                        at -= row_pieces;
-                        ++t;
-                    }
-                    x[i] = make_uint4(0, 0, 0, 0);
-                    to[i] = t < count ? xs + t * parts * x_stride + at * per_piece * 2 : 0;
-                    const int64_t k = k0 + static_cast<int64_t>(at) * per_piece;
-                    if (t < count && k < K)
-                        x[i] = ld_global(static_cast<const char*>(a.x) +
-                                         (((m0 + t) * a.K + k) << log_size));
-                }
-#pragma unroll
-                for (int i = 0; i < kXAhead; ++i)
-                    if (to[i] != 0) store_x(x[i], a.xtype, to[i], x_stride);
+            const int k0 = slice_at(slice) * kW4Inner, k1 = slice_at(slice + 1) * kW4Inner;
+            const int own = (k1 < K ? k1 : K) - k0;
+            if (warp == 0) {
+                if (lane == 0) mbar_arrive_expect_tx(x_bar, tokens * own << log_size);
+                __syncwarp();
+                if (lane < tokens)
+                    bulk_copy(xs + (a.xtype == TW_X_BF16
+                                        ? lane * x_stride
+                                        : landing(lane, tokens, parts * x_stride,
+                                                  (k1 - k0) << log_size)),
+                              static_cast<const char*>(a.x) +
+                                  (((m0 + lane) * a.K + k0) << log_size),
+                              own << log_size, x_bar);
             }
+            if (!mbar_wait_slice(x_bar, x_phase, nullptr)) atomicOr(plan.status, 1u);
+            x_phase ^= 1u;
+            if (a.xtype == TW_X_BF16) {
+                for (int e = threadIdx.x; k1 > K && e < tokens * 16; e += kThreads)
+                    if (e % 16 * 8 < k1 - K)
+                        sts128(xs + e / 16 * x_stride + own * 2 + e % 16 * 16,
+                               make_uint4(0, 0, 0, 0));
+            } else if (a.xtype == TW_X_F32) {
+                widen_x<TW_X_F32>(xs, x_stride, tokens, k1 - k0, own);
+            } else if (a.xtype == TW_X_INT8) {
+                widen_x<TW_X_INT8>(xs, x_stride, tokens, k1 - k0, own);
+            } else {
+                widen_x<TW_X_E4M3>(xs, x_stride, tokens, k1 - k0, own);
+            }
+            // (Ordered before bulk copies of other tokens to the same place.)
+            fence_async_shared();
             __syncthreads();
         };
         if (slices == 1) stage_x(0);
@@ -496,6 +527,7 @@ template <bool INT4, int G>
 void* entry(int nt) {
     return nt == 1   ? reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 1, G>)
            : nt == 2 ? reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 2, G>)
+           : nt == 3 ? reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 3, G>)
                      : reinterpret_cast<void*>(&w4_gemm_kernel<INT4, 4, G>);
 }
 void* kernel_for(int wtype, int nt, int group) {
@@ -512,10 +544,11 @@ int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
     const int64_t sums = (static_cast<int64_t>(split) * p.slices << p.log_shares) *
                          ((p.pass + split - 1) / split) * columns * kRowStride * 4;
     const int64_t rings =
-        kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8);
+        kWarps * (p.slots * chunk_of(nt) * w4_tile_bytes(group) + kMaxSlots * 8) + 16;
     const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
-    return sums + rings + static_cast<int64_t>(columns) *
-                              (x_tiles(tiles, split, p.slices) * kW4Inner + kXPad) * 2;
+    const int64_t inner = x_tiles(tiles, split, p.slices) * kW4Inner;
+    const int64_t landing = p.a.xtype == TW_X_BF16 ? 0 : inner * (p.a.xtype == TW_X_F32 ? 4 : 1);
+    return sums + rings + columns * (inner + kXPad) * 2 + landing;
 }
 // What a CTA may use where two share an SM.
 int64_t half_smem(int smem_optin) { return (smem_optin - 1024) / 2; }
@@ -542,7 +575,7 @@ cudaLaunchConfig_t config(int grid, int split, size_t smem, bool pdl, void* stre
 
 int w4_gemm_prepare(int smem_optin, int (*clusters)[4]) {
     for (int wtype : {TW_INT4, TW_E2M1})
-        for (int nt = 1; nt <= 4; nt *= 2)
+        for (int nt = 1; nt <= 4; ++nt)
             for (int group = 32; group <= 128; group *= 2) {
                 cudaError_t e =
                     cudaFuncSetAttribute(kernel_for(wtype, nt, group),
@@ -570,23 +603,26 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     const int64_t stripes = (a.N + kW4Channels - 1) / kW4Channels;
     const int64_t tiles = (a.K + kW4Inner - 1) / kW4Inner;
     // Every cut that fits, by the time it takes in ns: a warp's tiles (more of them with
-    // two CTAs on an SM than with one) and pieces, each pass's barrier, of a cluster or not,
-    // staging x; eight CTAs in a cluster seldom find room.  Fitted to 356 cuts of 26 sizes
-    // (1 to 32 tokens, 300 to 32768 channels, K 256 to 8192): the cut taken is 3 % slower
-    // than the best on average, 19 % at most.  The most tokens at a time that fit; one
-    // token that does not fit the SMs of a budget goes in slices, staged for each pass.
-    constexpr int64_t kPiece = 770, kPass = 1200, kClusterPass = 1300, kStage = 160;
-    constexpr int64_t kSecondCta = 390, kClusterOf8 = 2500;
+    // two CTAs on an SM than with one) and pieces, each pass's barrier, x on its way into
+    // shared memory, and what a second CTA and a cluster cost once.  Fitted to 830 times
+    // of 31 sizes (1 to 32 tokens, 300 to 32768 channels, K 256 to 8192): the cut taken
+    // is 2 % slower than the best of them on average, 14 % at most.  The most tokens at a
+    // time that fit, even shares of them; one token that does not fit the SMs of a budget
+    // goes in slices, staged for each pass.
+    constexpr int64_t kTile2 = 365, kBlock2 = 222, kTile1 = 220, kBlock1 = 107;
+    constexpr int64_t kPiece = 780, kPass = 1440, kClusterPass = 930;
+    constexpr int64_t kSecondCta = 410, kCluster = 450, kClusterOf8 = 1200;
+    const int64_t stage_of = a.xtype == TW_X_BF16 ? 43 : 75;
     W4Plan best{}, plan{a, 0, 0, 0, 1, 0, 0, d.status};
     int64_t best_cost = -1, best_smem = 0, best_sets = 0;
     int nt = 0;
     auto choose = [&](int64_t tokens, int slices) {
         const int columns = static_cast<int>(tokens) * parts;
-        const int blocks = columns <= 8 ? 1 : columns <= 16 ? 2 : 4;
+        const int blocks = (columns + 7) / 8;
         plan.tokens = static_cast<int>(tokens);
         plan.slices = slices;
         for (int ctas = whole ? 2 : 1; ctas > 0; --ctas)
-            for (int i = 0; i < 4 && (1 << i) <= tiles; ++i) {
+            for (int i = 0; i < 4 && slices << i <= tiles; ++i) {  // a tile for each slice
                 int64_t sets = sms * ctas >> i;
                 const int64_t clusters = d.w4_clusters[ctas - 1][i];
                 if (i > 0 && sets > clusters) sets = clusters;
@@ -614,13 +650,15 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
                     const int64_t rounds =
                         ((own < plan.pass ? own : plan.pass) * shares + kWarps - 1) / kWarps;
                     const int64_t each = (inner + shares - 1) / shares;
-                    const int64_t tile = ctas == 2 ? 232 + 152 * (blocks - 1) : 156 + 98 * (blocks - 1);
-                    const int64_t stage = columns * inner * kStage / 16;
+                    const int64_t tile = ctas == 2 ? kTile2 + kBlock2 * (blocks - 1)
+                                                   : kTile1 + kBlock1 * (blocks - 1);
+                    const int64_t stage = columns * inner * stage_of / 16;
                     const int64_t cost =
                         passes * (slices * rounds * (each * tile + kPiece) + kPass +
                                   (i > 0 ? kClusterPass : 0)) +
                         (slices == 1 ? stage : stage * slices * passes) +
-                        (ctas == 2 ? kSecondCta : 0) + (i == 3 ? kClusterOf8 : 0);
+                        (ctas == 2 ? kSecondCta : 0) + (i > 0 ? kCluster : 0) +
+                        (i == 3 ? kClusterOf8 : 0);
                     if (best_cost >= 0 && cost >= best_cost) continue;
                     best_cost = cost;
                     best = plan;
@@ -633,8 +671,8 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
         return best_cost >= 0;
     };
     bool found = false;
-    for (int64_t tokens = a.M < kColumnsMax / parts ? a.M : kColumnsMax / parts;
-         tokens > 0 && !found; --tokens)
+    const int64_t most = kColumnsMax / parts, turns = (a.M + most - 1) / most;
+    for (int64_t tokens = (a.M + turns - 1) / turns; tokens > 0 && !found; --tokens)
         found = choose(tokens, 1);
     for (int slices = 2; !found && slices <= tiles; slices *= 2) found = choose(1, slices);
     if (!found) return static_cast<int>(cudaErrorInvalidConfiguration);
