@@ -380,8 +380,9 @@ int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int grou
  * group's products are exact and add up in fp32; the group's sum times its scale
  * adds up over the groups in fp32 too (fp32 x is cut into three bf16 terms,
  * without loss down to 2^-96 in magnitude).  The order of the sum depends on the
- * sizes and max_sms only.  Made for few tokens: from some 64 tokens on,
- * tw_dequantize_w4 and a library product are faster.
+ * sizes, the types and max_sms only.  Made for few tokens: tw_dequantize_w4 and a
+ * library product are faster from 33 tokens on where the weights in bf16 stay in the
+ * L2 cache, from 65 on where they do not.
  * Rules: T at most 2^31 - 512; x, packed and out 16-byte aligned, x_scale 4-byte
  * aligned; out overlaps no input. */
 int tw_gemm_w4(const void* x, const float* x_scale, const void* packed, void* out, int64_t T,

@@ -91,9 +91,13 @@ def two_chunk_layer_step_q8(x, x_scale, w, w_scale, partials, residual, weight, 
     gemm_stream.wait_stream(fused_stream)
 
 
-# From this many tokens on, reading 4-bit weights back and a library product are faster
-# than the product on 4 bits (8192 x 8192: see sandwich_layer_step_w4).
-W4_LIBRARY_TOKENS = 48
+def w4_library_tokens(channels, inner):
+    """From this many tokens on, reading 4-bit weights of [channels, inner] back and a
+    library product of their bfloat16 form are faster than the product on 4 bits: 33 where
+    that form stays in the L2 cache (4096 x 4096: 32 tokens 10.9 us against 15.1, 40 tokens
+    15.9 against 12.8), 65 where it does not (8192 x 8192: 48 tokens 37.7 us against 45.7,
+    64 tokens 47.4 against 45.7, 96 tokens 70 against 51)."""
+    return 33 if 2 * channels * inner < 1 << 27 else 65
 
 
 def sandwich_layer_step_w4(x, w, partials, residual, weight, out, residual_out, eps,
@@ -108,11 +112,11 @@ def sandwich_layer_step_w4(x, w, partials, residual, weight, out, residual_out, 
     ``out_scale`` is given.  ``x`` may be in 8 bits with ``x_scale``, as that form leaves
     rows.
 
-    ``workspace``, a [H, K] bfloat16 tensor, is for many tokens: from W4_LIBRARY_TOKENS
+    ``workspace``, a [H, K] bfloat16 tensor, is for many tokens: from w4_library_tokens(H, K)
     on a bfloat16 ``x`` (with bfloat16 partials) is multiplied by the weights read back
     into it, a plain library GEMM."""
     stream = torch.cuda.current_stream() if stream is None else stream
-    if (workspace is not None and x.shape[0] >= W4_LIBRARY_TOKENS
+    if (workspace is not None and x.shape[0] >= w4_library_tokens(*workspace.shape)
             and x.dtype == partials[0].dtype == torch.bfloat16):
         tw.tw_dequantize_w4(w, workspace, stream=stream)
         with torch.cuda.stream(stream):

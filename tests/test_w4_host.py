@@ -8,7 +8,7 @@ import torch
 
 from tests import w4_reference as ref
 from reduce_residual_rmsnorm_tw_gb300 import build as twbuild
-from reduce_residual_rmsnorm_tw_gb300 import tw
+from reduce_residual_rmsnorm_tw_gb300 import layer_step, tw
 
 OK, INVALID, ALIGN, ALIAS, UNSUP = 0, -1, -2, -3, -5
 BASE, MB = 0x7f0000000000, 1 << 20
@@ -149,3 +149,8 @@ def test_reference_rounds_middles_to_even_codes():
     assert np.array_equal(ref.quantise(w, 32, "int4")[0][0, :5], [7, 0, 2, 2, -4])
     w[0, :8] = [6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, -5]
     assert np.array_equal(ref.quantise(w, 32, "e2m1")[0][0, :8], [6, 0, 1, 1, 2, 2, 4, -4])
+
+
+def test_many_tokens_go_to_the_library():
+    assert layer_step.w4_library_tokens(4096, 4096) == 33
+    assert layer_step.w4_library_tokens(8192, 8192) == 65
