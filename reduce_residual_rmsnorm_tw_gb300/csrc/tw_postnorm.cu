@@ -9,7 +9,11 @@
 // stays in registers for both.  (One pass over sums of s^2, r^2, r v and v^2
 // would give mean x^2 too, but loses it to cancellation where the block's output
 // and the residual nearly cancel.)  Bound by HBM: n_parts + 1 rows (and a gate's) in,
-// n_out + 1 out.
+// n_out + 1 out.  These kernels serve few tokens (a cluster of eight CTAs to a token)
+// and short rows (a CTA or less to a row); many tokens with long rows stream through
+// a ring (tw_postnorm_rows.cu).  Few tokens are bound by their chain of latencies: the
+// launch, one load, two exchanges (8 x 1 x 8192 bf16 2.8 us, 64 tokens 4.7; the step
+// with one norm 2.5 and 4.1).
 #include "tw_tcgen05.cuh"
 
 namespace tw {

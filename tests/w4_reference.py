@@ -90,8 +90,9 @@ def product_bound(x, w, out, group, dtype, fp32_x):
     """Error allowed of out = x w^T (64-bit, scales included).  A group's products
     are exact; its sum is a chain of group / 16 matrix steps, each off by a rounding
     or truncation of the sum so far and by the alignment of its 16 terms (8 more of
-    them in all); groups, warps and the three terms of fp32 x are joined by fp32
-    additions (sixteen warps, eight CTAs); a scale multiplies; the result is rounded to dtype."""
+    them in all); groups, pieces of K (of a tile at least) and the three terms of fp32 x (the
+    small ones first) are joined by fp32 additions; a scale multiplies; the result is
+    rounded to dtype."""
     size = np.abs(x) @ np.abs(w).T * (1.01 if fp32_x else 1.0)
     tiles = -(-w.shape[1] // 128)
     adds = tiles * (128 // group) + 24 * (3 if fp32_x else 1) + 2
