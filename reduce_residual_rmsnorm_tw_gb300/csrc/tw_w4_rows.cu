@@ -6,9 +6,9 @@
 // of channel 2 i + l / 16 -- exactly one 32-bit word of the tile -- so a group's
 // maximum is a few shuffles and a channel's words are 64 contiguous bytes.
 // Bound by HBM: the rows in and half a byte per weight out, or the other way
-// round (8192 x 8192 bf16 to int4 31.9 us, 5.3 TB/s; back 27.0, 6.3 TB/s; 4090 x 5120 fp32
-// to e2m1 with groups of 32 19.0 and 15.8).  What keeps the first from it are the 11
-// instructions a weight takes: 65 % of the issue slots.
+// round (8192 x 8192 bf16 to int4 27.6 us, 6.1 TB/s, to e2m1 30.9; back 25.7, 6.6 TB/s;
+// 4090 x 5120 fp32 to e2m1 with groups of 32 16.7 and 15.2).  Quantising takes some ten
+// instructions a weight, for which loads in flight have to cover.
 #include "tw_device.cuh"
 
 namespace tw {
@@ -92,11 +92,51 @@ __device__ __forceinline__ float off_middle(float p, float v, float s) {
     return __uint_as_float(bits);
 }
 
+// Whether any of eight floats has zeros only in its last 16 bits, as middles have.
+__device__ __forceinline__ bool any_round(const float* q) {
+    uint32_t least = 0xffffffffu;  // two halves side by side
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        asm("min.u16x2 %0, %0, %1;"
+            : "+r"(least)
+            : "r"(__byte_perm(__float_as_uint(q[e]), __float_as_uint(q[e + 1]), 0x5410)));
+    return (least & 0xffffu) == 0 || least >> 16 == 0;
+}
+
+// Quotients of bf16 v, plus kGridBase: v times an approximate reciprocal, off by 2^-20 at
+// most, rounded to multiples of 2^-15.  A real quotient is a middle, which that gives
+// exactly, or 2^-14 of one away at least, which stays on its side.
+constexpr float kGridBase = 384.f;
+template <bool PLUS_BASE>
+__device__ __forceinline__ void grid_quotients(float* q, const float* v, float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+        asm("{\n\t.reg .b64 a, h, c;\n\t"
+            "mov.b64 a, {%2, %3};\n\t"
+            "mov.b64 h, {%4, %4};\n\t"
+            "mov.b64 c, {%5, %5};\n\t"
+            "fma.rn.f32x2 a, a, h, c;\n\t"
+            "mov.b64 {%0, %1}, a;\n\t}"
+            : "=f"(q[e]), "=f"(q[e + 1])
+            : "f"(v[e]), "f"(v[e + 1]), "f"(r), "f"(kGridBase));
+        if constexpr (!PLUS_BASE)
+            asm("{\n\t.reg .b64 a, c;\n\t"
+                "mov.b64 a, {%0, %1};\n\t"
+                "mov.b64 c, {%2, %2};\n\t"
+                "add.rn.f32x2 a, a, c;\n\t"
+                "mov.b64 {%0, %1}, a;\n\t}"
+                : "+f"(q[e]), "+f"(q[e + 1])
+                : "f"(-kGridBase));
+    }
+}
+
 // The word that holds eight codes (tw.h): q[0..7] quotients.  int4: 2^23 + 8 + q is
 // rounded to the nearest even integer and holds q + 8 in its last bits; a half's four
 // are put together by multiplying by 16 and adding, modulo 2^32 (of the rest, 0x4b000000,
 // nothing reaches the last 24 bits).
-__device__ __forceinline__ uint32_t word_int4(const float* q) {
+__device__ __forceinline__ uint32_t word_int4(const float* q, float base) {
     uint32_t half[2] = {0, 0};
 #pragma unroll
     for (int v = 3; v >= 0; --v) {
@@ -104,27 +144,29 @@ __device__ __forceinline__ uint32_t word_int4(const float* q) {
         asm("{\n\t.reg .b64 a, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
             "add.rn.f32x2 a, a, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
             : "=r"(b[0]), "=r"(b[1])
-            : "f"(q[2 * v]), "f"(q[2 * v + 1]), "f"(8388616.f));
+            : "f"(q[2 * v]), "f"(q[2 * v + 1]), "f"(8388616.f - base));
 #pragma unroll
         for (int h = 0; h < 2; ++h) half[h] = half[h] * 16u + b[h];
     }
     return __byte_perm(half[0], half[1], 0x5410);
 }
 __device__ __forceinline__ uint32_t word_e2m1(const float* q) {
-    uint32_t w;  // nibbles: values 0, 2, 4, 6 in the low half, 1, 3, 5, 7 in the high
+    uint32_t w;  // nibbles: values 6, 2, 4, 0 in the low half, 7, 3, 5, 1 in the high: the
+                 // order whose fields take the fewest shifts
     asm("{\n\t.reg .b8 a, b, c, d;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 a, %3, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 b, %7, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 c, %4, %2;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %6;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %3, %7;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %1, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %4, %8;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %2, %6;\n\t"
         "mov.b32 %0, {a, b, c, d};\n\t}"
         : "=r"(w)
         : "f"(q[0]), "f"(q[1]), "f"(q[2]), "f"(q[3]), "f"(q[4]), "f"(q[5]), "f"(q[6]),
           "f"(q[7]));
-    return (w & 0x00080008u) << 12 | (w & 0x00070007u) << 6 |    // 15, 8..6
-           (w & 0x00800080u) << 5 | (w & 0x00700070u) >> 1 |     // 12, 5..3
-           (w & 0x08000800u) << 3 | (w & 0x07000700u) << 1 |     // 14, 11..9
-           (w & 0x80008000u) >> 2 | (w & 0x70007000u) >> 12;     // 13, 2..0
+    return (w & 0x80078007u) |                                   // 15; 2..0
+           (w >> 6 & 0x01c001c0u) |                              // 8..6
+           (w >> 1 & 0x00380038u) | (w << 5 & 0x10001000u) |     // 5..3, 12
+           (w << 1 & 0x0e000e00u) | (w << 3 & 0x40004000u) |     // 11..9, 14
+           (w << 10 & 0x20002000u);                              // 13
 }
 
 // The eight values of a word.
@@ -173,70 +215,92 @@ struct Unit {
     }
 };
 
-// kDepth: steps (of two channels) whose loads are in flight at once.
-template <typename T, bool INT4, int G, int kDepth>
-__global__ void __launch_bounds__(kThreads)
+// Steps (of two channels) of a warp, whose loads are in flight at once, and CTAs on an SM
+// that find registers: bf16 a whole tile and four (three CTAs 31.2 us, 28.9; half a tile
+// 33), fp32 half a tile, the next CTA the other half, and five (a whole tile in two steps
+// 18.4, 17.0; four CTAs 17.0, 16.7).
+template <typename T>
+__host__ __device__ constexpr int depth_of() { return sizeof(T) == 2 ? 8 : 4; }
+
+template <typename T, bool INT4, int G>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 5)
     quantize_w4_kernel(const __grid_constant__ W4RowsArgs a) {
     constexpr int kTile = w4_tile_bytes(G);
-    grid_dependency_wait();
-    grid_launch_dependents();
+    constexpr int kDepth = depth_of<T>(), kParts = kW4Channels / 2 / kDepth;
     const int lane = threadIdx.x % 32, kk = lane % 16;
     const int K = static_cast<int>(a.K);
     const int tiles_k = (K + kW4Inner - 1) / kW4Inner;
     const int units_k = (tiles_k + kTilesPerUnit - 1) / kTilesPerUnit;
-    const int64_t units = (a.N + kW4Channels - 1) / kW4Channels * units_k;
+    const int64_t units = (a.N + kW4Channels - 1) / kW4Channels * units_k * kParts;
     const bool sectors = (reinterpret_cast<uintptr_t>(a.from) & 31) == 0;
+    // The first rows on their way into L2 while the launch before this one ends (a hint
+    // that reads nothing: what that launch writes is seen all the same).
+    if (threadIdx.x < 2 * kDepth) {
+        const Unit at(blockIdx.x / kParts, units_k);
+        const int64_t n =
+            at.stripe * kW4Channels + blockIdx.x % kParts * (2 * kDepth) + threadIdx.x;
+        const int k = at.tile * kW4Inner;
+        const int left = K - k < kTilesPerUnit * kW4Inner ? K - k : kTilesPerUnit * kW4Inner;
+        if (n < a.N)
+            bulk_prefetch_l2(static_cast<const T*>(a.from) + n * a.K + k,
+                             static_cast<uint32_t>(left * sizeof(T)));
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const Unit at(unit, units_k);
+        const Unit at(unit / kParts, units_k);
         if (at.tile >= tiles_k) continue;
+        const int i0 = static_cast<int>(unit % kParts) * kDepth;
         const int64_t n0 = at.stripe * kW4Channels;
         const int rows = a.N - n0 < kW4Channels ? static_cast<int>(a.N - n0) : kW4Channels;
         const int k = at.tile * kW4Inner + kk * 8;
         const T* from = static_cast<const T*>(a.from) + (n0 + lane / 16) * a.K + k;
         char* to = static_cast<char*>(a.to) + (at.stripe * tiles_k + at.tile) * kTile;
+        Eight<T> raw[kDepth];
 #pragma unroll
-        for (int i0 = 0; i0 < kW4Channels / 2; i0 += kDepth) {
-            Eight<T> raw[kDepth];
+        for (int i = 0; i < kDepth; ++i) {
+            if (2 * (i0 + i) + lane / 16 < rows && k < K)
+                raw[i].load(from + 2 * (i0 + i) * a.K, sectors);
+            else
+                raw[i].zero();
+        }
+        uint32_t most[kDepth];
 #pragma unroll
-            for (int i = 0; i < kDepth; ++i) {
-                if (2 * (i0 + i) + lane / 16 < rows && k < K)
-                    raw[i].load(from + 2 * (i0 + i) * a.K, sectors);
-                else
-                    raw[i].zero();
-            }
-            uint32_t most[kDepth];
+        for (int i = 0; i < kDepth; ++i) most[i] = __float_as_uint(raw[i].max_abs8());
+        // NaN above everything: the bits of non-negative floats are in order.
 #pragma unroll
-            for (int i = 0; i < kDepth; ++i) most[i] = __float_as_uint(raw[i].max_abs8());
-            // NaN above everything: the bits of non-negative floats are in order.
+        for (int o = 1; o < G / 8; o *= 2)
 #pragma unroll
-            for (int o = 1; o < G / 8; o *= 2)
+            for (int i = 0; i < kDepth; ++i)
+                most[i] = max(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
 #pragma unroll
-                for (int i = 0; i < kDepth; ++i)
-                    most[i] = max(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-#pragma unroll
-            for (int i = 0; i < kDepth; ++i) {
-                const int row = 2 * (i0 + i) + lane / 16;
-                const float m = __uint_as_float(most[i]);
-                const bool finite = quant_finite(m);
-                const bool zero = !finite || m < kQuantTiny;
-                const float s = group_scale<T, INT4>(zero ? 1.f : m);
+        for (int i = 0; i < kDepth; ++i) {
+            const int row = 2 * (i0 + i) + lane / 16;
+            const float m = __uint_as_float(most[i]);
+            const bool finite = quant_finite(m);
+            const bool zero = !finite || m < kQuantTiny;
+            const float s = group_scale<T, INT4>(zero ? 1.f : m);
+            float f[8], q[8];
+            raw[i].to_float(f);
+            constexpr bool kGrid = sizeof(T) == 2;
+            if constexpr (kGrid) {
+                grid_quotients<INT4>(q, f, s);
+            } else {
                 const RowExact by(s, 1.f);
-                float f[8], q[8];
-                raw[i].to_float(f);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) by.quotients(q + e, f + e);
-                if constexpr (sizeof(T) == 4) {
+                if (any_round(q)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) q[e] = off_middle(q[e], f[e], s);
                 }
-                uint32_t word = INT4 ? word_int4(q) : word_e2m1(q);
-                if (zero) word = INT4 ? 0x88888888u : 0u;
-                *reinterpret_cast<uint32_t*>(to + word_at(row, kk)) = word;
-                if (kk % (G / 8) == 0) {
-                    const float held = !finite ? __uint_as_float(0x7fff0000u) : zero ? 0.f : s;
-                    *reinterpret_cast<uint16_t*>(to + scale_at<G>(row, kk)) =
-                        static_cast<uint16_t>(__float_as_uint(held) >> 16);
-                }
+            }
+            uint32_t word = INT4 ? word_int4(q, kGrid ? kGridBase : 0.f) : word_e2m1(q);
+            if (zero) word = INT4 ? 0x88888888u : 0u;
+            *reinterpret_cast<uint32_t*>(to + word_at(row, kk)) = word;
+            if (kk % (G / 8) == 0) {
+                const float held = !finite ? __uint_as_float(0x7fff0000u) : zero ? 0.f : s;
+                *reinterpret_cast<uint16_t*>(to + scale_at<G>(row, kk)) =
+                    static_cast<uint16_t>(__float_as_uint(held) >> 16);
             }
         }
     }
@@ -246,14 +310,20 @@ template <typename T, bool INT4, int G>
 __global__ void __launch_bounds__(kThreads)
     dequantize_w4_kernel(const __grid_constant__ W4RowsArgs a) {
     constexpr int kTile = w4_tile_bytes(G), kSteps = kW4Channels / 2;
-    grid_dependency_wait();
-    grid_launch_dependents();
     const int lane = threadIdx.x % 32, kk = lane % 16;
     const int K = static_cast<int>(a.K);
     const int tiles_k = (K + kW4Inner - 1) / kW4Inner;
     const int units_k = (tiles_k + kTilesPerUnit - 1) / kTilesPerUnit;
     const int64_t units = (a.N + kW4Channels - 1) / kW4Channels * units_k;
     const bool sectors = (reinterpret_cast<uintptr_t>(a.to) & 31) == 0;
+    if (threadIdx.x == 0) {  // as above
+        const Unit at(blockIdx.x, units_k);
+        const int left = tiles_k - at.tile < kTilesPerUnit ? tiles_k - at.tile : kTilesPerUnit;
+        bulk_prefetch_l2(static_cast<const char*>(a.from) + (at.stripe * tiles_k + at.tile) * kTile,
+                         static_cast<uint32_t>(left * kTile));
+    }
+    grid_dependency_wait();
+    grid_launch_dependents();
     for (int64_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
         const Unit at(unit, units_k);
         if (at.tile >= tiles_k) continue;
@@ -299,7 +369,7 @@ __global__ void __launch_bounds__(kThreads)
 template <typename T, bool INT4, int G>
 void* entry(bool quantize) {
     return quantize
-               ? reinterpret_cast<void*>(&quantize_w4_kernel<T, INT4, G, sizeof(T) == 2 ? 8 : 4>)
+               ? reinterpret_cast<void*>(&quantize_w4_kernel<T, INT4, G>)
                : reinterpret_cast<void*>(&dequantize_w4_kernel<T, INT4, G>);
 }
 template <typename T, bool INT4>
@@ -321,8 +391,11 @@ void* kernel_for(const W4RowsArgs& a, bool quantize) {
 // us against 51.1), fewer that loop, each alone on its SM, under a budget.
 int launch(const W4RowsArgs& a, bool quantize, int max_sms, int sm_count, void* stream) {
     const int64_t tiles_k = (a.K + kW4Inner - 1) / kW4Inner;
+    const int parts = !quantize ? 1 : kW4Channels / 2 /
+                                          (a.dtype == TW_BF16 ? depth_of<__nv_bfloat16>()
+                                                              : depth_of<float>());
     const int64_t units = (a.N + kW4Channels - 1) / kW4Channels *
-                          ((tiles_k + kTilesPerUnit - 1) / kTilesPerUnit);
+                          ((tiles_k + kTilesPerUnit - 1) / kTilesPerUnit) * parts;
     const bool whole = max_sms >= sm_count;
     const int64_t most = whole ? (int64_t{1} << 31) - 1 : max_sms;
     return launch_with_pdl(kernel_for(a, quantize), a, static_cast<int>(units < most ? units : most),
