@@ -294,15 +294,16 @@ void rows_shape(int64_t nvec, int* vpt, int* w) {
 }
 
 // Which kernel (us, 8 partials bf16: cluster / this file's rows / ring):
-//   rows to 8 KB   up to kRowsTokens tokens per SM this file's, a CTA or less per row,
-//                  two vectors a thread (64 x 4096 4.3 / 4.1 / 4.9, 200 x 4096 8.7 / 5.3
-//                  / 6.4, 2 x 400 x 4096 - / 6.3 / 6.0); rows below 4 KB always (2 x 4096
-//                  x 1024 - / 11.7 / 12.9)
+//   rows to 8 KB   few tokens per SM this file's, a CTA or less per row, two vectors a
+//                  thread: up to two (64 x 4096 4.3 / 4.1 / 4.9, 250 x 4096 - / 5.9 / 7.0,
+//                  2 x 400 x 4096 - / 6.2 / 5.9), with 4 KB up to four (600 x 2048 - / 7.0 /
+//                  6.9, 400 x 2048 - / 5.2 / 6.4); rows below 4 KB always (1000 x 256 - / 2.5 /
+//                  7.5, 2 x 1000 x 1024 - / 3.6 / 5.4; 2 x 4096 x 1024 - / 11.9 / 10.7)
 //   longer rows    a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
 //                  / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
 //   everything else the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9)
 constexpr int64_t kShortRowBytes = 4096, kRowsRowBytes = 8192;
-constexpr int64_t kRowsTokens = 2;
+int64_t rows_tokens(int64_t row_bytes) { return row_bytes <= kShortRowBytes ? 4 : 2; }
 
 cudaLaunchConfig_t cluster_config(int cluster, int64_t tokens, size_t smem, bool pdl, void* stream,
                                   cudaLaunchAttribute (&attr)[2]) {
@@ -376,7 +377,7 @@ int launch_postnorm(const PostParams& pp, int dtype, int max_sms, const PostDevi
         }
     }
     if (p.row_bytes >= kShortRowBytes &&
-        (p.row_bytes > kRowsRowBytes || tokens > kRowsTokens * sms))
+        (p.row_bytes > kRowsRowBytes || tokens > rows_tokens(p.row_bytes) * sms))
         return launch_postnorm_rows(pp, dtype, static_cast<int>(sms), whole, d.smem_optin, stream);
     int vpt = 0, w = 0;
     rows_shape(nvec, &vpt, &w);

@@ -5,15 +5,14 @@
 // x = residual_scale * residual + block_scale * gate * u; residual_out = x;
 // out[k] = x / rms(x) * weight.
 //
-// A CTA, alone on its SM, is two pipelines of eight warps, each with a producer
-// warp and half of the ring (rows above 24 KB: one of sixteen, whose ring holds
-// more of them).  A ring slot holds one row: a token's partials come
+// A CTA, alone on its SM, is one to eight pipelines that share sixteen warps, each with a
+// producer warp and its part of the ring (pipelines_for, below).  A ring slot holds one row: a token's partials come
 // first and are added up and handed back one by one, its residual and gate last;
 // those stay in their slots while the sum's square is reduced, so that registers
 // hold one row in fp32 only; the two weights lie in shared memory (in registers they
 // spilled: 8 x 1024 x 8192 36.8 us against 28.9).  Each of the two reductions is a
-// warp sum and one barrier of the pipeline; while one pipeline waits there the other
-// streams.  A gate that tokens share is copied for each of them: out of L2.
+// warp sum and one barrier of the pipeline; while one pipeline waits there the others
+// stream.  A gate that tokens share is copied for each of them: out of L2.
 // Bound by HBM: n_parts + 1 rows (and a gate's) in, n_out + 1 out (8 x 1024 x 8192 bf16
 // 29.0 us, 6.4 TB/s; 4 x 1111 x 5120 fp32 with a gate and two outputs 28.4; 2 x 2048 x
 // 4096 with a gate per token 17.4, 5.8 TB/s: 13 rows a CTA, the last of them alone).
@@ -24,16 +23,17 @@ namespace {
 
 constexpr int kWarps = 16;     // of all pipelines, without the producers
 constexpr int kMaxSlots = 16;  // of a pipeline
+constexpr int kMaxPipes = 8;
 __host__ __device__ constexpr int block_of(int pipes) { return 32 * (kWarps + pipes); }
 
 struct Header {
-    uint64_t full[2][kMaxSlots], empty[2][kMaxSlots];  // of each pipeline
+    uint64_t full[kMaxPipes][kMaxSlots], empty[kMaxPipes][kMaxSlots];  // of each pipeline
     // Warp totals: [reduction][buffer][warp].
     float sums[2][2][kWarps];
     float most[2][kWarps];
     int abort;
 };
-constexpr int kHeaderBytes = 1536;
+constexpr int kHeaderBytes = 2560;
 static_assert(sizeof(Header) <= kHeaderBytes, "header too large");
 
 struct RingPos {
@@ -50,9 +50,6 @@ __device__ __forceinline__ void gave_up(const Params& p, volatile int* abort) {
     *abort = 1;
     atomicOr(p.status, 1u);
 }
-
-// Pipelines for rows of this size.
-constexpr int64_t kOnePipeBytes = 24 * 1024;
 
 // NV: 16-byte vectors of a row per thread.
 template <typename T, int NV, int kPipes, bool Q8>
@@ -156,7 +153,7 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
             *reinterpret_cast<uint4*>(weights + v * 16) =
                 ld_global_nc(static_cast<const char*>(from) + (v < nvec ? v : v - nvec) * 16);
     }
-    named_barrier(3, 32 * kWarps);
+    named_barrier(1 + kMaxPipes, 32 * kWarps);
     RingPos pos;
     bool alive = true;
     int buf = 0;
@@ -276,11 +273,35 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
     }
 }
 
+// Pipelines for rows of this size.  More of them hide each other's barriers, where the
+// ring still holds rows enough for each and there are tokens for all:
+//   rows above 24 KB   one, whose ring holds more of them
+//   rows to 5 KB       eight, with more than four tokens to an SM (8 x 2048 x 2048 bf16 with
+//                      two, four and eight 25.0, 16.9 and 16.2 us; 600 tokens fp32 7.3, 5.5 and 5.9)
+//   rows to 8 KB       four, unless their last round is emptier than two's by more than
+//                      they gain, the more the shorter the row (8 x 700 x 3000 12.4 -> 11.0,
+//                      2 x 4096 x 4096 30.0 -> 27.3, but 2 x 2048 x 4096 16.0 -> 16.3)
+//   others             two (fp32 rows of 10 KB, four: 15.0 -> 16.0)
+int pipelines_for(int64_t row_bytes, int64_t tokens, int64_t sms) {
+    auto rounds = [&](int pipes) { return (tokens + pipes * sms - 1) / (pipes * sms) * pipes; };
+    if (row_bytes > 24 * 1024) return 1;
+    if (row_bytes <= 5 * 1024 && tokens > 4 * sms) return 8;
+    return row_bytes <= 8 * 1024 && rounds(4) * row_bytes < rounds(2) * 9 * 1024 ? 4 : 2;
+}
+
 template <typename T, bool Q8>
 void* entry(int nv, int pipes) {
     if (pipes == 1) return reinterpret_cast<void*>(&postnorm_rows_kernel<T, 4, 1, Q8>);
+    // (Rows of 4 KB at least: two vectors a thread and more.)
+    if (pipes == 8)
+        return nv <= 4 ? reinterpret_cast<void*>(&postnorm_rows_kernel<T, 4, 8, Q8>)
+                       : reinterpret_cast<void*>(&postnorm_rows_kernel<T, 5, 8, Q8>);
+    if (pipes == 4)
+        return nv <= 2   ? reinterpret_cast<void*>(&postnorm_rows_kernel<T, 2, 4, Q8>)
+               : nv == 3 ? reinterpret_cast<void*>(&postnorm_rows_kernel<T, 3, 4, Q8>)
+                         : reinterpret_cast<void*>(&postnorm_rows_kernel<T, 4, 4, Q8>);
     switch (nv) {
-        case 1: return reinterpret_cast<void*>(&postnorm_rows_kernel<T, 1, 2, Q8>);
+        case 1:
         case 2: return reinterpret_cast<void*>(&postnorm_rows_kernel<T, 2, 2, Q8>);
         case 3: return reinterpret_cast<void*>(&postnorm_rows_kernel<T, 3, 2, Q8>);
         case 4: return reinterpret_cast<void*>(&postnorm_rows_kernel<T, 4, 2, Q8>);
@@ -299,7 +320,7 @@ void* kernel_for(int dtype, int nv, int pipes, bool q8) {
 int postnorm_rows_prepare(int smem_optin) {
     for (int dt = 0; dt < 2; ++dt)
         for (int nv = 1; nv <= 6; ++nv)
-            for (int pipes = 1; pipes <= 2; ++pipes)
+            for (int pipes = 1; pipes <= 8; pipes *= 2)
                 for (bool q8 : {false, true}) {
                     cudaError_t e = cudaFuncSetAttribute(
                         kernel_for(dt, nv, pipes, q8), cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -312,14 +333,14 @@ int postnorm_rows_prepare(int smem_optin) {
 int launch_postnorm_rows(const PostParams& pp, int dtype, int sms, bool whole, int smem_optin,
                          void* stream) {
     const Params& p = pp.p;
-    const int pipes = p.row_bytes > kOnePipeBytes ? 1 : 2;
+    const int64_t tokens = p.t1 - p.t0;
+    const int pipes = pipelines_for(p.row_bytes, tokens, sms);
     const int threads = 32 * kWarps / pipes;
     const int nv = static_cast<int>((p.row_bytes / 16 + threads - 1) / threads);
     const int64_t held = kHeaderBytes + 2 * p.row_bytes;
     int slots = static_cast<int>((smem_optin - held) / (pipes * p.row_bytes));
     if (slots > kMaxSlots) slots = kMaxSlots;
     if (slots < 2) return static_cast<int>(cudaErrorInvalidConfiguration);
-    const int64_t tokens = p.t1 - p.t0;
     size_t smem = static_cast<size_t>(held + pipes * slots * p.row_bytes);
     if (smem < kExclusiveSmemBytes) smem = kExclusiveSmemBytes;
     cudaLaunchConfig_t cfg = {};

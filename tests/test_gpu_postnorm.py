@@ -110,6 +110,20 @@ def test_budgets(T, H, dtype, max_sms):
     check(2, T, H, dtype, gate_tokens=1, max_sms=max_sms)
 
 
+@pytest.mark.parametrize("quant", [None, "int8"])
+@pytest.mark.parametrize("n_parts,T,H,dtype,max_sms", [
+    (8, 640, 2048, "bf16", None), (3, 641, 2496, "bf16", None), (2, 700, 1284, "f32", None),
+    (16, 41, 2560, "bf16", 8), (1, 37, 1024, "f32", 7), (5, 40, 2568, "bf16", 8),
+    (4, 420, 2888, "bf16", None), (2, 2500, 4096, "bf16", None), (3, 14, 1900, "f32", 2),
+    (2, 700, 4096, "bf16", None), (9, 330, 5000, "bf16", None), (2, 320, 12288, "bf16", None),
+    (6, 7, 12296, "bf16", 1)])
+def test_rows_through_the_ring(n_parts, T, H, dtype, max_sms, quant):
+    """Rows around the sizes at which a ring's pipelines change, few and many to a CTA."""
+    for in_place in (False, True):
+        check(n_parts, T, H, dtype, gate_tokens=3 if T % 2 else None, max_sms=max_sms, quant=quant,
+              in_place=in_place, t0=1, t1=T - 1, n_out=2, block_scale=0.5)
+
+
 @pytest.mark.parametrize("quant", [None, "e4m3"])
 @pytest.mark.parametrize("T,t0,t1", [(9, 4, 7), (9, 0, 1), (9, 8, 9), (500, 3, 499), (9, 5, 5)])
 def test_ranges_and_in_place(T, t0, t1, quant):
