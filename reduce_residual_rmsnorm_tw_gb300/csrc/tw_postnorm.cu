@@ -42,18 +42,22 @@ __device__ __forceinline__ void st_peer_f32(float* local, uint32_t rank, float v
                  : "memory");
 }
 
+// MANY: CTAs come after each other on the SMs, so four of them share one (64 registers):
+// fewer partials in flight a thread, the weights read when they are needed (2 x 4096 x
+// 1024 11.9 -> 9.4 us, 8 x 2048 x 1024 10.7 -> 8.9, 2 x 16000 x 256 11.0 -> 9.6; where all CTAs
+// run at once 2 x 1000 x 1024 3.6 -> 4.2).  Three of them, or half the loads in five: slower.
 // VPT: 16-byte vectors of the row per thread; W: warps per row (of a CTA, where a
 // cluster of CTAs shares the row: CL).
-template <typename T, int VPT, int W, bool CL, bool Q8>
-__global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
+template <typename T, int VPT, int W, bool CL, bool Q8, bool MANY = false>
+__global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? 4 : 0)
     postnorm_kernel(const __grid_constant__ PostParams pp) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
     constexpr int kWarps = (CL ? kClusterCta : kThreads) / 32;
     constexpr int kRows = kWarps / W;
     // Rows of partials whose loads are in flight at once.
-    constexpr int kAhead = VPT >= 8 ? 1 : 8 / VPT;
-    constexpr bool kEarly = VPT <= 2;
+    constexpr int kAhead = (MANY ? 4 : 8) / VPT;
+    constexpr bool kEarly = VPT <= 2 && !MANY;
     const Params& p = pp.p;
     // Warp totals: [second reduction][buffer][warp], of sums and of maxima.
     __shared__ float warp_part[2][2][kWarps];
@@ -251,7 +255,12 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads)
 }
 
 template <typename T, bool Q8>
-void* postnorm_rows_entry(int vpt, int w) {
+void* postnorm_rows_entry(int vpt, int w, bool many) {
+    if (many)  // rows below 4 KB
+        return w == 4     ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, false, Q8, true>)
+               : w == 2   ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 2, false, Q8, true>)
+               : vpt == 2 ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 1, false, Q8, true>)
+                          : reinterpret_cast<void*>(&postnorm_kernel<T, 1, 1, false, Q8, true>);
     switch (w * 16 + vpt) {
         case 1 * 16 + 1: return reinterpret_cast<void*>(&postnorm_kernel<T, 1, 1, false, Q8>);
         case 1 * 16 + 2: return reinterpret_cast<void*>(&postnorm_kernel<T, 2, 1, false, Q8>);
@@ -272,18 +281,20 @@ void* postnorm_cluster_entry(int vpt) {
     }
 }
 
-// The instantiation for vpt vectors per thread and w warps per row (0: a cluster).
-void* postnorm_kernel_for(int dtype, int vpt, int w, bool q8) {
+// The instantiation for vpt vectors per thread and w warps per row (0: a cluster), many
+// rows or few.
+void* postnorm_kernel_for(int dtype, int vpt, int w, bool q8, bool many = false) {
     if (dtype == TW_BF16) {
         using T = __nv_bfloat16;
         if (w == 0) return q8 ? postnorm_cluster_entry<T, true>(vpt)
                               : postnorm_cluster_entry<T, false>(vpt);
-        return q8 ? postnorm_rows_entry<T, true>(vpt, w) : postnorm_rows_entry<T, false>(vpt, w);
+        return q8 ? postnorm_rows_entry<T, true>(vpt, w, many)
+                  : postnorm_rows_entry<T, false>(vpt, w, many);
     }
     if (w == 0) return q8 ? postnorm_cluster_entry<float, true>(vpt)
                           : postnorm_cluster_entry<float, false>(vpt);
-    return q8 ? postnorm_rows_entry<float, true>(vpt, w)
-              : postnorm_rows_entry<float, false>(vpt, w);
+    return q8 ? postnorm_rows_entry<float, true>(vpt, w, many)
+              : postnorm_rows_entry<float, false>(vpt, w, many);
 }
 
 // Warps per row and vectors per thread for rows of nvec <= 512 vectors.
@@ -298,7 +309,7 @@ void rows_shape(int64_t nvec, int* vpt, int* w) {
 //                  thread: up to two (64 x 4096 4.3 / 4.1 / 4.9, 250 x 4096 - / 5.9 / 7.0,
 //                  2 x 400 x 4096 - / 6.2 / 5.9), with 4 KB up to four (600 x 2048 - / 7.0 /
 //                  6.9, 400 x 2048 - / 5.2 / 6.4); rows below 4 KB always (1000 x 256 - / 2.5 /
-//                  7.5, 2 x 1000 x 1024 - / 3.6 / 5.4; 2 x 4096 x 1024 - / 11.9 / 10.7)
+//                  7.5, 2 x 1000 x 1024 - / 3.6 / 5.4, 2 x 4096 x 1024 - / 9.4 / 10.7)
 //   longer rows    a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
 //                  / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
 //   everything else the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9)
@@ -384,7 +395,9 @@ int launch_postnorm(const PostParams& pp, int dtype, int max_sms, const PostDevi
     const int64_t rows = kThreads / 32 / w;
     const int64_t ctas = (tokens + rows - 1) / rows;
     const int64_t most = whole ? (int64_t{1} << 31) - 1 : sms;
-    return launch_with_pdl(postnorm_kernel_for(dtype, vpt, w, p.q8 != 0), pp,
+    // More CTAs than run at once (two on an SM), which leaves W < 8 only: longer rows are few.
+    const bool many = whole && w < 8 && ctas > 2 * sms;
+    return launch_with_pdl(postnorm_kernel_for(dtype, vpt, w, p.q8 != 0, many), pp,
                            static_cast<int>(ctas < most ? ctas : most), kThreads, smem, whole,
                            stream);
 }

@@ -6,8 +6,9 @@
 // out[k] = x / rms(x) * weight.
 //
 // A CTA, alone on its SM, is one to eight pipelines that share sixteen warps, each with a
-// producer warp and its part of the ring (pipelines_for, below).  A ring slot holds one row: a token's partials come
-// first and are added up and handed back one by one, its residual and gate last;
+// producer warp and its part of the ring (pipelines_for, below).  A ring slot holds one
+// row: a token's partials come first and are added up and handed back one by one, its
+// residual and gate last;
 // those stay in their slots while the sum's square is reduced, so that registers
 // hold one row in fp32 only; the two weights lie in shared memory (in registers they
 // spilled: 8 x 1024 x 8192 36.8 us against 28.9).  Each of the two reductions is a
@@ -107,7 +108,8 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
         for (int64_t t = first; t < p.t1 && !stop; t += step)
             for (int r = 0; r < rows; ++r, ++issued, pos.next(n_slots)) {
                 const uint32_t s = pos.slot;
-                if (*abort || (issued >= n_slots && !mbar_wait(empty + 8 * s, pos.phase ^ 1u, abort))) {
+                if (*abort ||
+                    (issued >= n_slots && !mbar_wait(empty + 8 * s, pos.phase ^ 1u, abort))) {
                     gave_up(p, abort);
                     stop = true;
                     break;
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
             for (int e = 0; e < E; ++e) x[k][e] = 0.f;
         for (int r = 0; r < p.n_parts; ++r, pos.next(n_slots)) {
             wait_full(pos);
-            const unsigned char* row = rows_at + (pipe * n_slots + pos.slot) * row_bytes + gtid * 16;
+            const unsigned char* row =
+                rows_at + (pipe * n_slots + pos.slot) * row_bytes + gtid * 16;
 #pragma unroll
             for (int k = 0; k < NV; ++k)
                 if (gtid + k * kPipeThreads < nvec)
@@ -277,7 +280,8 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
 // ring still holds rows enough for each and there are tokens for all:
 //   rows above 24 KB   one, whose ring holds more of them
 //   rows to 5 KB       eight, with more than four tokens to an SM (8 x 2048 x 2048 bf16 with
-//                      two, four and eight 25.0, 16.9 and 16.2 us; 600 tokens fp32 7.3, 5.5 and 5.9)
+//                      two, four and eight 25.0, 16.9 and 16.2 us; 5 x 600 x 1024 fp32 7.3,
+//                      5.5 and 5.9)
 //   rows to 8 KB       four, unless their last round is emptier than two's by more than
 //                      they gain, the more the shorter the row (8 x 700 x 3000 12.4 -> 11.0,
 //                      2 x 4096 x 4096 30.0 -> 27.3, but 2 x 2048 x 4096 16.0 -> 16.3)

@@ -124,9 +124,9 @@ constexpr float kInt8Factor = 128.f;
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.u32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
-// Sixteen bytes of x (4 fp32 or 16 8-bit values) as bf16 to `to` and, fp32, as three terms that add up to them to three rows `stride`
-// apart: the leading eight bits, cut off, then the next eight, then the rest; an
-// infinity or a NaN as its own first term.
+// Sixteen bytes of x (4 fp32 or 16 8-bit values) as bf16 to `to` and, fp32, as three terms
+// that add up to them to three rows `stride` apart: the leading eight bits, cut off, then
+// the next eight, then the rest; an infinity or a NaN as its own first term.
 template <int XTYPE>
 __device__ __forceinline__ void store_x(const uint4& x, uint32_t to, int stride) {
     const uint32_t word[4] = {x.x, x.y, x.z, x.w};
@@ -263,7 +263,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int log_shares = plan.log_shares, shares = 1 << log_shares, slices = plan.slices;
     const int rank = split > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
     const int lo = tiles_k * rank >> log_split, hi = tiles_k * (rank + 1) >> log_split;
-    auto slice_at = [&](int s) { return slices == 1 ? (s ? hi : lo) : lo + (hi - lo) * s / slices; };
+    auto slice_at = [&](int s) {
+        return slices == 1 ? (s ? hi : lo) : lo + (hi - lo) * s / slices;
+    };
     const int64_t sets = gridDim.x >> log_split, set = blockIdx.x >> log_split;
     const int first = static_cast<int>(stripes * set / sets);
     const int end = static_cast<int>(stripes * (set + 1) / sets);
@@ -495,7 +497,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int pieces = (split * slices) << log_shares;
             const int mine = ((items >> log_shares) - rank + split - 1) >> log_split;  // stripes
             const int apart = owned * columns * kRowStride;
-            const float factor = (INT4 ? kInt4Factor : 1.f) * (a.xtype == TW_X_INT8 ? kInt8Factor : 1.f);
+            const float factor =
+                (INT4 ? kInt4Factor : 1.f) * (a.xtype == TW_X_INT8 ? kInt8Factor : 1.f);
             for (int e = threadIdx.x; e < mine * tokens * kW4Channels; e += kThreads) {
                 const int ch = e % kW4Channels, rest = e / kW4Channels;
                 const int i = tokens == 1 ? rest : rest / tokens, t = rest - i * tokens;
@@ -591,9 +594,9 @@ int w4_gemm_prepare(int smem_optin, int (*clusters)[4]) {
     for (int ctas = 1; ctas <= 2; ++ctas)
         for (int i = 0; i < 4; ++i) {
             cudaLaunchAttribute attr[2];
+            const int64_t smem = ctas == 1 ? smem_optin : half_smem(smem_optin);
             const cudaLaunchConfig_t cfg =
-                config(1 << i, 1 << i, static_cast<size_t>(ctas == 1 ? smem_optin : half_smem(smem_optin)),
-                       false, nullptr, attr);
+                config(1 << i, 1 << i, static_cast<size_t>(smem), false, nullptr, attr);
             cudaError_t e = cudaOccupancyMaxActiveClusters(&clusters[ctas - 1][i],
                                                            kernel_for(TW_INT4, 1, 128), &cfg);
             if (e != cudaSuccess) return static_cast<int>(e);

@@ -330,7 +330,8 @@ __global__ void __launch_bounds__(kThreads)
         const int64_t n0 = at.stripe * kW4Channels;
         const int rows = a.N - n0 < kW4Channels ? static_cast<int>(a.N - n0) : kW4Channels;
         const int k = at.tile * kW4Inner + kk * 8;
-        const char* from = static_cast<const char*>(a.from) + (at.stripe * tiles_k + at.tile) * kTile;
+        const char* from =
+            static_cast<const char*>(a.from) + (at.stripe * tiles_k + at.tile) * kTile;
         T* to = static_cast<T*>(a.to) + (n0 + lane / 16) * a.K + k;
         uint32_t word[kSteps];
         uint16_t scale[kSteps];
@@ -398,8 +399,9 @@ int launch(const W4RowsArgs& a, bool quantize, int max_sms, int sm_count, void* 
                           ((tiles_k + kTilesPerUnit - 1) / kTilesPerUnit) * parts;
     const bool whole = max_sms >= sm_count;
     const int64_t most = whole ? (int64_t{1} << 31) - 1 : max_sms;
-    return launch_with_pdl(kernel_for(a, quantize), a, static_cast<int>(units < most ? units : most),
-                           kThreads, whole ? 0 : kExclusiveSmemBytes, whole, stream);
+    return launch_with_pdl(kernel_for(a, quantize), a,
+                           static_cast<int>(units < most ? units : most), kThreads,
+                           whole ? 0 : kExclusiveSmemBytes, whole, stream);
 }
 
 }  // namespace

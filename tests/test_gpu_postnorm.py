@@ -125,6 +125,15 @@ def test_rows_through_the_ring(n_parts, T, H, dtype, max_sms, quant):
 
 
 @pytest.mark.parametrize("quant", [None, "e4m3"])
+@pytest.mark.parametrize("n_parts,T,H,dtype", [
+    (3, 2600, 248, "bf16"), (8, 2500, 512, "bf16"), (2, 1300, 1016, "bf16"), (5, 700, 1992, "bf16"),
+    (1, 2450, 100, "f32"), (9, 1300, 508, "f32"), (4, 620, 1020, "f32")])
+def test_more_short_rows_than_run_at_once(n_parts, T, H, dtype, quant):
+    check(n_parts, T, H, dtype, post=T % 4 != 0, gate_tokens=7, quant=quant, in_place=True,
+          t0=2, t1=T - 1, residual_scale=0.5)
+
+
+@pytest.mark.parametrize("quant", [None, "e4m3"])
 @pytest.mark.parametrize("T,t0,t1", [(9, 4, 7), (9, 0, 1), (9, 8, 9), (500, 3, 499), (9, 5, 5)])
 def test_ranges_and_in_place(T, t0, t1, quant):
     for in_place in (False, True):
