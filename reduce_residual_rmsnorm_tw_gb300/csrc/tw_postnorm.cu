@@ -42,21 +42,22 @@ __device__ __forceinline__ void st_peer_f32(float* local, uint32_t rank, float v
                  : "memory");
 }
 
-// MANY: CTAs come after each other on the SMs, so four of them share one (64 registers):
-// fewer partials in flight a thread, the weights read when they are needed (2 x 4096 x
-// 1024 11.9 -> 9.4 us, 8 x 2048 x 1024 10.7 -> 8.9, 2 x 16000 x 256 11.0 -> 9.6; where all CTAs
-// run at once 2 x 1000 x 1024 3.6 -> 4.2).  Three of them, or half the loads in five: slower.
+// MANY: three or four CTAs share an SM: fewer partials in flight a thread, the weights read
+// when they are needed (2 x 4096 x 1024 11.9 -> 9.4 us, 8 x 2048 x 1024 10.7 -> 8.9, 2 x
+// 16000 x 256 11.0 -> 9.6; but where two on an SM are enough 2 x 1000 x 1024 3.6 -> 4.2).
+__host__ __device__ constexpr int many_ctas(int vpt) { return vpt == 3 ? 3 : 4; }
+
 // VPT: 16-byte vectors of the row per thread; W: warps per row (of a CTA, where a
 // cluster of CTAs shares the row: CL).
 template <typename T, int VPT, int W, bool CL, bool Q8, bool MANY = false>
-__global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? 4 : 0)
+__global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? many_ctas(VPT) : 0)
     postnorm_kernel(const __grid_constant__ PostParams pp) {
     using V = Vec<T>;
     constexpr int E = V::kElems;
     constexpr int kWarps = (CL ? kClusterCta : kThreads) / 32;
     constexpr int kRows = kWarps / W;
     // Rows of partials whose loads are in flight at once.
-    constexpr int kAhead = (MANY ? 4 : 8) / VPT;
+    constexpr int kAhead = MANY && VPT < 3 ? 4 / VPT : 8 / VPT;
     constexpr bool kEarly = VPT <= 2 && !MANY;
     const Params& p = pp.p;
     // Warp totals: [second reduction][buffer][warp], of sums and of maxima.
@@ -256,8 +257,10 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? 4 : 0)
 
 template <typename T, bool Q8>
 void* postnorm_rows_entry(int vpt, int w, bool many) {
-    if (many)  // rows below 4 KB
-        return w == 4     ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, false, Q8, true>)
+    if (many)
+        return vpt == 3   ? reinterpret_cast<void*>(&postnorm_kernel<T, 3, 8, false, Q8, true>)
+               : w == 8   ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 8, false, Q8, true>)
+               : w == 4   ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 4, false, Q8, true>)
                : w == 2   ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 2, false, Q8, true>)
                : vpt == 2 ? reinterpret_cast<void*>(&postnorm_kernel<T, 2, 1, false, Q8, true>)
                           : reinterpret_cast<void*>(&postnorm_kernel<T, 1, 1, false, Q8, true>);
@@ -297,24 +300,26 @@ void* postnorm_kernel_for(int dtype, int vpt, int w, bool q8, bool many = false)
               : postnorm_rows_entry<float, false>(vpt, w, many);
 }
 
-// Warps per row and vectors per thread for rows of nvec <= 512 vectors.
+// Warps per row and vectors per thread for rows of nvec <= 768 vectors.
 void rows_shape(int64_t nvec, int* vpt, int* w) {
     *w = 1;
     *vpt = nvec <= 32 ? 1 : 2;
     while (*w < 8 && nvec > static_cast<int64_t>(*w) * 32 * *vpt) *w *= 2;
+    if (nvec > static_cast<int64_t>(*w) * 32 * *vpt) *vpt = 3;
 }
 
 // Which kernel (us, 8 partials bf16: cluster / this file's rows / ring):
-//   rows to 8 KB   few tokens per SM this file's, a CTA or less per row, two vectors a
-//                  thread: up to two (64 x 4096 4.3 / 4.1 / 4.9, 250 x 4096 - / 5.9 / 7.0,
-//                  2 x 400 x 4096 - / 6.2 / 5.9), with 4 KB up to four (600 x 2048 - / 7.0 /
-//                  6.9, 400 x 2048 - / 5.2 / 6.4); rows below 4 KB always (1000 x 256 - / 2.5 /
-//                  7.5, 2 x 1000 x 1024 - / 3.6 / 5.4, 2 x 4096 x 1024 - / 9.4 / 10.7)
-//   longer rows    a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
-//                  / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
-//   everything else the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9)
-constexpr int64_t kShortRowBytes = 4096, kRowsRowBytes = 8192;
-int64_t rows_tokens(int64_t row_bytes) { return row_bytes <= kShortRowBytes ? 4 : 2; }
+//   rows from 8 KB   a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
+//                    / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
+//   rows to 12 KB    this file's, a CTA or less per row, while all CTAs run at once: four
+//                    on an SM (500 x 4096 - / 8.9 / 10.4, 2 x 1000 x 2048 - / 5.0 / 6.1),
+//                    from 8 KB three (400 x 5120 - / 9.8 / 11.1; with 16 KB it would be two,
+//                    256 x 8192 - / 10.4 / 10.1); rows
+//                    below 4 KB always (1000 x 256 - / 2.5 / 7.5, 2 x 4096 x 1024 - / 9.4 / 10.7)
+//   everything else  the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9, 1000 x 4096 - /
+//                    18.4 / 15.8)
+// Under a budget each CTA is alone on its SM: few rows to each, to 8 KB, go without the ring.
+constexpr int64_t kShortRowBytes = 4096, kRowsRowBytes = 8192, kLongestRowBytes = 12288;
 
 cudaLaunchConfig_t cluster_config(int cluster, int64_t tokens, size_t smem, bool pdl, void* stream,
                                   cudaLaunchAttribute (&attr)[2]) {
@@ -387,16 +392,16 @@ int launch_postnorm(const PostParams& pp, int dtype, int max_sms, const PostDevi
                 cudaLaunchKernelExC(&cfg, postnorm_kernel_for(dtype, vc, 0, p.q8 != 0), args));
         }
     }
-    if (p.row_bytes >= kShortRowBytes &&
-        (p.row_bytes > kRowsRowBytes || tokens > rows_tokens(p.row_bytes) * sms))
-        return launch_postnorm_rows(pp, dtype, static_cast<int>(sms), whole, d.smem_optin, stream);
     int vpt = 0, w = 0;
     rows_shape(nvec, &vpt, &w);
     const int64_t rows = kThreads / 32 / w;
     const int64_t ctas = (tokens + rows - 1) / rows;
+    const int64_t at_once = (whole ? many_ctas(vpt) : vpt == 3 ? 0 : 2) * sms;
+    if (p.row_bytes >= kShortRowBytes && (p.row_bytes > kLongestRowBytes || ctas > at_once))
+        return launch_postnorm_rows(pp, dtype, static_cast<int>(sms), whole, d.smem_optin, stream);
+    // Two CTAs on an SM need not spare registers.
+    const bool many = (whole && ctas > 2 * sms) || vpt == 3;
     const int64_t most = whole ? (int64_t{1} << 31) - 1 : sms;
-    // More CTAs than run at once (two on an SM), which leaves W < 8 only: longer rows are few.
-    const bool many = whole && w < 8 && ctas > 2 * sms;
     return launch_with_pdl(postnorm_kernel_for(dtype, vpt, w, p.q8 != 0, many), pp,
                            static_cast<int>(ctas < most ? ctas : most), kThreads, smem, whole,
                            stream);

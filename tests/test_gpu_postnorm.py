@@ -127,8 +127,10 @@ def test_rows_through_the_ring(n_parts, T, H, dtype, max_sms, quant):
 @pytest.mark.parametrize("quant", [None, "e4m3"])
 @pytest.mark.parametrize("n_parts,T,H,dtype", [
     (3, 2600, 248, "bf16"), (8, 2500, 512, "bf16"), (2, 1300, 1016, "bf16"), (5, 700, 1992, "bf16"),
-    (1, 2450, 100, "f32"), (9, 1300, 508, "f32"), (4, 620, 1020, "f32")])
-def test_more_short_rows_than_run_at_once(n_parts, T, H, dtype, quant):
+    (1, 2450, 100, "f32"), (9, 1300, 508, "f32"), (4, 620, 1020, "f32"),
+    (3, 600, 4096, "bf16"), (2, 1100, 2048, "bf16"), (5, 450, 5120, "bf16"), (4, 308, 3068, "f32"),
+    (1, 340, 6144, "bf16"), (2, 605, 1996, "f32")])
+def test_short_rows_beside_each_other(n_parts, T, H, dtype, quant):
     check(n_parts, T, H, dtype, post=T % 4 != 0, gate_tokens=7, quant=quant, in_place=True,
           t0=2, t1=T - 1, residual_scale=0.5)
 
