@@ -139,6 +139,7 @@ struct W4RowsArgs {
     void* to;
     int64_t N, K;
     int group, dtype, wtype;
+    unsigned warm = 0;  // CTAs that warm L2 (set at the launch)
 };
 int launch_w4_quantize(const W4RowsArgs& a, int max_sms, int sm_count, void* stream);
 int launch_w4_dequantize(const W4RowsArgs& a, int max_sms, int sm_count, void* stream);
