@@ -63,6 +63,14 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
+// A barrier of the cluster in two halves, which orders nothing: behind the first half a
+// CTA runs and has read the sums it held.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -312,7 +320,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             bulk_prefetch_l2(place(ld), static_cast<uint32_t>(
                                             (ld.tiles < kWarm ? ld.tiles : kWarm) * kTile));
     }
-    if (split > 1) cluster_barrier();  // every CTA runs before any writes into it
+    // A CTA may write into the others' sums: waited for before the first of a pass.
+    bool may_write = split == 1;
+    auto wait_to_write = [&]() {
+        if (may_write) return;
+        cluster_wait();
+        may_write = true;
+    };
+    if (split > 1) cluster_arrive_relaxed();
     grid_dependency_wait();
     grid_launch_dependents();
 
@@ -466,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         load();
                     }
                     // The piece's sums, to where its stripe's rank adds them up.
+                    wait_to_write();
                     const int i = at.stripe - at.at;
                     const int which = ((rank * slices + at.slice) << log_shares) +
                                       (at.item & (shares - 1));
@@ -489,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             }
             __syncwarp();
+            wait_to_write();
             if (split > 1)
                 cluster_barrier();
             else
@@ -521,11 +538,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             // The sums are read before another pass (and x before other tokens') comes.
             __syncwarp();
-            if (at.at + plan.pass < end || m0 + plan.tokens < a.M) {
-                if (split > 1)
-                    cluster_barrier();
-                else
-                    __syncthreads();
+            const bool last = at.at + plan.pass >= end;
+            if (!last || m0 + plan.tokens < a.M) {
+                if (split > 1) {
+                    cluster_arrive_relaxed();
+                    may_write = false;
+                }
+                if (split == 1 || last) __syncthreads();
             }
         }
     }
