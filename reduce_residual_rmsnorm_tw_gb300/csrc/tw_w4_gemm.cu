@@ -631,15 +631,15 @@ int launch_w4_gemm(const W4GemmArgs& a, int max_sms, const DeviceInfo& d, void* 
     const int64_t tiles = (a.K + kW4Inner - 1) / kW4Inner;
     // Every cut that fits, by the time it takes in ns: a warp's tiles (more of them with
     // two CTAs on an SM than with one) and pieces, each pass's barrier, x on its way into
-    // shared memory, and what a second CTA and a cluster cost once.  Fitted to 830 times
-    // of 31 sizes (1 to 32 tokens, 300 to 32768 channels, K 256 to 8192): the cut taken
-    // is 2 % slower than the best of them on average, 14 % at most.  The most tokens at a
+    // shared memory, and what a second CTA and a cluster cost once.  Fitted to 976 times
+    // of 36 sizes (1 to 32 tokens, 300 to 32768 channels, K 256 to 8192): the cut taken
+    // is 2 % slower than the best of them on average, 12 % at most.  The most tokens at a
     // time that fit, even shares of them; one token that does not fit the SMs of a budget
     // goes in slices, staged for each pass.
-    constexpr int64_t kTile2 = 365, kBlock2 = 222, kTile1 = 220, kBlock1 = 107;
-    constexpr int64_t kPiece = 780, kPass = 1440, kClusterPass = 930;
-    constexpr int64_t kSecondCta = 410, kCluster = 450, kClusterOf8 = 1200;
-    const int64_t stage_of = a.xtype == TW_X_BF16 ? 43 : 75;
+    constexpr int64_t kTile2 = 382, kBlock2 = 223, kTile1 = 221, kBlock1 = 80;
+    constexpr int64_t kPiece = 1030, kPass = 595, kClusterPass = 860;
+    constexpr int64_t kSecondCta = 541, kCluster = 370, kClusterOf8 = 3350;
+    const int64_t stage_of = a.xtype == TW_X_BF16 ? 63 : 160;
     W4Plan best{}, plan{a, 0, 0, 0, 1, 0, 0, d.status};
     int64_t best_cost = -1, best_smem = 0, best_sets = 0;
     int nt = 0;
