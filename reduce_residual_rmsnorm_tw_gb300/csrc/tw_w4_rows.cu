@@ -318,7 +318,8 @@ __global__ void __launch_bounds__(kThreads)
     const int units_k = (tiles_k + kTilesPerUnit - 1) / kTilesPerUnit;
     const int64_t units = (a.N + kW4Channels - 1) / kW4Channels * units_k;
     const bool sectors = (reinterpret_cast<uintptr_t>(a.to) & 31) == 0;
-    if (threadIdx.x == 0 && blockIdx.x < a.warm) {  // as above
+    // As above, by every CTA (8192 x 8192 27.0 -> 25.6 us; by the first ones only 26.7).
+    if (threadIdx.x == 0) {
         const Unit at(blockIdx.x, units_k);
         const int left = tiles_k - at.tile < kTilesPerUnit ? tiles_k - at.tile : kTilesPerUnit;
         bulk_prefetch_l2(static_cast<const char*>(a.from) + (at.stripe * tiles_k + at.tile) * kTile,

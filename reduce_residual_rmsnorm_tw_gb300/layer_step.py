@@ -94,9 +94,9 @@ def two_chunk_layer_step_q8(x, x_scale, w, w_scale, partials, residual, weight, 
 def w4_library_tokens(channels, inner):
     """From this many tokens on, reading 4-bit weights of [channels, inner] back and a
     library product of their bfloat16 form are faster than the product on 4 bits: 33 where
-    that form stays in the L2 cache (4096 x 4096: 32 tokens 10.9 us against 15.1, 40 tokens
-    15.9 against 12.8), 65 where it does not (8192 x 8192: 48 tokens 37.7 us against 45.7,
-    64 tokens 47.4 against 45.7, 96 tokens 70 against 51)."""
+    that form stays in the L2 cache (4096 x 4096: 32 tokens 9.6 us against 14.6, 40 tokens
+    15.1 against 12.3), 65 where it does not (8192 x 8192: 48 tokens 36.4 us against 44.8,
+    64 tokens 43.5 against 44.8, 96 tokens 64.5 against 50.3)."""
     return 33 if 2 * channels * inner < 1 << 27 else 65
 
 
