@@ -379,7 +379,8 @@ int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int grou
  * xtype; x_scale is fp32 [T] for 8-bit x and NULL otherwise; out is [T, N].  A
  * group's products are exact and add up in fp32; the group's sum times its scale
  * adds up over the groups in fp32 too (fp32 x is cut into three bf16 terms,
- * without loss down to 2^-96 in magnitude).  The order of the sum depends on the
+ * without loss down to 2^-96 in magnitude; of bf16 x below 2^-110 bits may be
+ * lost).  The order of the sum depends on the
  * sizes, the types and max_sms only.  Made for few tokens: tw_dequantize_w4 and a
  * library product are faster from 33 tokens on where the weights in bf16 stay in the
  * L2 cache, from 65 on where they do not.

@@ -7,6 +7,7 @@ every step of the computation in its CUDA kernels.  There is no fallback: if
 ``libtw.so`` is missing the first call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -294,9 +295,14 @@ def _dense(name, t, shape, dtype):
         raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
 
 
+@functools.cache
+def _pointer_array(n):
+    return ctypes.c_void_p * n
+
+
 def _pointers(name, tensors, shape, dtype, dev):
     """The pointers of alike tensors on device ``dev`` as a ctypes array."""
-    ptrs = (ctypes.c_void_p * len(tensors))()
+    ptrs = _pointer_array(len(tensors))()
     for i, t in enumerate(tensors):
         if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous {list(shape)} {dtype} tensors")
@@ -384,14 +390,18 @@ def tw_gemm_q8(x, x_scale, w, w_scale, out, t0=0, t1=None, max_sms=None, stream=
         _stream_handle(stream), _DTYPES[out.dtype], qt))
 
 
-def _optional(name, t, shape, dtype, dev):
-    """The pointer of a tensor that may be left out."""
-    if t is None:
-        return None
-    _dense(name, t, shape, dtype)
+def _pointer(name, t, shape, dtype, dev):
+    """The pointer of a tensor on device ``dev``."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {list(shape)} {dtype} tensor")
     if t.get_device() != dev:
         raise ValueError("every tensor must be on the current CUDA device")
     return t.data_ptr()
+
+
+def _optional(name, t, shape, dtype, dev):
+    """The pointer of a tensor that may be left out."""
+    return None if t is None else _pointer(name, t, shape, dtype, dev)
 
 
 def _postnorm(entry, partials, residual, weight, out, out_scale, residual_out, eps, post_weight,
@@ -416,18 +426,18 @@ def _postnorm(entry, partials, residual, weight, out, out_scale, residual_out, e
         tail += (_quantised(out[0]),)
         o_arr = _pointers("out", out, shape, out[0].dtype, dev)
         scales = (_pointers("out_scale", out_scale, (T,), torch.float32, dev),)
-    _dense("residual", residual, shape, dtype)
-    _dense("residual_out", residual_out, shape, dtype)
-    _dense("weight", weight, (H,), dtype)
+    res = _pointer("residual", residual, shape, dtype, dev)
+    res_out = _pointer("residual_out", residual_out, shape, dtype, dev)
+    w = _pointer("weight", weight, (H,), dtype, dev)
     post = _optional("post_weight", post_weight, (H,), dtype, dev)
     if gate is not None and gate_tokens < 1:
         raise ValueError("gate_tokens must be at least 1")
-    g = None if gate is None else _optional("gate", gate, (-(-T // gate_tokens), H), dtype, dev)
-    _on_current_device(residual, weight, residual_out)
+    g = None if gate is None else _pointer("gate", gate, (-(-T // gate_tokens), H), dtype, dev)
+    if dev < 0:
+        raise ValueError("every tensor must be on the current CUDA device")
     if T == 0:
         return
-    _check(entry(p_arr, n, post, g, gate_tokens, residual.data_ptr(), weight.data_ptr(), o_arr,
-                 *scales, n_out, residual_out.data_ptr(), T, H,
+    _check(entry(p_arr, n, post, g, gate_tokens, res, w, o_arr, *scales, n_out, res_out, T, H,
                  eps if post_eps is None else post_eps, eps, block_scale, residual_scale, t0,
                  T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
                  _stream_handle(stream), *tail))
@@ -553,25 +563,28 @@ def tw_gemm_w4(x, w, out, x_scale=None, t0=0, t1=None, max_sms=None, stream=None
     """out[t, n] = sum_k x[t, k] * w[n, k] on rows [t0, t1): ``x`` [T, k] bfloat16
     or float32, or int8 or float8_e4m3fn with ``x_scale`` [T]; ``w`` a W4Weight;
     ``out`` [T, n] bfloat16 or float32."""
-    if x.dim() != 2 or x.shape[1] != w.k:
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != w.k:
         raise ValueError(f"x must be [T, {w.k}]")
-    T = x.shape[0]
-    xt = _XTYPES.get(x.dtype)
-    if xt is None or out.dtype not in _DTYPES:
+    T = shape[0]
+    xt, dt = _XTYPES.get(x.dtype), _DTYPES.get(out.dtype)
+    if xt is None or dt is None:
         raise ValueError(f"dtypes {x.dtype}, {out.dtype} not supported")
     if (x_scale is None) != (xt < 2):
         raise ValueError("x_scale goes with 8-bit x, and only with it")
     if not x.is_contiguous():
         raise ValueError("x must be contiguous")
-    _dense("out", out, (T, w.n), out.dtype)
-    _on_current_device(x, w.packed, out)
-    scale = _optional("x_scale", x_scale, (T,), torch.float32, x.get_device())
+    dev = torch.cuda.current_device() if x.is_cuda else -1
+    to = _pointer("out", out, (T, w.n), out.dtype, dev)
+    if dev < 0 or x.get_device() != dev or w.packed.get_device() != dev:
+        raise ValueError("every tensor must be on the current CUDA device")
+    scale = _optional("x_scale", x_scale, (T,), torch.float32, dev)
     if T == 0:
         return
     _check(load().tw_gemm_w4(
-        x.data_ptr(), scale, w.packed.data_ptr(), out.data_ptr(), T, w.n, w.k, w.group, t0,
+        x.data_ptr(), scale, w.packed.data_ptr(), to, T, w.n, w.k, w.group, t0,
         T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
-        _stream_handle(stream), xt, _DTYPES[out.dtype], w.wtype))
+        _stream_handle(stream), xt, dt, w.wtype))
 
 
 def tw_split_launch(partials, residual, weight, out, residual_out, eps,

@@ -121,6 +121,33 @@ def test_infinities_and_nans_stay_in_their_token_and_channel():
         assert np.isfinite(got[[0, 3, 5]][:, np.arange(40) != 7]).all()
 
 
+def test_nan_of_8_bits_and_scales_stay_in_their_token():
+    w4, w64 = make(40, 208, 64, "e2m1")
+    x, scale, x64 = make_x(9, 208, "e4m3")
+    x[3, 100] = float("nan")
+    scale[5], scale[6] = float("nan"), 0.0
+    x64[6] = 0
+    out = torch.empty(9, 40, device="cuda")
+    tw.tw_gemm_w4(x, w4, out, x_scale=scale)
+    assert out[[3, 5]].isnan().all() and not out[6].any()
+    rest = [0, 1, 2, 4, 7, 8]
+    check(out[rest], x64[rest], w64, 64, False)
+
+
+@pytest.mark.parametrize("xtype", ["bf16", "f32"])
+def test_small_x_keeps_its_bits(xtype):
+    """Down to the magnitude that the header names, next to a large scale."""
+    least = 2.0 ** (-110 if xtype == "bf16" else -96)
+    v = torch.zeros(16, 64)
+    v[:, 5] = 1
+    w4 = tw.W4Weight.from_values(v.cuda(), torch.full((16, 2), 2.0 ** 90).cuda(), 32, "int4")
+    x = torch.zeros(3, 64, dtype=X[xtype])
+    x[:, 5] = torch.tensor([1.0, 1.9921875, 1.2421875 if xtype == "bf16" else 1 + 2.0 ** -23]) * least
+    out = torch.empty(3, 16, device="cuda")
+    tw.tw_gemm_w4(x.cuda(), w4, out)
+    assert torch.equal(out.cpu(), (x[:, 5:6].double() * 2.0 ** 90).float().expand(3, 16))
+
+
 def test_fp32_x_keeps_all_its_bits():
     """x of 24 significant bits against weights that pick one of them: exact."""
     k = 128
