@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? many_ctas(
     // Rows of partials whose loads are in flight at once.
     constexpr int kAhead = MANY && VPT < 3 ? 4 / VPT : 8 / VPT;
     constexpr bool kEarly = VPT <= 2 && !MANY;
+    constexpr bool kLate = MANY && VPT < 3;
     const Params& p = pp.p;
     // Warp totals: [second reduction][buffer][warp], of sums and of maxima.
     __shared__ float warp_part[2][2][kWarps];
@@ -147,8 +148,9 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? many_ctas(
     // barrier (W == kWarps) are one.
     for (; t < p.t1; t += step, buf ^= 1) {
         const int64_t row_off = t * p.row_bytes;
-        // What the sum does not need is on its way beside it, the weights too where
-        // there are registers for them.
+        // What the sum does not need is on its way beside it, the weights too where there
+        // are registers for them; where other CTAs hide its latency, only behind it (2 x
+        // 4096 x 1024 9.4 -> 9.0 us, 4 x 2000 x 1504 10.8 -> 9.6; 10 KB rows 9.8 -> 10.7).
         uint4 res[VPT], gate[VPT], pw[VPT], wv[VPT];
         const char* gate_row =
             pp.gate ? static_cast<const char*>(pp.gate) + t / pp.gate_tokens * p.row_bytes
@@ -159,11 +161,17 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? many_ctas(
                                                 static_cast<int64_t>(v) * 16)
                                     : make_uint4(0, 0, 0, 0);
         };
+        auto load_beside = [&]() {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-            res[k] = load(static_cast<const char*>(p.residual) + row_off, k);
-            gate[k] = load(gate_row, k);
-            if constexpr (kEarly) {
+            for (int k = 0; k < VPT; ++k) {
+                res[k] = load(static_cast<const char*>(p.residual) + row_off, k);
+                gate[k] = load(gate_row, k);
+            }
+        };
+        if constexpr (!kLate) load_beside();
+        if constexpr (kEarly) {
+#pragma unroll
+            for (int k = 0; k < VPT; ++k) {
                 pw[k] = load(pp.post_weight, k);
                 wv[k] = load(p.weight, k);
             }
@@ -191,6 +199,7 @@ __global__ void __launch_bounds__(CL ? kClusterCta : kThreads, MANY ? many_ctas(
                     if (r0 + a < p.n_parts && v_begin + rtid + k * W * 32 < v_end)
                         add_vec(s[k], raw[a][k], static_cast<T*>(nullptr));
         }
+        if constexpr (kLate) load_beside();
         float c = 1.f, most = 0.f;
         if (pp.post_weight) {
             float ss2[2] = {0.f, 0.f};
@@ -312,10 +321,10 @@ void rows_shape(int64_t nvec, int* vpt, int* w) {
 //   rows from 8 KB   a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
 //                    / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
 //   rows to 12 KB    this file's, a CTA or less per row, while all CTAs run at once: four
-//                    on an SM (500 x 4096 - / 8.9 / 10.4, 2 x 1000 x 2048 - / 5.0 / 6.1),
+//                    on an SM (500 x 4096 - / 8.7 / 10.4, 2 x 1000 x 2048 - / 4.8 / 6.1),
 //                    from 8 KB three (400 x 5120 - / 9.8 / 11.1; with 16 KB it would be two,
 //                    256 x 8192 - / 10.4 / 10.1); rows
-//                    below 4 KB always (1000 x 256 - / 2.5 / 7.5, 2 x 4096 x 1024 - / 9.4 / 10.7)
+//                    below 4 KB always (1000 x 256 - / 2.5 / 7.5, 2 x 4096 x 1024 - / 9.0 / 10.7)
 //   everything else  the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9, 1000 x 4096 - /
 //                    18.4 / 15.8)
 // Under a budget each CTA is alone on its SM: few rows to each, to 8 KB, go without the ring.
