@@ -174,3 +174,52 @@ def test_other_streams_of_other_calls_see_whole_results():
     tw.tw_gemm_w4(x, w4, outs[1], stream=s1)
     s1.synchronize()
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("T,H", [(1, 512), (6, 2048), (24, 4096)])
+def test_weights_laid_out_again_just_before_they_are_used(T, H):
+    """Calls right behind each other see what the one before wrote, not what was there."""
+    g = torch.Generator(device="cuda").manual_seed(H)
+    ws = [torch.randn(H, H, generator=g, device="cuda").bfloat16() for _ in range(6)]
+    x = torch.randn(T, H, generator=g, device="cuda").bfloat16()
+    w4 = tw.W4Weight(H, H, 64, "int4")
+    apart = [[torch.zeros(T, H, device="cuda"), torch.zeros_like(ws[0])] for _ in ws]
+    for w, (out, back) in zip(ws, apart):
+        for call in (lambda: tw.tw_quantize_w4(w, w4), lambda: tw.tw_gemm_w4(x, w4, out),
+                     lambda: tw.tw_dequantize_w4(w4, back)):
+            call()
+            torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    got = [[torch.zeros_like(out), torch.zeros_like(back)] for out, back in apart]
+    with torch.cuda.graph(graph):
+        for w, (out, back) in zip(ws, got):
+            tw.tw_quantize_w4(w, w4)
+            tw.tw_gemm_w4(x, w4, out)
+            tw.tw_dequantize_w4(w4, back)
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for (a, b), (c, d) in zip(apart, got):
+        assert torch.equal(a, c) and torch.equal(b, d)
+
+
+def test_two_graphs_replayed_at_once():
+    """Captured calls share nothing: two graphs of one layer's weights beside each other."""
+    layers = [Layer(9, 2048, 2, [("int4", 128), ("e2m1", 64)], "int8", seed=3) for _ in range(2)]
+    layers[1].w4 = layers[0].w4
+    graphs, streams = [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for layer in layers:
+        layer.run()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(4):
+                layer.run()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for layer in layers:
+        layer.check()
+    assert tw.tw_device_status() == 0
