@@ -279,9 +279,9 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
 // Pipelines for rows of this size.  More of them hide each other's barriers, where the
 // ring still holds rows enough for each and there are tokens for all:
 //   rows above 24 KB   one, whose ring holds more of them
-//   rows to 5 KB       eight, with more than four tokens to an SM (8 x 2048 x 2048 bf16 with
+//   rows to 5 KB       eight, unless four's rounds are fewer tokens (8 x 2048 x 2048 bf16 with
 //                      two, four and eight 25.0, 16.9 and 16.2 us; 5 x 600 x 1024 fp32 7.3,
-//                      5.5 and 5.9)
+//                      5.5 and 5.9, 6 x 1500 x 2048 bf16 16.0, 11.6 and 13.1)
 //   rows to 8 KB       four, unless their last round is emptier than two's by more than
 //                      they gain, the more the shorter the row (8 x 700 x 3000 12.4 -> 11.0,
 //                      2 x 4096 x 4096 30.0 -> 27.3, but 2 x 2048 x 4096 16.0 -> 16.3)
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
 int pipelines_for(int64_t row_bytes, int64_t tokens, int64_t sms) {
     auto rounds = [&](int pipes) { return (tokens + pipes * sms - 1) / (pipes * sms) * pipes; };
     if (row_bytes > 24 * 1024) return 1;
-    if (row_bytes <= 5 * 1024 && tokens > 4 * sms) return 8;
+    if (row_bytes <= 5 * 1024 && rounds(8) <= rounds(4)) return 8;
     return row_bytes <= 8 * 1024 && rounds(4) * row_bytes < rounds(2) * 9 * 1024 ? 4 : 2;
 }
 
