@@ -81,11 +81,12 @@ __device__ __forceinline__ float group_scale(float m) {
 
 // An fp32 quotient p of v / s that may be the very middle of two codes though the
 // real one is not: an ulp towards the real one.  Middles have at most four
-// significant bits, so p times s is exact and so is the sign of the remainder.
+// significant bits, so p times s is exact and so is the sign of the remainder.  A zero
+// (v = 0, or a quotient that underflowed) is no middle and has no ulp below it.
 // (bf16 v: never needed, a real quotient is the middle or a 2^-12th of it away.)
 __device__ __forceinline__ float off_middle(float p, float v, float s) {
     uint32_t bits = __float_as_uint(p);
-    if ((bits & 0xffffu) == 0) {
+    if ((bits & 0xffffu) == 0 && p != 0.f) {
         const float rest = fmaf(-p, s, v);
         if (rest != 0.f) bits += (rest > 0.f) == (p > 0.f) ? 1u : ~0u;
     }
