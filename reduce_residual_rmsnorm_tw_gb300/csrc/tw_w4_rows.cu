@@ -7,7 +7,7 @@
 // maximum is a few shuffles and a channel's words are 64 contiguous bytes.
 // Bound by HBM: the rows in and half a byte per weight out, or the other way
 // round (8192 x 8192 bf16 to int4 27.6 us, 6.1 TB/s, to e2m1 30.9; back 25.7, 6.6 TB/s;
-// 4090 x 5120 fp32 to e2m1 with groups of 32 16.7 and 15.2).  Quantising takes some ten
+// 4090 x 5120 fp32 to e2m1 with groups of 32 17.1 and 15.0).  Quantising takes some ten
 // instructions a weight, for which loads in flight have to cover.
 #include "tw_device.cuh"
 
@@ -131,6 +131,27 @@ __device__ __forceinline__ void grid_quotients(float* q, const float* v, float s
                 : "+f"(q[e]), "+f"(q[e + 1])
                 : "f"(-kGridBase));
     }
+}
+
+// Quotients of fp32 v: p = v r with an approximate reciprocal r, then p + (v - p s) r,
+// the remainder being exact but for what is below fp32's range (Markstein's correction:
+// right to 2^-45 before the one rounding, under every scale; a reciprocal in two parts is
+// not from 2^125 up, where its low part is a subnormal).
+__device__ __forceinline__ void quotients(float* q, const float* v, float s) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+#pragma unroll
+    for (int e = 0; e < 8; e += 2)
+        asm("{\n\t.reg .b64 a, p, h, s;\n\t"
+            "mov.b64 a, {%2, %3};\n\t"
+            "mov.b64 h, {%4, %4};\n\t"
+            "mov.b64 s, {%5, %5};\n\t"
+            "mul.rn.f32x2 p, a, h;\n\t"
+            "fma.rn.f32x2 a, p, s, a;\n\t"
+            "fma.rn.f32x2 p, a, h, p;\n\t"
+            "mov.b64 {%0, %1}, p;\n\t}"
+            : "=f"(q[e]), "=f"(q[e + 1])
+            : "f"(v[e]), "f"(v[e + 1]), "f"(r), "f"(-s));
 }
 
 // The word that holds eight codes (tw.h): q[0..7] quotients.  int4: 2^23 + 8 + q is
@@ -289,9 +310,7 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 5)
             if constexpr (kGrid) {
                 grid_quotients<INT4>(q, f, s);
             } else {
-                const RowExact by(s, 1.f);
-#pragma unroll
-                for (int e = 0; e < 8; e += 2) by.quotients(q + e, f + e);
+                quotients(q, f, s);
                 if (any_round(q)) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) q[e] = off_middle(q[e], f[e], s);

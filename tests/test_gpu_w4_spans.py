@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests.test_gpu_w4_rows import check
+from tests.w4_reference import LEVELS
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +29,25 @@ def test_quotients_that_underflow(most, small, kind):
         w[2 * group + negative] = -small if negative else small
         w[2 * group + negative, 17] = -most
     check(torch.from_numpy(w), group, kind)
+
+
+@pytest.mark.parametrize("kind", ["int4", "e2m1"])
+@pytest.mark.parametrize("exponent", list(range(98, 126)))
+def test_middles_under_large_scales(exponent, kind):
+    """Values on the middle between two codes and up to four ulps beside it, under scales of
+    every mantissa up to the largest that fp32 weights can have."""
+    group, levels = 32, LEVELS[kind]
+    middles = ((levels[:-1] + levels[1:]) / 2).astype(np.float32)
+    rows = []
+    for i in range(128):
+        scale = np.ldexp(1 + i / 128, exponent)
+        if scale * levels[-1] > np.finfo(np.float32).max:
+            continue
+        middle = middles * np.float32(scale)  # exact: 4 bits times 8
+        for away in (-4, -2, -1, 0, 1, 2, 4):
+            row = np.zeros(group, dtype=np.float32)
+            row[0] = scale * levels[-1]  # 8 bits times 3 at most
+            row[1:8] = (middle.view(np.int32) + np.int32(away)).view(np.float32)
+            row[8:15] = -row[1:8]
+            rows.append(row)
+    check(torch.from_numpy(np.stack(rows)), group, kind)
