@@ -352,16 +352,18 @@ cudaLaunchConfig_t cluster_config(int cluster, int64_t tokens, size_t smem, bool
 
 int postnorm_prepare(int smem_optin, int (*clusters)[3][2]) {
     if (smem_optin < kExclusiveSmemBytes + 2048) return static_cast<int>(cudaErrorInvalidValue);
+    // (Which also loads them, those for many rows too, whose launches ask for no shared memory.)
     for (int dt = 0; dt < 2; ++dt)
         for (int w = 0; w <= 8; w = w ? 2 * w : 1)
-            for (int vpt = 1; vpt <= 8; vpt *= 2)
-                for (bool q8 : {false, true}) {
-                    void* fn = postnorm_kernel_for(dt, vpt, w, q8);
-                    if (!fn) continue;
-                    cudaError_t e = cudaFuncSetAttribute(
-                        fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
-                    if (e != cudaSuccess) return static_cast<int>(e);
-                }
+            for (int vpt = 1; vpt <= 4; ++vpt)
+                for (bool q8 : {false, true})
+                    for (bool many : {false, true}) {
+                        void* fn = postnorm_kernel_for(dt, vpt, w, q8, many);
+                        if (!fn) continue;
+                        cudaError_t e = cudaFuncSetAttribute(
+                            fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kExclusiveSmemBytes);
+                        if (e != cudaSuccess) return static_cast<int>(e);
+                    }
     // Clusters of 8 CTAs that run at once, by vectors per thread (1, 2, 4).
     for (int v = 0; v < 3; ++v) {
         cudaLaunchAttribute attr[2];
