@@ -63,13 +63,17 @@ __device__ __forceinline__ void bulk_copy(uint32_t dst, const void* src, uint32_
         "l"(src), "r"(bytes), "r"(bar)
         : "memory");
 }
-// A barrier of the cluster in two halves, which orders nothing: behind the first half a
-// CTA runs and has read the sums it held.
+// A barrier of the cluster in two halves.  At the start the first half says only that the
+// CTA runs, and orders nothing; between passes that it has read the sums it held, which the
+// others' next ones, behind the second half, must not overtake: a release.
 __device__ __forceinline__ void cluster_arrive_relaxed() {
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_arrive_release() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_wait() {
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool last = at.at + plan.pass >= end;
             if (!last || m0 + plan.tokens < a.M) {
                 if (split > 1) {
-                    cluster_arrive_relaxed();
+                    cluster_arrive_release();
                     may_write = false;
                 }
                 if (split == 1 || last) __syncthreads();
