@@ -212,6 +212,8 @@ __device__ __forceinline__ void widen_x(uint32_t xs, int x_stride, int tokens, i
 
 // Floats between the columns of a piece's sums (a fragment's stores meet no bank twice).
 constexpr int kRowStride = kW4Channels + 4;
+// Bytes of shared memory before the sums (the word that says that a wait gave up).
+constexpr int kHeader = 16;
 // Tiles that a warp warms L2 with before the launch before this one has ended.
 constexpr int kWarm = 16;
 // Tiles of x that a CTA holds at a time.
@@ -286,9 +288,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     // [piece][i / split][column][kRowStride].  Then the rings, their barriers, x.
     const int columns = plan.tokens * parts;
     const int owned = (plan.pass + split - 1) >> log_split;
-    float* sums = reinterpret_cast<float*>(smem);
+    // Before them, not 0 where a copy did not arrive in time (the device status says so).
+    volatile int* const gave_up = reinterpret_cast<volatile int*>(smem);
+    float* sums = reinterpret_cast<float*>(smem + kHeader);
     const uint32_t rings =
-        smem_addr(smem) + ((split * slices) << log_shares) * owned * columns * kRowStride * 4;
+        smem_addr(sums) + ((split * slices) << log_shares) * owned * columns * kRowStride * 4;
     const uint32_t ring = rings + warp * plan.slots * kSlot;
     const uint32_t bars = rings + kWarps * plan.slots * kSlot;
     const uint32_t bar = bars + warp * kMaxSlots * 8;
@@ -297,7 +301,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 
     if (lane == 0) {
         for (int i = 0; i < plan.slots; ++i) mbar_init(bar + i * 8, 1);
-        if (warp == 0) mbar_init(x_bar, 1);
+        if (warp == 0) {
+            mbar_init(x_bar, 1);
+            *gave_up = 0;
+        }
         mbar_init_fence();
     }
     __syncthreads();
@@ -335,9 +342,27 @@ __global__ void __launch_bounds__(kThreads, 2)
     grid_dependency_wait();
     grid_launch_dependents();
 
+    // Waits for a copy.  Where one gives up the CTA's others wait no longer than a copy in
+    // flight takes to land; nothing more is stored, and behind the pass and its block of
+    // tokens the CTA, with the others of its cluster, leaves.
+    auto await = [&](uint32_t on, uint32_t parity) {
+        uint64_t start = 0;
+        for (uint32_t tries = 1; !mbar_try_wait(on, parity); ++tries) {
+            if (tries % 64 != 0) continue;
+            const uint64_t now = global_timer_ns();
+            if (start == 0) start = now;
+            if (now - start <= kWaitLimitNs / 1000 ||
+                (now - start <= kWaitLimitNs && !*gave_up))
+                continue;
+            *gave_up = 1;
+            atomicOr(plan.status, 1u);
+            break;
+        }
+    };
     const uint32_t one = elect_one();
     uint32_t slot_ld = 0, slot = 0, phase = 0, x_phase = 0;
-    for (int64_t m0 = 0; m0 < a.M; m0 += plan.tokens) {
+    int64_t m0 = 0;
+    for (; m0 < a.M && !*gave_up; m0 += plan.tokens) {
         const int tokens = static_cast<int>(a.M - m0 < plan.tokens ? a.M - m0 : plan.tokens);
         const int cols = tokens * parts;
         // The next chunk to load.
@@ -390,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                                   (((m0 + lane) * a.K + k0) << log_size),
                               own << log_size, x_bar);
             }
-            if (!mbar_wait_slice(x_bar, x_phase, nullptr)) atomicOr(plan.status, 1u);
+            await(x_bar, x_phase);
             x_phase ^= 1u;
             if (a.xtype == TW_X_BF16) {
                 for (int e = threadIdx.x; k1 > K && e < tokens * 16; e += kThreads)
@@ -430,9 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     float total[NT][4] = {};
                     uint32_t x_at = (at.first - slice_at(at.slice)) * (kW4Inner * 2);
                     for (int i = 0; i < tiles; i += kChunk) {
-                        // (A copy that does not arrive: the device status says so.)
-                        if (!mbar_wait_slice(bar + slot * 8, phase, nullptr))
-                            atomicOr(plan.status, 1u);
+                        await(bar + slot * 8, phase);
                         const uint32_t t = ring + slot * kSlot + lane * 16;
                         const uint32_t ts = ring + slot * kSlot + 1024 + row * (512 / G);
 #pragma unroll
@@ -490,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const int which = ((rank * slices + at.slice) << log_shares) +
                                       (at.item & (shares - 1));
                     uint32_t to =
-                        smem_addr(smem) +
+                        smem_addr(sums) +
                         ((which * owned + (i >> log_split)) * columns * kRowStride + row) * 4;
                     if (split > 1) to = map_to_rank(to, static_cast<uint32_t>(i & (split - 1)));
 #pragma unroll
@@ -510,13 +533,17 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
             __syncwarp();
             wait_to_write();
+            // (The others would add up what this CTA has left them.)
+            if (split > 1 && *gave_up && lane < split)
+                st_cluster_f32(map_to_rank(smem_addr(smem), static_cast<uint32_t>(lane)), 1.f);
             if (split > 1)
                 cluster_barrier();
             else
                 __syncthreads();
             // Every piece of the pass is there: this rank's stripes, added up in order.
             const int pieces = (split * slices) << log_shares;
-            const int mine = ((items >> log_shares) - rank + split - 1) >> log_split;  // stripes
+            const int mine =  // stripes
+                *gave_up ? 0 : ((items >> log_shares) - rank + split - 1) >> log_split;
             const int apart = owned * columns * kRowStride;
             const float factor =
                 (INT4 ? kInt4Factor : 1.f) * (a.xtype == TW_X_INT8 ? kInt8Factor : 1.f);
@@ -552,6 +579,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     }
+    // Given up: copies in flight have time to land before their shared memory is another CTA's.
+    if (m0 < a.M) {
+        wait_to_write();
+        const uint64_t start = global_timer_ns();
+        while (global_timer_ns() - start < kWaitLimitNs / 100) {
+        }
+    }
 }
 
 template <bool INT4, int G>
@@ -579,7 +613,7 @@ int64_t smem_bytes(int nt, int columns, int64_t K, int group, const W4Plan& p) {
     const int tiles = static_cast<int>((K + kW4Inner - 1) / kW4Inner);
     const int64_t inner = x_tiles(tiles, split, p.slices) * kW4Inner;
     const int64_t landing = p.a.xtype == TW_X_BF16 ? 0 : inner * (p.a.xtype == TW_X_F32 ? 4 : 1);
-    return sums + rings + columns * (inner + kXPad) * 2 + landing;
+    return kHeader + sums + rings + columns * (inner + kXPad) * 2 + landing;
 }
 // What a CTA may use where two share an SM.
 int64_t half_smem(int smem_optin) { return (smem_optin - 1024) / 2; }
