@@ -114,10 +114,18 @@ def sandwich_layer_step_w4(x, w, partials, residual, weight, out, residual_out, 
 
     ``workspace``, a [H, K] bfloat16 tensor, is for many tokens: from w4_library_tokens(H, K)
     on a bfloat16 ``x`` (with bfloat16 partials) is multiplied by the weights read back
-    into it, a plain library GEMM."""
+    into it, a plain library GEMM.  What is refused does not depend on the number of
+    tokens."""
     stream = torch.cuda.current_stream() if stream is None else stream
-    if (workspace is not None and x.shape[0] >= w4_library_tokens(*workspace.shape)
+    if workspace is not None and (workspace.shape != (w.n, w.k) or not workspace.is_contiguous()
+                                  or workspace.dtype != torch.bfloat16
+                                  or workspace.device != w.packed.device):
+        raise ValueError(f"workspace must be a contiguous [{w.n}, {w.k}] bfloat16 tensor on the "
+                         "weights' device")
+    if (workspace is not None and x.shape[0] >= w4_library_tokens(w.n, w.k)
             and x.dtype == partials[0].dtype == torch.bfloat16):
+        # The checks of the product on 4 bits (of no rows: it launches nothing).
+        tw.tw_gemm_w4(x, w, partials[0], x_scale=x_scale, t1=0, stream=stream)
         tw.tw_dequantize_w4(w, workspace, stream=stream)
         with torch.cuda.stream(stream):
             torch.matmul(x, workspace.t(), out=partials[0])
