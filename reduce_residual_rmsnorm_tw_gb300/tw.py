@@ -495,11 +495,13 @@ class W4Weight:
         if scale.shape != (n, -(-k // group)):
             raise ValueError(f"scale must be [{n}, {-(-k // group)}]")
         held = scale.to(torch.bfloat16)
-        if not torch.equal(held.float().nan_to_num(-1.0), scale.float().nan_to_num(-1.0)):
+        # (A NaN stays one; bf16 infinities are numbers here, what rounds to one is not.)
+        if not torch.all((held.double() == scale.double()) | scale.isnan()):
             raise ValueError("scale must hold bf16 numbers")
         stripes, tiles = -(-n // 16), -(-k // 128)
         v = torch.zeros(stripes * 16, tiles * 128, dtype=torch.float32, device=values.device)
         v[:n, :k] = values
+        same = values.dtype != torch.float64 or torch.equal(v[:n, :k].double(), values)
         if kind == "int4":
             code = v.round().clamp(-8, 7)
             exact, code = code, code.to(torch.int32) + 8
@@ -512,7 +514,7 @@ class W4Weight:
             code = magnitude.to(torch.int32) + torch.signbit(v).to(torch.int32) * 8
             # Where the three low bits and the sign of a word's values go.
             fields = [(7, 6, 15), (7, 3, 12), (7, 9, 14), (7, 0, 13)]
-        if not torch.equal(exact, v):
+        if not same or not torch.equal(exact, v):
             raise ValueError(f"values hold numbers that {kind} does not")
         # [stripe, half, row, tile, k / 32, k / 8 % 4, k / 2 % 4, k % 2]
         code = code.view(stripes, 2, 8, tiles, 4, 4, 4, 2)
