@@ -536,14 +536,21 @@ class W4Weight:
         return self
 
 
+def _packed(w, dev):
+    """The pointer of a W4Weight's packed bytes, which are those of its shape."""
+    size = -(-w.n // 16) * -(-w.k // 128) * (1024 + 4096 // w.group)
+    return _pointer("packed", w.packed, (size,), torch.uint8, dev)
+
+
 def tw_quantize_w4(w, into, max_sms=None, stream=None):
     """Quantise ``w`` ([n, k] bfloat16 or float32) into ``into``, a W4Weight."""
     if w.dtype not in _DTYPES:
         raise ValueError(f"dtype {w.dtype} not supported (bfloat16 or float32)")
     _dense("w", w, (into.n, into.k), w.dtype)
-    _on_current_device(w, into.packed)
+    packed = _packed(into, w.get_device())
+    _on_current_device(w)
     _check(load().tw_quantize_w4(
-        w.data_ptr(), into.packed.data_ptr(), into.n, into.k, into.group,
+        w.data_ptr(), packed, into.n, into.k, into.group,
         _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[w.dtype],
         into.wtype))
 
@@ -554,9 +561,10 @@ def tw_dequantize_w4(w, out, max_sms=None, stream=None):
     if out.dtype not in _DTYPES:
         raise ValueError(f"dtype {out.dtype} not supported (bfloat16 or float32)")
     _dense("out", out, (w.n, w.k), out.dtype)
-    _on_current_device(out, w.packed)
+    packed = _packed(w, out.get_device())
+    _on_current_device(out)
     _check(load().tw_dequantize_w4(
-        w.packed.data_ptr(), out.data_ptr(), w.n, w.k, w.group,
+        packed, out.data_ptr(), w.n, w.k, w.group,
         _ALL_SMS if max_sms is None else max_sms, _stream_handle(stream), _DTYPES[out.dtype],
         w.wtype))
 
@@ -578,13 +586,14 @@ def tw_gemm_w4(x, w, out, x_scale=None, t0=0, t1=None, max_sms=None, stream=None
         raise ValueError("x must be contiguous")
     dev = torch.cuda.current_device() if x.is_cuda else -1
     to = _pointer("out", out, (T, w.n), out.dtype, dev)
-    if dev < 0 or x.get_device() != dev or w.packed.get_device() != dev:
+    packed = _packed(w, dev)
+    if dev < 0 or x.get_device() != dev:
         raise ValueError("every tensor must be on the current CUDA device")
     scale = _optional("x_scale", x_scale, (T,), torch.float32, dev)
     if T == 0:
         return
     _check(load().tw_gemm_w4(
-        x.data_ptr(), scale, w.packed.data_ptr(), to, T, w.n, w.k, w.group, t0,
+        x.data_ptr(), scale, packed, to, T, w.n, w.k, w.group, t0,
         T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
         _stream_handle(stream), xt, dt, w.wtype))
 
