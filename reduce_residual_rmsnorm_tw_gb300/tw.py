@@ -437,7 +437,9 @@ def _postnorm(entry, partials, residual, weight, out, out_scale, residual_out, e
         raise ValueError("every tensor must be on the current CUDA device")
     if T == 0:
         return
-    _check(entry(p_arr, n, post, g, gate_tokens, res, w, o_arr, *scales, n_out, res_out, T, H,
+    # (T tokens to a row of the gate and more are one row for all; more than 64 bits hold
+    # would come out as another number.)
+    _check(entry(p_arr, n, post, g, min(gate_tokens, T), res, w, o_arr, *scales, n_out, res_out, T, H,
                  eps if post_eps is None else post_eps, eps, block_scale, residual_scale, t0,
                  T if t1 is None else t1, _ALL_SMS if max_sms is None else max_sms,
                  _stream_handle(stream), *tail))
