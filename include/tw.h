@@ -380,10 +380,14 @@ int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int grou
  * group's products are exact and add up in fp32; the group's sum times its scale
  * adds up over the groups in fp32 too (fp32 x is cut into three bf16 terms,
  * without loss down to 2^-96 in magnitude; of bf16 x below 2^-110 bits may be
- * lost).  The order of the sum depends on the
- * sizes, the types and max_sms only.  Made for few tokens: tw_dequantize_w4 and a
- * library product are faster from 33 tokens on where the weights in bf16 stay in the
- * L2 cache, from 65 on where they do not.
+ * lost).  Under small scales a group's contribution, before x_scale, is held to
+ * 2^-143 (TW_INT4) or 2^-150 (TW_E2M1), half of fp32's least step as the kernel holds
+ * it; int8 x loses nothing there.  The order of the sum depends on the
+ * sizes, the types and max_sms only.  Made for few tokens: W is read again for every
+ * 32 of them (10 of fp32 x).  tw_gemm_q8 on the same weights in 8 bits is faster from
+ * about 12 (e4m3) and 20 (int8) tokens on; tw_dequantize_w4, which rounds w to dtype,
+ * and a library product are from 33 on where the weights in bf16 stay in the L2
+ * cache, from 65 on where they do not.
  * Rules: T at most 2^31 - 512; x, packed and out 16-byte aligned, x_scale 4-byte
  * aligned; out overlaps no input. */
 int tw_gemm_w4(const void* x, const float* x_scale, const void* packed, void* out, int64_t T,

@@ -81,7 +81,8 @@ __device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
 
 // A word's eight values as four pairs of bf16, (k, k + 1) for k = 0, 2, 4, 6: the
 // values themselves (e2m1) or times 2^-7 (int4; the factor comes back in at the
-// end, so results below 2^-119 in magnitude may lose bits).  bf16 numbers below
+// end, so a group's contribution below 2^-119 in magnitude, fp32's 2^-126 times 2^7, may
+// lose bits).  bf16 numbers below
 // 2^-125 are their last eight bits times 2^-133, so that two nibbles in eight need no
 // shift.
 constexpr float kInt4Factor = 128.f;
@@ -130,7 +131,9 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// int8 x is held times 2^-7: a byte in a bf16's last bits is v 2^-133 (as in widen).
+// int8 x is held times 2^-7: a byte in a bf16's last bits is v 2^-133 (as in widen).  No
+// bits are lost for it: a group's sum is a multiple of 2^-14 (e2m1: 2^-8), times a bf16
+// scale's last bit one of 2^-147, which fp32 holds below its normal range too.
 constexpr float kInt8Factor = 128.f;
 
 __device__ __forceinline__ void sts64(uint32_t addr, uint32_t a, uint32_t b) {
