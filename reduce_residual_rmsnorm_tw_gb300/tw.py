@@ -498,7 +498,8 @@ class W4Weight:
             raise ValueError(f"scale must be [{n}, {-(-k // group)}]")
         held = scale.to(torch.bfloat16)
         # (A NaN stays one; bf16 infinities are numbers here, what rounds to one is not.)
-        if not torch.all((held.double() == scale.double()) | scale.isnan()):
+        exact = scale.double()
+        if not torch.all((held.double() == exact) | exact.isnan()):
             raise ValueError("scale must hold bf16 numbers")
         stripes, tiles = -(-n // 16), -(-k // 128)
         v = torch.zeros(stripes * 16, tiles * 128, dtype=torch.float32, device=values.device)

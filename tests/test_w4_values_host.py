@@ -47,6 +47,14 @@ def test_every_bf16_scale_is_taken(dtype):
                        s.double().nan_to_num(nan=7.0, posinf=1e300, neginf=-1e300))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.int32, torch.float8_e4m3fn,
+                                   torch.float8_e5m2])
+def test_scales_of_other_types(dtype):
+    s = torch.tensor([0.0, 1.0, 2.0, 4.0, 16.0, -8.0, 64.0, 128.0]).view(4, 2)
+    got = ref.unpack(tw.W4Weight.from_values(torch.ones(4, 64), s.to(dtype), 32, "int4"))[1]
+    assert np.array_equal(got, s.double().numpy())
+
+
 @pytest.mark.parametrize("dtype", [torch.int8, torch.int64, torch.float16, torch.float64])
 def test_values_of_any_type(dtype):
     v = torch.arange(-8, 8).repeat(8, 4).to(dtype)
