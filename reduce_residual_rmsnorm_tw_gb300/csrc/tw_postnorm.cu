@@ -318,12 +318,12 @@ void rows_shape(int64_t nvec, int* vpt, int* w) {
 }
 
 // Which kernel (us, 8 partials bf16: cluster / this file's rows / ring):
-//   rows from 8 KB   a cluster per token while all of them run at once (1 x 8192 2.7 / 4.6
+//   rows above 8 KB  a cluster per token while all of them run at once (1 x 8192 2.8 / 4.6
 //                    / 5.5, 100 x 8192 5.4 / 7.3 / 6.6, 128 x 8192 8.6 / - / 7.1)
 //   rows to 12 KB    this file's, a CTA or less per row, while all CTAs run at once: four
-//                    on an SM (500 x 4096 - / 8.7 / 10.4, 2 x 1000 x 2048 - / 4.8 / 6.1),
-//                    from 8 KB three (400 x 5120 - / 9.8 / 11.1; with 16 KB it would be two,
-//                    256 x 8192 - / 10.4 / 10.1); rows
+//                    on an SM (1 x 4096 - / 2.8 / -, 500 x 4096 - / 8.7 / 10.4, 2 x 1000 x
+//                    2048 - / 4.8 / 6.1), above 8 KB three (400 x 5120 - / 9.8 / 11.1; with
+//                    16 KB it would be two, 256 x 8192 - / 10.4 / 10.1); rows
 //                    below 4 KB always (1000 x 256 - / 2.5 / 7.5, 2 x 4096 x 1024 - / 9.0 / 10.7)
 //   everything else  the ring kernel's bulk copies (1024 x 8192 - / 38.3 / 28.9, 1000 x 4096 - /
 //                    18.4 / 15.8)

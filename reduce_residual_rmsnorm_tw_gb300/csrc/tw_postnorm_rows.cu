@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(block_of(kPipes), 1)
         mbar_init_fence();
     }
     __syncthreads();
-    // Pipeline g's tokens: t0 + block + (2 i + g) * grid.
+    // Pipeline g's tokens: t0 + block + (kPipes i + g) * grid.
     const int64_t first = p.t0 + blockIdx.x + static_cast<int64_t>(pipe) * gridDim.x;
     const int64_t step = static_cast<int64_t>(kPipes) * gridDim.x;
     // The first token's rows on their way into L2 while the launch before this one ends

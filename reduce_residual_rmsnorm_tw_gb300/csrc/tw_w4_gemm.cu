@@ -20,9 +20,9 @@
 // warps take pieces in turn and never wait for each other, but leave their sums where
 // the stripe's CTA of the cluster adds them up, in their order, when all are done.
 //
-// Measured: 1 x 8192 x 8192 int4 10.4 us, of which 4 are the launch, x and the join (a K
-// of 256 takes 4.0), the rest 5.4 TB/s; 8 x 8192 x 32768 31.7, 4.4 TB/s; 16 x 8192 x
-// 8192 14.9, 32 22.6, where the matrix instructions set the pace: one takes 6 to 8
+// Measured: 1 x 8192 x 8192 int4 10.5 us, of which 4 are the launch, x and the join (a K
+// of 256 takes 4.0), the rest 5.4 TB/s; 8 x 8192 x 32768 32.7, 4.3 TB/s; 16 x 8192 x
+// 8192 14.5, 32 22.5, where the matrix instructions set the pace: one takes 6 to 8
 // clocks of an SM's quarter, and four blocks of columns need four for each piece of W.
 #include <cuda_fp16.h>
 

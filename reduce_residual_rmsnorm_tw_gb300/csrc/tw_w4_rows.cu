@@ -6,8 +6,8 @@
 // of channel 2 i + l / 16 -- exactly one 32-bit word of the tile -- so a group's
 // maximum is a few shuffles and a channel's words are 64 contiguous bytes.
 // Bound by HBM: the rows in and half a byte per weight out, or the other way
-// round (8192 x 8192 bf16 to int4 27.6 us, 6.1 TB/s, to e2m1 30.9; back 25.7, 6.6 TB/s;
-// 4090 x 5120 fp32 to e2m1 with groups of 32 17.1 and 15.0).  Quantising takes some ten
+// round (8192 x 8192 bf16 to int4 27.2 us, 6.2 TB/s, to e2m1 30.7; back 25.6, 6.6 TB/s;
+// 4090 x 5120 fp32 to e2m1 with groups of 32 17.0 and 15.1).  Quantising takes some ten
 // instructions a weight, for which loads in flight have to cover.
 #include "tw_device.cuh"
 

@@ -94,9 +94,9 @@ def two_chunk_layer_step_q8(x, x_scale, w, w_scale, partials, residual, weight, 
 def w4_library_tokens(channels, inner):
     """From this many tokens on, reading 4-bit weights of [channels, inner] back and a
     library product of their bfloat16 form are faster than the product on 4 bits: 33 where
-    that form stays in the L2 cache (4096 x 4096: 32 tokens 9.6 us against 14.6, 40 tokens
-    15.1 against 12.3), 65 where it does not (8192 x 8192: 48 tokens 36.4 us against 44.8,
-    64 tokens 43.5 against 44.8, 96 tokens 64.5 against 50.3)."""
+    that form stays in the L2 cache (4096 x 4096: 32 tokens 9.8 us against 14.5, 40 tokens
+    15.6 against 12.3), 65 where it does not (8192 x 8192: 48 tokens 37.3 us against 43.9,
+    64 tokens 44.0 against 44.1, 96 tokens 65.5 against 49.7)."""
     return 33 if 2 * channels * inner < 1 << 27 else 65
 
 
@@ -114,8 +114,12 @@ def sandwich_layer_step_w4(x, w, partials, residual, weight, out, residual_out, 
 
     ``workspace``, a [H, K] bfloat16 tensor, is for many tokens: from w4_library_tokens(H, K)
     on a bfloat16 ``x`` (with bfloat16 partials) is multiplied by the weights read back
-    into it, a plain library GEMM.  What is refused does not depend on the number of
-    tokens."""
+    into it, a plain library GEMM (1024 x 8192 x 8192 0.10 ms against 0.69).  Reading back
+    rounds a weight's up to eleven bits to bfloat16's eight, which the product on 4 bits
+    does not: without a workspace results do not change at that number of tokens, and a
+    prompt takes the product's time, which reads the weights again for every 32 tokens.
+    8-bit and float32 ``x``, and float32 partials, always do (float32 ``x`` for every ten).
+    What is refused does not depend on the number of tokens."""
     stream = torch.cuda.current_stream() if stream is None else stream
     if workspace is not None and (workspace.shape != (w.n, w.k) or not workspace.is_contiguous()
                                   or workspace.dtype != torch.bfloat16
