@@ -369,7 +369,9 @@ int tw_quantize_w4(const void* w, void* packed, int64_t N, int64_t K, int group,
                    void* stream, int dtype, int wtype);
 
 /* The weights that packed form stands for, q * s rounded to dtype, as dense
- * [N, K] rows: for a library product of many tokens. */
+ * [N, K] rows: for a library product of many tokens.  (A scale that was rounded up may
+ * make q * s exceed dtype's largest number where a weight is within 2^-8 of it: then an
+ * infinity.) */
 int tw_dequantize_w4(const void* packed, void* w, int64_t N, int64_t K, int group, int max_sms,
                      void* stream, int dtype, int wtype);
 
